@@ -39,10 +39,16 @@ RLCA_EST_ELIG_TRACE = 6
 RLCA_EST_PREFIX_SUM = 7
 RLCA_EST_AFFINE_SCAN = 8
 RLCA_EST_VALUE_TARGETS = 9
+RLCA_EST_TOKEN_LOGPROB = 10
+RLCA_EST_TOKEN_LOGPROB_BACKWARD = 11
+RLCA_EST_LAYER_NORM_BACKWARD = 12
+RLCA_EST_CLIP_GRADS = 13
 
 RLCA_F32 = 0
 RLCA_I32 = 1
 RLCA_MAX_ACTIONS = 64
+RLCA_MAX_HEAD_DIM = 65536
+RLCA_MAX_HEAD_ROWS = 16777216
 RLCA_STATIC_SCRATCH_BYTES = 1 << 20
 RLCA_STATUS_WAIT_TIMEOUT = 0x1
 RLCA_STATUS_INDEX = 0x2
@@ -73,6 +79,12 @@ SIGNATURES = {
     "rlca_elig_trace": (_i, [_p, _p, _p, _p, _i64, _i64, _f, _f, _u32, _p, _sz, _p]),
     "rlca_episodic_prefix_sum": (_i, [_p, _i, _p, _p, _p, _i64, _i64, _u32, _p, _sz, _p]),
     "rlca_affine_scan": (_i, [_p, _p, _p, _p, _i64, _i64, _i, _u32, _p, _sz, _p]),
+    "rlca_layer_norm": (_i, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _f, _u32, _p]),
+    "rlca_layer_norm_backward": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _u32, _p, _sz, _p]),
+    "rlca_token_logprob": (_i, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _f, _u32, _p, _sz, _p]),
+    "rlca_token_logprob_backward": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _f, _u32,
+                                         _p, _sz, _p]),
+    "rlca_clip_grads": (_i, [_p, _p, _p, _p, _i64, _f, _f, _p, _p, _sz, _p]),
 }
 
 

@@ -2,11 +2,12 @@
 // argument validation on the host, launch planning, and launches on the
 // caller's stream.  Nothing here allocates memory or synchronises.
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
-#include <initializer_list>
 
+#include "host_checks.h"
 #include "internal.h"
+#include "policy.h"
+#include "policy_checks.h"
 #include "rlca.h"
 
 namespace rlca {
@@ -24,51 +25,6 @@ int next_pow2(int64_t x) {
   return p;
 }
 
-std::atomic<int> g_sm_count[256];
-
-cudaError_t sm_count_of_current_device(int* out) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 256) {
-    int c = g_sm_count[dev].load(std::memory_order_relaxed);
-    if (c > 0) {
-      *out = c;
-      return cudaSuccess;
-    }
-  }
-  int c = 0;
-  e = cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 256) g_sm_count[dev].store(c, std::memory_order_relaxed);
-  *out = c;
-  return cudaSuccess;
-}
-
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-
-bool overlap(const Span& a, const Span& b) {
-  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// every output against every input and every other output
-bool any_overlap(std::initializer_list<Span> ins, std::initializer_list<Span> outs) {
-  for (const Span& o : outs) {
-    for (const Span& i : ins)
-      if (overlap(o, i)) return true;
-    for (const Span& o2 : outs)
-      if (&o2 != &o && overlap(o, o2)) return true;
-  }
-  return false;
-}
-
-bool aligned(const void* p, uintptr_t a) { return p == nullptr || ((uintptr_t)p % a) == 0; }
-
 // sizes: negative / too large -> invalid; returns 1 when the call is decided
 // (invalid, or empty and therefore done)
 int check_sizes(int64_t E, int64_t T, int* status) {
@@ -82,8 +38,6 @@ int check_sizes(int64_t E, int64_t T, int* status) {
   }
   return 0;
 }
-
-bool flags_ok(uint32_t flags, uint32_t allowed) { return (flags & ~allowed) == 0u; }
 
 constexpr uint32_t kLayoutFlags = RLCA_TIME_MAJOR | RLCA_MULTIPASS | RLCA_INPUTS_READY;
 // flags of the calls whose float arrays may be bfloat16
@@ -478,7 +432,7 @@ int rlca_device_status(unsigned int* status, int clear) {
   const bool c = clear != 0;
   cudaError_t (*const units[])(unsigned int*, bool) = {status_values, status_values_bf16_a, status_values_bf16_b,
                                                        status_offpolicy, status_offpolicy_bf16, status_forward,
-                                                       status_forward_bf16};
+                                                       status_forward_bf16, status_norm, status_head, status_clip};
   for (auto f : units)
     if (f(status, c) != cudaSuccess) return RLCA_ERR_CUDA;
   return RLCA_OK;
@@ -487,6 +441,7 @@ int rlca_device_status(unsigned int* status, int clear) {
 int rlca_workspace_size(int estimator, int64_t E, int64_t T, int32_t num_actions, uint32_t flags, size_t* bytes) {
   if (bytes == nullptr) return RLCA_ERR_INVALID_ARG;
   *bytes = 0;
+  if (policy_estimator(estimator)) return policy_workspace_size(estimator, E, T, num_actions, flags, bytes);
   Kind kind;
   switch (estimator) {
     case RLCA_EST_GAE: kind = Kind::Gae; break;

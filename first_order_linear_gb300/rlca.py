@@ -27,6 +27,8 @@ from ._lib import check
 __all__ = [
     "rlca_gae", "rlca_value_targets", "rlca_discounted_return", "rlca_td_lambda", "rlca_vtrace", "rlca_retrace",
     "rlca_elig_trace", "rlca_episodic_prefix_sum", "rlca_affine_scan", "rlca_workspace_size",
+    "rlca_layer_norm", "rlca_layer_norm_backward", "rlca_token_logprob", "rlca_token_logprob_backward",
+    "rlca_clip_grads",
 ]
 
 
@@ -425,3 +427,188 @@ def rlca_affine_scan(alpha, beta, carry=None, *, reverse=True, out=None, time_ma
             _stream(dev, stream)))
         _hold(dev, stream, ws, out)
     return out
+
+
+# ---- the policy update around the scans ------------------------------------
+# Matrices here are 2-D with contiguous rows at any row stride (a slice of a
+# wider buffer works); everything else is contiguous as above.
+
+def _check_matrix(t, name, dtypes, shape, device):
+    """Checks a matrix input and returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape) if shape else '2 dimensions'}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)} below width {width})")
+    return t.stride(0)
+
+
+def _out(t, name, dtype, shape, device, want=True):
+    """An output buffer: the one given (checked), a new one, or None."""
+    if t is None and want:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, (dtype,), shape, device, required=False)
+    return t
+
+
+def rlca_layer_norm(x, weight, bias=None, *, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of ``x`` [N, D]: ``(y, mean, rstd)``, the
+    statistics float32 for :func:`rlca_layer_norm_backward`."""
+    lib = _lib.load()
+    fdt = _fdt(x, "x")
+    dev = x.device
+    stride = _check_matrix(x, "x", (fdt,), None, dev)
+    N, D = x.shape
+    _check(weight, "weight", (fdt,), (D,), dev)
+    _check(bias, "bias", (fdt,), (D,), dev, required=False)
+    y = _out(y, "y", fdt, (N, D), dev)
+    mean = _out(mean, "mean", torch.float32, (N,), dev)
+    rstd = _out(rstd, "rstd", torch.float32, (N,), dev)
+    _require_cuda(dev)
+    with torch.cuda.device(dev):
+        check("rlca_layer_norm", lib.rlca_layer_norm(
+            _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), N, D, stride, eps, _fflag(fdt),
+            _stream(dev, stream)))
+        _hold(dev, stream, y, mean, rstd)
+    return y, mean, rstd
+
+
+def rlca_layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbias=None, want_dx=True,
+                             want_dweight=True, want_dbias=True, workspace=None, stream=None):
+    """Gradient of :func:`rlca_layer_norm`: ``(dx, dweight, dbias)`` (None
+    for those not wanted; at least one is)."""
+    lib = _lib.load()
+    fdt = _fdt(x, "x")
+    dev = x.device
+    x_stride = _check_matrix(x, "x", (fdt,), None, dev)
+    N, D = x.shape
+    dy_stride = _check_matrix(dy, "dy", (fdt,), (N, D), dev)
+    _check(weight, "weight", (fdt,), (D,), dev)
+    _check(mean, "mean", _F, (N,), dev)
+    _check(rstd, "rstd", _F, (N,), dev)
+    dx = _out(dx, "dx", fdt, (N, D), dev, want_dx)
+    dweight = _out(dweight, "dweight", fdt, (D,), dev, want_dweight)
+    dbias = _out(dbias, "dbias", fdt, (D,), dev, want_dbias)
+    if dx is None and dweight is None and dbias is None:
+        raise ValueError("no output wanted")
+    _require_cuda(dev)
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_LAYER_NORM_BACKWARD, N, D, 0, _fflag(fdt), dev, workspace)
+        check("rlca_layer_norm_backward", lib.rlca_layer_norm_backward(
+            _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), N, D,
+            dy_stride, x_stride, _fflag(fdt), _ptr(ws), wsb, _stream(dev, stream)))
+        _hold(dev, stream, ws, dx, dweight, dbias)
+    return dx, dweight, dbias
+
+
+def _check_head(hidden, weight, tokens, temperature):
+    fdt = _fdt(hidden, "hidden")
+    dev = hidden.device
+    hidden_stride = _check_matrix(hidden, "hidden", (fdt,), None, dev)
+    N, D = hidden.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a 2-D tensor [V, D]")
+    weight_stride = _check_matrix(weight, "weight", (fdt,), (weight.shape[0], D), dev)
+    _check(tokens, "tokens", _I32, (N,), dev)
+    if not temperature > 0.0:
+        raise ValueError(f"temperature {temperature} must be positive")
+    return fdt, dev, N, D, weight.shape[0], hidden_stride, weight_stride
+
+
+def rlca_token_logprob(hidden, weight, tokens, *, temperature=1.0, logp=None, lse=None, entropy=None,
+                       want_entropy=True, workspace=None, stream=None):
+    """Log-probabilities of ``tokens`` [N] (int32) under the policy
+    softmax(hidden [N, D] weight [V, D]^T / temperature), without storing
+    the logits: ``(logp, lse, entropy)``, float32, entropy None when not
+    wanted.  -logp is the cross entropy.  A row whose token lies outside
+    [0, V) takes no part: its results are 0."""
+    lib = _lib.load()
+    fdt, dev, N, D, V, hs, wst = _check_head(hidden, weight, tokens, temperature)
+    logp = _out(logp, "logp", torch.float32, (N,), dev)
+    lse = _out(lse, "lse", torch.float32, (N,), dev)
+    entropy = _out(entropy, "entropy", torch.float32, (N,), dev, want_entropy)
+    _require_cuda(dev)
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_TOKEN_LOGPROB, N, D, V, _fflag(fdt), dev, workspace)
+        check("rlca_token_logprob", lib.rlca_token_logprob(
+            _ptr(hidden), _ptr(weight), _ptr(tokens), _ptr(logp), _ptr(lse), _ptr(entropy), N, D, V, hs, wst,
+            1.0 / temperature, _fflag(fdt), _ptr(ws), wsb, _stream(dev, stream)))
+        _hold(dev, stream, ws, logp, lse, entropy)
+    return logp, lse, entropy
+
+
+def rlca_token_logprob_backward(hidden, weight, tokens, lse, d_logp, *, entropy=None, d_entropy=None,
+                                temperature=1.0, d_hidden=None, d_weight=None, want_d_hidden=True,
+                                want_d_weight=True, workspace=None, stream=None):
+    """Gradient of :func:`rlca_token_logprob` for the factors ``d_logp`` [N]
+    and, with the saved ``entropy``, ``d_entropy`` [N] (float32):
+    ``(d_hidden, d_weight)``, None for one not wanted (at least one is)."""
+    lib = _lib.load()
+    fdt, dev, N, D, V, hs, wst = _check_head(hidden, weight, tokens, temperature)
+    for name, t, required in (("lse", lse, True), ("d_logp", d_logp, True), ("entropy", entropy, False),
+                              ("d_entropy", d_entropy, False)):
+        _check(t, name, _F, (N,), dev, required=required)
+    if (entropy is None) != (d_entropy is None):
+        raise ValueError("entropy and d_entropy come together")
+    d_hidden = _out(d_hidden, "d_hidden", fdt, (N, D), dev, want_d_hidden)
+    d_weight = _out(d_weight, "d_weight", fdt, (V, D), dev, want_d_weight)
+    if d_hidden is None and d_weight is None:
+        raise ValueError("no output wanted")
+    _require_cuda(dev)
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_TOKEN_LOGPROB_BACKWARD, N, D, V, _fflag(fdt), dev, workspace)
+        check("rlca_token_logprob_backward", lib.rlca_token_logprob_backward(
+            _ptr(hidden), _ptr(weight), _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(d_logp), _ptr(d_entropy),
+            _ptr(d_hidden), _ptr(d_weight), N, D, V, hs, wst, 1.0 / temperature, _fflag(fdt), _ptr(ws), wsb,
+            _stream(dev, stream)))
+        _hold(dev, stream, ws, d_hidden, d_weight)
+    return d_hidden, d_weight
+
+
+def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, norm=None, workspace=None, stream=None):
+    """Global norm of the gradient tensors ``grads`` (each float32 or
+    bfloat16, any shape) and the tensors times min(1, max_norm / (norm +
+    eps)) -- unscaled when the norm is not finite: ``(clipped, norm)``, norm
+    a float32 scalar tensor.  ``out`` takes the results: a list of matching
+    tensors, or ``grads`` itself to scale in place.  ``norm_only`` leaves the
+    tensors alone and returns ``(None, norm)``."""
+    lib = _lib.load()
+    grads = list(grads)
+    if norm is None and not grads:
+        raise ValueError("no gradients and no norm buffer: the device is unknown")
+    dev = grads[0].device if grads else norm.device
+    n = len(grads)
+    if norm_only:
+        out = None
+    elif out is None:
+        out = [torch.empty_like(g, memory_format=torch.contiguous_format) for g in grads]
+    else:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError(f"out has {len(out)} tensors, expected {n}")
+    for k, g in enumerate(grads):
+        _check(g, f"grads[{k}]", (_fdt(g, f"grads[{k}]"),), g.shape, dev)
+        if out is not None and out[k] is not g:
+            _check(out[k], f"out[{k}]", (g.dtype,), g.shape, dev)
+    norm = _out(norm, "norm", torch.float32, (), dev)
+    _require_cuda(dev)
+    gp = (C.c_void_p * n)(*[g.data_ptr() for g in grads])
+    op = None if out is None else (C.c_void_p * n)(*[o.data_ptr() for o in out])
+    sizes = (C.c_int64 * n)(*[g.numel() for g in grads])
+    dtypes = (C.c_uint32 * n)(*[_fflag(g.dtype) for g in grads])
+    with torch.cuda.device(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_CLIP_GRADS, n, 1, 0, 0, dev, workspace)
+        check("rlca_clip_grads", lib.rlca_clip_grads(gp, op, sizes, dtypes, n, max_norm, eps, _ptr(norm), _ptr(ws), wsb,
+                                                     _stream(dev, stream)))
+        _hold(dev, stream, ws, norm, *(out or ()))
+    return out, norm

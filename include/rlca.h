@@ -127,6 +127,12 @@ typedef struct CUstream_st *rlca_stream_t;
 #define RLCA_EST_PREFIX_SUM        7
 #define RLCA_EST_AFFINE_SCAN       8
 #define RLCA_EST_VALUE_TARGETS     9
+/* the policy-update operators: E = rows, T = row width, num_actions = vocabulary
+ * (RLCA_EST_CLIP_GRADS: E = number of tensors, T ignored unless 0) */
+#define RLCA_EST_TOKEN_LOGPROB          10
+#define RLCA_EST_TOKEN_LOGPROB_BACKWARD 11
+#define RLCA_EST_LAYER_NORM_BACKWARD    12
+#define RLCA_EST_CLIP_GRADS             13
 
 /* ---- prefix-sum element types ------------------------------------------- */
 #define RLCA_F32 0
@@ -397,6 +403,148 @@ int rlca_affine_scan(const float *alpha, const float *beta,
                      const float *carry, float *out, int64_t E, int64_t T,
                      int reverse, uint32_t flags, void *workspace,
                      size_t workspace_bytes, rlca_stream_t stream);
+
+/* ---- the policy update around the scans ----------------------------------
+ *
+ * A policy over a vocabulary of tokens trains on the scans' advantages.  The
+ * entry points below are the operators of such an update that stand next to
+ * the scans: the final layer norm, the head's log-probabilities and entropy
+ * (V-Trace's logp_target), the gradients of both, and the clipping of all
+ * gradients by their global norm.  No counterpart in the paper.
+ *
+ * Conventions: as above (device pointers, caller's stream, no allocation, no
+ * synchronisation, host-side argument errors), and
+ *  - matrices are row-major; an input matrix has a row stride in elements (at
+ *    least its width), outputs are dense;
+ *  - with RLCA_BF16 the arrays documented as "x" hold bfloat16; statistics,
+ *    log-probabilities and per-row factors are float32 always.  Arithmetic is
+ *    float32 or better, and an output is rounded once;
+ *  - RLCA_BF16 is the only flag;
+ *  - results do not depend on scheduling: no floating-point atomics.
+ */
+
+/*
+ * Layer norm of N rows of width D:
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps)
+ * with the biased variance over the row (computed from the centred row).
+ *   x                      [N,D] x, row stride x_stride, required
+ *   weight                 [D] x, required
+ *   bias                   [D] x, NULL = 0
+ *   y                      [N,D] x output, required
+ *   mean, rstd             [N] f32 outputs, NULL = not written
+ * N == 0 or D == 0 returns RLCA_OK and enqueues nothing.  Errors:
+ * RLCA_ERR_INVALID_ARG also for x_stride < D and eps not in [0, inf).
+ */
+int rlca_layer_norm(const float *x, const float *weight, const float *bias,
+                    float *y, float *mean, float *rstd, int64_t N, int64_t D,
+                    int64_t x_stride, float eps, uint32_t flags,
+                    rlca_stream_t stream);
+
+/*
+ * Gradient of rlca_layer_norm from its saved statistics.  With
+ * g = dy * weight and xh = (x - mean) * rstd:
+ *   dx = rstd * (g - mean_D(g) - xh * mean_D(g * xh))
+ *   dweight = sum_N dy * xh,  dbias = sum_N dy
+ *   dy                     [N,D] x, row stride dy_stride, required
+ *   x                      [N,D] x, row stride x_stride, required
+ *   weight                 [D] x, required
+ *   mean, rstd             [N] f32, required
+ *   dx                     [N,D] x output, NULL = not written
+ *   dweight, dbias         [D] x outputs, NULL = not written
+ * Workspace: RLCA_EST_LAYER_NORM_BACKWARD.  N == 0 writes zeros to dweight
+ * and dbias; D == 0 enqueues nothing.
+ */
+int rlca_layer_norm_backward(const float *dy, const float *x,
+                             const float *weight, const float *mean,
+                             const float *rstd, float *dx, float *dweight,
+                             float *dbias, int64_t N, int64_t D,
+                             int64_t dy_stride, int64_t x_stride,
+                             uint32_t flags, void *workspace,
+                             size_t workspace_bytes, rlca_stream_t stream);
+
+/*
+ * Log-probabilities of taken tokens and entropies of a policy head, straight
+ * from its input rows; the N x V logits are never stored:
+ *   z_ij   = inv_temperature * <hidden_i, weight_j>
+ *   lse_i  = log sum_j exp(z_ij)
+ *   logp_i = z_i,tokens[i] - lse_i     (the cross entropy is -logp)
+ *   ent_i  = lse_i - sum_j softmax(z_i)_j z_ij
+ * A row whose token is outside [0, V) takes no part: its three results are
+ * 0 and its hidden row is not used.
+ *   hidden                 [N,D] x, row stride hidden_stride, required
+ *   weight                 [V,D] x, row stride weight_stride, required
+ *   tokens                 [N] i32, required
+ *   logp, lse              [N] f32 outputs, required
+ *   entropy                [N] f32 output, NULL = not written
+ * Workspace: RLCA_EST_TOKEN_LOGPROB.  N == 0 enqueues nothing.  Errors:
+ * RLCA_ERR_INVALID_ARG also for D < 1, V < 1, a row stride below D,
+ * inv_temperature not finite; RLCA_ERR_UNSUPPORTED for D above
+ * RLCA_MAX_HEAD_DIM, N or V above RLCA_MAX_HEAD_ROWS.
+ */
+#define RLCA_MAX_HEAD_DIM  65536
+#define RLCA_MAX_HEAD_ROWS 16777216
+int rlca_token_logprob(const float *hidden, const float *weight,
+                       const int32_t *tokens, float *logp, float *lse,
+                       float *entropy, int64_t N, int64_t D, int64_t V,
+                       int64_t hidden_stride, int64_t weight_stride,
+                       float inv_temperature, uint32_t flags, void *workspace,
+                       size_t workspace_bytes, rlca_stream_t stream);
+
+/*
+ * Gradient of rlca_token_logprob, for factors g = d_logp and e = d_entropy
+ * and the saved lse and entropy; the logits are recomputed in pieces of the
+ * vocabulary:
+ *   dz_ij    = inv_temperature * (g_i ([j = tokens[i]] - p_ij)
+ *                                 - e_i p_ij (z_ij - lse_i + ent_i))
+ *   d_hidden = dz weight,   d_weight = dz^T hidden
+ * A row that takes no part has gradient 0 and adds nothing to d_weight,
+ * whatever its inputs hold.
+ *   hidden, weight, tokens as above, required
+ *   lse                    [N] f32, required
+ *   entropy, d_entropy     [N] f32, both or neither NULL (NULL = e is 0)
+ *   d_logp                 [N] f32, required
+ *   d_hidden               [N,D] x output, NULL = not written
+ *   d_weight               [V,D] x output, NULL = not written
+ * Workspace: RLCA_EST_TOKEN_LOGPROB_BACKWARD.  N == 0 writes zeros to
+ * d_weight.  Errors as for rlca_token_logprob.
+ */
+int rlca_token_logprob_backward(const float *hidden, const float *weight,
+                                const int32_t *tokens, const float *lse,
+                                const float *entropy, const float *d_logp,
+                                const float *d_entropy, float *d_hidden,
+                                float *d_weight, int64_t N, int64_t D,
+                                int64_t V, int64_t hidden_stride,
+                                int64_t weight_stride, float inv_temperature,
+                                uint32_t flags, void *workspace,
+                                size_t workspace_bytes, rlca_stream_t stream);
+
+/*
+ * Global norm of `count` gradient tensors, and the tensors scaled by it:
+ *   norm  = sqrt(sum over all elements of g^2)
+ *   scale = min(1, max_norm / (norm + eps)), or 1 when norm is not finite
+ *   out_k = scale * grad_k
+ * so a step whose norm overflowed or met a NaN is left for the caller to
+ * judge by the norm.  Squares are summed in float32 over short runs and in
+ * float64 beyond, in a fixed order.
+ *   grads                  host array of count device pointers
+ *   outs                   host array of count device pointers; NULL = only
+ *                          the norm.  outs[k] == grads[k] scales in place; any
+ *                          other overlap is an error where it is within one
+ *                          pair, and the caller's to avoid across pairs
+ *   sizes                  host array of element counts (0 allowed; the
+ *                          pointers are then not read)
+ *   dtypes                 host array: 0 (float32) or RLCA_BF16, of both
+ *                          grads[k] and outs[k]
+ *   max_norm               >= 0 (infinity: scale 1)
+ *   norm                   [1] f32 output, required
+ * The host arrays are read before the call returns.  Workspace:
+ * RLCA_EST_CLIP_GRADS.  count == 0 writes 0 to norm.
+ */
+int rlca_clip_grads(const void *const *grads, void *const *outs,
+                    const int64_t *sizes, const uint32_t *dtypes,
+                    int64_t count, float max_norm, float eps, float *norm,
+                    void *workspace, size_t workspace_bytes,
+                    rlca_stream_t stream);
 
 #ifdef __cplusplus
 }
