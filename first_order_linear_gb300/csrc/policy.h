@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>  // CUtensorMap
 #include <cuda_runtime.h>
 
 namespace rlca {
@@ -85,5 +86,12 @@ cudaError_t status_head(unsigned int* word, bool clear);
 cudaError_t status_clip(unsigned int* word, bool clear);
 
 int checked_build_status(cudaStream_t s);
+
+// Map of `planes` bfloat16 matrices [rows, width] (strides in elements, both
+// multiples of 8; base 16-byte aligned) for copies of 64 x box_rows boxes in
+// the 128-byte swizzle; what lies outside reads as zero.  False when the
+// encoder is unavailable or refuses.
+bool encode_matrix_map(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t planes,
+                       int64_t row_stride, int64_t plane_stride, int box_rows);
 
 }  // namespace rlca

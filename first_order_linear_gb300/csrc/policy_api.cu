@@ -37,6 +37,8 @@ int head_sizes(int64_t N, int64_t D, int64_t V) {
   return RLCA_OK;
 }
 
+bool temperature_ok(float inv) { return inv > 0.f && std::isfinite(inv); }
+
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws != nullptr && have >= need && aligned(ws, 16));
 }
@@ -123,7 +125,7 @@ int rlca_token_logprob(const float* hidden, const float* weight, const int32_t* 
                        rlca_stream_t stream) {
   const int st = head_sizes(N, D, V);
   if (st != RLCA_OK) return st;
-  if (!flags_ok(flags, RLCA_BF16) || !std::isfinite(inv_temperature)) return RLCA_ERR_INVALID_ARG;
+  if (!flags_ok(flags, RLCA_BF16) || !temperature_ok(inv_temperature)) return RLCA_ERR_INVALID_ARG;
   if (N == 0) return RLCA_OK;
   if (!hidden || !weight || !tokens || !logp || !lse || !stride_ok(hidden_stride, D) || !stride_ok(weight_stride, D))
     return RLCA_ERR_INVALID_ARG;
@@ -150,7 +152,7 @@ int rlca_token_logprob_backward(const float* hidden, const float* weight, const 
                                 size_t workspace_bytes, rlca_stream_t stream) {
   const int st = head_sizes(N, D, V);
   if (st != RLCA_OK) return st;
-  if (!flags_ok(flags, RLCA_BF16) || !std::isfinite(inv_temperature)) return RLCA_ERR_INVALID_ARG;
+  if (!flags_ok(flags, RLCA_BF16) || !temperature_ok(inv_temperature)) return RLCA_ERR_INVALID_ARG;
   if (!d_hidden && !d_weight) return RLCA_ERR_INVALID_ARG;
   const size_t es = ebytes(flags), n = (size_t)N * 4;
   if (N == 0) {

@@ -1,0 +1,347 @@
+// tc.cuh -- a persistent matrix product on the 5th-generation tensor cores:
+// TMA-fed shared-memory ring, tcgen05.mma into TMEM, and an epilogue functor
+// that gets the float32 accumulator 32 columns at a time.
+//
+//   C(m, n) = sum over terms (pa, pb), sum over k of A[pa](m, k) * B[pb](n, k)
+//
+// A and B are bfloat16 with float32 accumulation.  float32 operands come as
+// three bfloat16 planes whose sum is the value to 24 bits (hi, mid, lo, each
+// the rounding of what the ones before left over); the six products of planes
+// down to 2^-16 of the first are then the `terms`, smallest first so that the
+// accumulator's rounding acts on small values while it is small.
+//
+// Either operand may be K-major (k contiguous in memory) or MN-major (m or n
+// contiguous): the shared-memory descriptors and the instruction descriptor
+// say which, so no operand is ever transposed in memory.
+//
+// One CTA an SM: warps 0-7 run the epilogue (warp w reads TMEM lanes
+// 32 (w % 4) .. + 31 and the tile's column half w / 4), warp 8 issues the
+// copies, warp 9 the matrix instructions.  The accumulator is double-buffered
+// in TMEM (2 x 256 columns), so the epilogue of one tile runs under the
+// product of the next.  Every wait is bounded: a wait that gives up records
+// the timeout in the status word and raises a shared flag that ends all
+// roles; the copies in flight are then waited for (bounded) before TMEM is
+// freed.
+#pragma once
+
+#include "tma.cuh"
+
+namespace rlca {
+
+constexpr int kTcM = 128;      // rows of a CTA's tile
+constexpr int kTcN = 256;      // columns of a tile
+constexpr int kTcK = 64;       // k per stage: one 128-byte swizzle row of bfloat16
+constexpr int kTcStages = 4;
+constexpr int kTcEpiWarps = 8;
+constexpr int kTcThreads = 32 * (kTcEpiWarps + 2);
+constexpr int kTcABytes = kTcM * kTcK * 2;
+constexpr int kTcBBytes = kTcN * kTcK * 2;
+constexpr int kTcStageBytes = kTcABytes + kTcBBytes;
+constexpr size_t kTcSmem = (size_t)kTcStages * kTcStageBytes + 1024;  // + alignment of the ring
+
+// the plane pairs of one product, four bits each for A's and B's plane
+struct TcTerms {
+  int n;
+  unsigned char a[6], b[6];
+};
+
+struct TcShape {
+  // extents; the one named by `count_axis` is *count, known on the device only
+  const int* count;
+  int count_axis;  // 0: none, 1: m, 2: k
+  int m, n, k;
+  // added to the tensor maps' coordinates: A's m, B's n, B's k
+  int a_m0, b_n0, b_k0;
+  int splits;      // the k axis in this many parts (each its own output)
+  int band;        // row tiles walked together before the next column tile
+  TcTerms terms;
+};
+
+// ---- tcgen05 ------------------------------------------------------------------
+__device__ __forceinline__ void tc_alloc(uint32_t* smem_dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// arrives on `bar` once every matrix instruction issued so far has completed
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// 32 columns of this warp's 32 TMEM lanes: one row a thread
+__device__ __forceinline__ void tc_load32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory matrix descriptor of a 128-byte-swizzled tile at `addr`
+// (1024-byte aligned but for the k offset inside a swizzle row).  K-major:
+// rows of 128 bytes, groups of 8 rows 1024 bytes apart.  MN-major: blocks of
+// 64 values of m (or n) x kTcK values of k, a block's 8-k groups 1024 bytes
+// apart, blocks kTcK * 128 bytes apart.
+template <bool MN>
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+  const uint64_t lead = MN ? (kTcK * 128) >> 4 : 1, stride = 1024 >> 4;
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (lead << 16) | (stride << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// ... advanced by 16 values of k
+template <bool MN>
+constexpr uint64_t kTcStepK = MN ? (2 * 1024) >> 4 : 32 >> 4;
+
+// bfloat16 x bfloat16 -> float32, M = 128, N = 256
+template <bool A_MN, bool B_MN>
+constexpr uint32_t kTcInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
+                              ((uint32_t)(kTcN >> 3) << 17) | ((uint32_t)(kTcM >> 4) << 24);
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// a bounded wait that also ends when another role has given up
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*stop) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      atomicOr(&g_tu_status, kStatusWaitTimeout);
+      *stop = 1;
+      return false;
+    }
+  }
+}
+
+// ---- tiles ------------------------------------------------------------------------
+struct TcTile {
+  int m0, n0, split, k_begin, k_end;  // k in stages
+};
+
+struct TcWalk {
+  int m, k, mt, nt, k_stages, per_split;
+  int64_t tiles;
+  __device__ TcWalk(const TcShape& s) {
+    const int count = s.count_axis ? *s.count : 0;
+    m = s.count_axis == 1 ? min(count, s.m) : s.m;
+    k = s.count_axis == 2 ? min(count, s.k) : s.k;
+    mt = (m + kTcM - 1) / kTcM;
+    nt = (s.n + kTcN - 1) / kTcN;
+    k_stages = (k + kTcK - 1) / kTcK;
+    per_split = (k_stages + s.splits - 1) / s.splits;
+    tiles = (int64_t)mt * nt * s.splits;
+  }
+  // bands of row tiles; inside a band the row tile runs fastest, so CTAs that
+  // run together share the band's rows of A and a few column tiles of B
+  __device__ TcTile at(int64_t t, const TcShape& s) const {
+    const int64_t plane = (int64_t)mt * nt;
+    TcTile r;
+    r.split = (int)(t / plane);
+    t -= r.split * plane;
+    const int64_t per_band = (int64_t)s.band * nt;
+    const int band = (int)(t / per_band);
+    t -= band * per_band;
+    const int rows = min(s.band, mt - band * s.band);
+    r.n0 = (int)(t / rows) * kTcN;
+    r.m0 = (band * s.band + (int)(t % rows)) * kTcM;
+    r.k_begin = min(k_stages, r.split * per_split);
+    r.k_end = min(k_stages, r.k_begin + per_split);
+    return r;
+  }
+};
+
+// Epi: struct State; begin(State&, tile, row, half) with row = the thread's
+// row of C and half = first column of its half tile; chunk(State&, col, v[32])
+// for the 32 columns from col on; end(State&).  m extent in walk.m.
+template <bool A_MN, bool B_MN, class Epi>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tc_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                      const __grid_constant__ TcShape s, const __grid_constant__ Epi epi) {
+  extern __shared__ unsigned char tc_smem_raw[];
+  __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int stop;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)tc_smem_raw + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_trigger();
+  if (warp == kTcEpiWarps + 1) tc_alloc(&tmem_base, 2 * kTcN);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kTcEpiWarps);
+    }
+    mbar_init(&drained, 1);
+    stop = 0;
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  const TcWalk walk(s);
+
+  if (warp == kTcEpiWarps) {
+    // ---- copies ----
+    if (lane == 0) {
+      // operands written by earlier kernels' ordinary stores, read by copies
+      asm volatile("fence.proxy.async;" ::: "memory");
+      tma_prefetch_map(&map_a);
+      tma_prefetch_map(&map_b);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < walk.tiles && ok; t += gridDim.x) {
+        const TcTile tile = walk.at(t, s);
+        for (int term = 0; term < s.terms.n && ok; ++term) {
+          const int pa = s.terms.a[term], pb = s.terms.b[term];
+          for (int ks = tile.k_begin; ks < tile.k_end; ++ks) {
+            if (!tc_wait(&empty[stage], phase ^ 1, &stop)) {
+              ok = false;
+              break;
+            }
+            unsigned char* sa = ring + stage * kTcStageBytes;
+            unsigned char* sb = sa + kTcABytes;
+            mbar_arrive_expect_tx(&full[stage], kTcStageBytes);
+            const int k0 = ks * kTcK;
+            if constexpr (A_MN) {
+#pragma unroll
+              for (int i = 0; i < kTcM / 64; ++i)
+                tma_load_3d(sa + i * kTcK * 128, &map_a, s.a_m0 + tile.m0 + 64 * i, k0, pa, &full[stage]);
+            } else {
+              tma_load_3d(sa, &map_a, k0, s.a_m0 + tile.m0, pa, &full[stage]);
+            }
+            if constexpr (B_MN) {
+#pragma unroll
+              for (int i = 0; i < kTcN / 64; ++i)
+                tma_load_3d(sb + i * kTcK * 128, &map_b, s.b_n0 + tile.n0 + 64 * i, s.b_k0 + k0, pb, &full[stage]);
+            } else {
+              tma_load_3d(sb, &map_b, s.b_k0 + k0, s.b_n0 + tile.n0, pb, &full[stage]);
+            }
+            if (++stage == kTcStages) stage = 0, phase ^= 1;
+          }
+        }
+      }
+      // Every copy that was issued lands before the CTA ends (when all went
+      // well the matrix instructions have waited for it too).  Stage i was
+      // last filled in `phase` if i < stage, else in the phase before, or
+      // never: that wait returns at once.
+      for (int i = 0; i < kTcStages; ++i) mbar_wait_bounded(&full[i], i < stage ? phase : phase ^ 1);
+    }
+  } else if (warp == kTcEpiWarps + 1) {
+    // ---- matrix instructions ----
+    if (lane == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < walk.tiles && ok; t += gridDim.x) {
+        const TcTile tile = walk.at(t, s);
+        const int steps = (tile.k_end - tile.k_begin) * s.terms.n;
+        if (steps == 0) continue;  // the epilogue takes zeros and waits for nothing
+        if (!tc_wait(&acc_empty[buf], acc_phase ^ 1, &stop)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kTcN;
+        for (int it = 0; it < steps; ++it) {
+          if (!tc_wait(&full[stage], phase, &stop)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(ring + stage * kTcStageBytes);
+          const uint64_t da = tc_desc<A_MN>(sa), db = tc_desc<B_MN>(sa + kTcABytes);
+#pragma unroll
+          for (int k = 0; k < kTcK / 16; ++k)
+            tc_mma(d, da + k * kTcStepK<A_MN>, db + k * kTcStepK<B_MN>, kTcInstr<A_MN, B_MN>, it > 0 || k > 0);
+          tc_commit(&empty[stage]);
+          if (++stage == kTcStages) stage = 0, phase ^= 1;
+        }
+        if (!ok) break;
+        tc_commit(&acc_full[buf]);
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1;
+      }
+      // whatever was issued completes before TMEM is freed
+      tc_commit(&drained);
+      mbar_wait_bounded(&drained, 0);
+    }
+  } else {
+    // ---- epilogue ----
+    const int quarter = warp & 3, half = warp >> 2;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    for (int64_t t = blockIdx.x; t < walk.tiles; t += gridDim.x) {
+      const TcTile tile = walk.at(t, s);
+      const bool zero = (tile.k_end - tile.k_begin) * s.terms.n == 0;
+      typename Epi::State st;
+      epi.begin(st, walk, tile, tile.m0 + quarter * 32 + lane, tile.n0 + half * (kTcN / 2));
+      if (!zero) {
+        // (one verdict for the warp: the TMEM loads need all its lanes)
+        if (!__all_sync(0xffffffffu, tc_wait(&acc_full[buf], acc_phase, &stop))) break;
+        tc_fence_after();
+      }
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTcN + half * (kTcN / 2);
+#pragma unroll 1
+      for (int c = 0; c < kTcN / 2; c += 32) {
+        float v[32];
+        if (zero) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        } else {
+          tc_load32(src + c, v);
+        }
+        epi.chunk(st, tile.n0 + half * (kTcN / 2) + c, v);
+      }
+      if (!zero) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1;
+      }
+      epi.end(st);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kTcEpiWarps + 1) tc_free(tmem, 2 * kTcN);
+}
+
+}  // namespace rlca

@@ -478,7 +478,7 @@ int rlca_layer_norm_backward(const float *dy, const float *x,
  *   entropy                [N] f32 output, NULL = not written
  * Workspace: RLCA_EST_TOKEN_LOGPROB.  N == 0 enqueues nothing.  Errors:
  * RLCA_ERR_INVALID_ARG also for D < 1, V < 1, a row stride below D,
- * inv_temperature not finite; RLCA_ERR_UNSUPPORTED for D above
+ * inv_temperature not positive and finite; RLCA_ERR_UNSUPPORTED for D above
  * RLCA_MAX_HEAD_DIM, N or V above RLCA_MAX_HEAD_ROWS.
  */
 #define RLCA_MAX_HEAD_DIM  65536

@@ -126,7 +126,8 @@ def test_token_logprob_refusals(lib):
     assert _head(lib, N=0, h=None) == OK
     assert _head_grad(lib, N=0, h=None, dw=None) == OK
     common = [dict(N=-1), dict(D=0), dict(V=0), dict(h=None), dict(w=None), dict(tok=None), dict(lse=None),
-              dict(hs=7), dict(wst=7), dict(it=math.nan), dict(it=math.inf), dict(flags=0x10)]
+              dict(hs=7), dict(wst=7), dict(it=math.nan), dict(it=math.inf), dict(it=0.0),
+              dict(it=-1.0), dict(flags=0x10)]
     for bad in common + [dict(logp=None), dict(logp=P[0]), dict(lse=P[3]), dict(ent=P[2])]:
         assert _head(lib, **bad) == INV, bad
     for bad in common + [dict(g=None), dict(ent=None), dict(e=None), dict(dh=None, dw=None), dict(dh=P[0]),
