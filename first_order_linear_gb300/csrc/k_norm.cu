@@ -1,4 +1,19 @@
 // Layer norm and its gradient.
+//
+//   y = (x - mean) rstd w + b
+//   dx = rstd (g - mean(g) - xh mean(g xh)),  g = dy w,  xh = (x - mean) rstd
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Both directions are bound by HBM: the forward pass reads and writes a row
+// once, the backward pass reads two rows and writes one.  A row is held in
+// registers (VPT vectors of 16 bytes a thread, TPR threads a row), so the
+// variance is the mean square of the centred row at no second read --
+// sum(x^2) - mean^2 would cancel for rows whose mean is large against their
+// spread.  CTAs are persistent: a thread keeps its columns' weight and bias
+// (and, backward, its columns' sums of dw and db) in registers over all its
+// rows, and loads the next row before it works on the current one.
+#include <algorithm>
+
 #include "policy.h"
 #include "reduce.cuh"
 
@@ -6,13 +21,150 @@ namespace rlca {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+// VE consecutive elements of type ST as they lie in memory
+template <class ST, int VE>
+struct Pack;
+template <>
+struct Pack<float, 4> {
+  using Raw = float4;
+  __device__ static Raw load(const float* p, int64_t i) { return __ldg(reinterpret_cast<const float4*>(p + i)); }
+  __device__ static Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ static void open(const Raw& r, float* v) { v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w; }
+  __device__ static void store(float* p, int64_t i, const float* v) { Stor<float>::st4(p, i, v); }
+};
+template <>
+struct Pack<bf16, 8> {
+  using Raw = uint4;
+  __device__ static Raw load(const float* p, int64_t i) {
+    return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i));
+  }
+  __device__ static Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
+  __device__ static void open(const Raw& r, float* v) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+  __device__ static void store(float* p, int64_t i, const float* v) { Stor<bf16>::st8(p, i, v); }
+};
+template <>
+struct Pack<float, 1> {
+  using Raw = float;
+  __device__ static Raw load(const float* p, int64_t i) { return __ldg(p + i); }
+  __device__ static Raw zero() { return 0.f; }
+  __device__ static void open(const Raw& r, float* v) { v[0] = r; }
+  __device__ static void store(float* p, int64_t i, const float* v) { p[i] = v[0]; }
+};
+template <>
+struct Pack<bf16, 1> {
+  using Raw = uint16_t;  // widened when used: a conversion at the load would wait for it
+  __device__ static Raw load(const float* p, int64_t i) { return __ldg(reinterpret_cast<const uint16_t*>(p) + i); }
+  __device__ static Raw zero() { return 0; }
+  __device__ static void open(const Raw& r, float* v) { v[0] = Stor<bf16>::from_bits(r); }
+  __device__ static void store(float* p, int64_t i, const float* v) { Stor<bf16>::st(p, i, v[0]); }
+};
 
-// y = (x - mean) * rstd * w + b.  The variance is the mean square of the
-// centred row (two passes over the row): sum(x^2) - mean^2 would cancel for
-// rows whose mean is large against their spread.
+// Threads of a CTA: whole warps of rows, or one row over the CTA.
+__host__ __device__ constexpr int cta_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
+
+// CTAs of `threads` threads an SM is to hold in the forward pass, by the
+// values a thread has in registers (more spill)
+__host__ __device__ constexpr int norm_resident(int threads, int values) {
+  const int n = (values >= 32 ? 512 : values >= 16 ? 768 : 1024) / threads;
+  return n > 0 ? n : 1;
+}
+
+// Sum of a row's values over its TPR threads.  `slot` selects one of two
+// scratch rows: a slot is written again only after a barrier that follows
+// its last read, so one barrier a sum is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (*scratch)[32], int slot) {
+  v = warp_sum(v);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) scratch[slot][warp] = v;
+    __syncthreads();
+    v = lane < W ? scratch[slot][lane] : 0.f;
+    v = warp_sum(v);
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  (The row loop's trip count is the same for all threads of a CTA
+// where a row takes the whole CTA, so the barriers match.)
+// ---------------------------------------------------------------------------
+template <class ST, int VE, int VPT, int TPR>
+__global__ void __launch_bounds__(cta_threads(TPR), norm_resident(cta_threads(TPR), VPT * VE))
+    norm_kernel(NormArgs a) {
+  using P = Pack<ST, VE>;
+  constexpr int ROWS = cta_threads(TPR) / TPR;  // rows of a CTA at a time
+  __shared__ float scratch[2][32];
+  const int lane = threadIdx.x % TPR;
+  const int nv = (int)(a.D / VE);
+  const float inv_d = 1.f / (float)a.D;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  pdl_trigger();
+  pdl_wait();
+
+  typename P::Raw w[VPT], b[VPT], x[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = lane + j * TPR;
+    const bool on = v < nv;
+    w[j] = on ? P::load(a.weight, (int64_t)v * VE) : P::zero();
+    b[j] = on && a.bias ? P::load(a.bias, (int64_t)v * VE) : P::zero();
+    x[j] = on && row < a.N ? P::load(a.x, row * a.x_stride + (int64_t)v * VE) : P::zero();
+  }
+  for (; row < a.N; row += step) {
+    float f[VPT][VE];
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      P::open(x[j], f[j]);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s += f[j][e];
+    }
+    const int64_t next = row + step;
+    if (next < a.N) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (lane + j * TPR < nv) x[j] = P::load(a.x, next * a.x_stride + (int64_t)(lane + j * TPR) * VE);
+    }
+    const float mean = row_sum<TPR>(s, scratch, 0) * inv_d;
+    float q = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool on = lane + j * TPR < nv;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        f[j][e] = on ? f[j][e] - mean : 0.f;
+        q = fmaf(f[j][e], f[j][e], q);
+      }
+    }
+    const float rstd = rsqrtf(row_sum<TPR>(q, scratch, 1) * inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = lane + j * TPR;
+      float fw[VE], fb[VE];
+      P::open(w[j], fw);
+      P::open(b[j], fb);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) f[j][e] = fmaf(f[j][e] * rstd, fw[e], fb[e]);
+      if (v < nv) P::store(a.y, row * a.D + (int64_t)v * VE, f[j]);
+    }
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+// rows too long for registers: three passes over the row
+constexpr int kLongThreads = 512;
 template <class ST>
-__global__ void __launch_bounds__(kNormThreads) norm_rows_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kLongThreads) norm_long_kernel(NormArgs a) {
   pdl_trigger();
   pdl_wait();
   __shared__ float scratch[32];
@@ -20,15 +172,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_rows_kernel(NormArgs a) {
   const float inv_d = 1.f / (float)a.D;
   const int64_t at = i * a.x_stride;
   float s = 0.f;
-  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) s += Stor<ST>::ld(a.x, at + c);
+  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) s += Stor<ST>::ld(a.x, at + c);
   const float mean = cta_sum(s, scratch) * inv_d;
   float q = 0.f;
-  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
     const float d = Stor<ST>::ld(a.x, at + c) - mean;
     q += d * d;
   }
   const float rstd = rsqrtf(cta_sum(q, scratch) * inv_d + a.eps);
-  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
     const float xh = (Stor<ST>::ld(a.x, at + c) - mean) * rstd;
     const float b = a.bias ? Stor<ST>::ld(a.bias, c) : 0.f;
     Stor<ST>::st(a.y, i * a.D + c, xh * Stor<ST>::ld(a.weight, c) + b);
@@ -39,8 +191,134 @@ __global__ void __launch_bounds__(kNormThreads) norm_rows_kernel(NormArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Backward.  Each CTA leaves the sums of dw and db over its rows in
+// ws[CTA][2][D]; a second kernel joins them in order.
+// ---------------------------------------------------------------------------
+__host__ __device__ constexpr int grad_resident(int threads, int values) {
+  const int n = (values >= 32 ? 384 : values >= 16 ? 512 : 640) / threads;
+  return n > 0 ? n : 1;
+}
+
+template <class ST, int VE, int VPT, int TPR>
+__global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TPR), VPT * VE)) norm_grad_kernel(NormGradArgs a) {
+  using P = Pack<ST, VE>;
+  constexpr int ROWS = cta_threads(TPR) / TPR;
+  __shared__ float scratch[2][2][32];
+  const int lane = threadIdx.x % TPR;
+  const int nv = (int)(a.D / VE);
+  const float inv_d = 1.f / (float)a.D;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const bool sums = a.dweight != nullptr || a.dbias != nullptr;
+  pdl_trigger();
+  pdl_wait();
+
+  typename P::Raw w[VPT], x[VPT], dy[VPT];
+  float dw[VPT][VE], db[VPT][VE];
+  float mean = 0.f, rstd = 0.f;
+  if (row < a.N) mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = lane + j * TPR;
+    const bool on = v < nv;
+    w[j] = on ? P::load(a.weight, (int64_t)v * VE) : P::zero();
+    x[j] = on && row < a.N ? P::load(a.x, row * a.x_stride + (int64_t)v * VE) : P::zero();
+    dy[j] = on && row < a.N ? P::load(a.dy, row * a.dy_stride + (int64_t)v * VE) : P::zero();
+#pragma unroll
+    for (int e = 0; e < VE; ++e) dw[j][e] = db[j][e] = 0.f;
+  }
+  int slot = 0;
+  for (; row < a.N; row += step) {
+    float xh[VPT][VE], g[VPT][VE];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float fw[VE];
+      P::open(x[j], xh[j]);
+      P::open(dy[j], g[j]);
+      P::open(w[j], fw);
+      const bool on = lane + j * TPR < nv;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        xh[j][e] = on ? (xh[j][e] - mean) * rstd : 0.f;
+        dw[j][e] = fmaf(g[j][e], xh[j][e], dw[j][e]);
+        db[j][e] += g[j][e];
+        g[j][e] *= fw[e];
+        s1 += g[j][e];
+        s2 = fmaf(g[j][e], xh[j][e], s2);
+      }
+    }
+    const float r = rstd;
+    const int64_t next = row + step;
+    if (next < a.N) {
+      mean = a.mean[next], rstd = a.rstd[next];
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = lane + j * TPR;
+        if (v < nv) {
+          x[j] = P::load(a.x, next * a.x_stride + (int64_t)v * VE);
+          dy[j] = P::load(a.dy, next * a.dy_stride + (int64_t)v * VE);
+        }
+      }
+    }
+    if (a.dx == nullptr) continue;
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if constexpr (TPR > 32) {
+      // both sums over one barrier; the slots alternate from row to row, so
+      // one is written again only after the other row's barrier
+      const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
+      if (l == 0) scratch[slot][0][warp] = s1, scratch[slot][1][warp] = s2;
+      __syncthreads();
+      s1 = warp_sum(l < TPR / 32 ? scratch[slot][0][l] : 0.f);
+      s2 = warp_sum(l < TPR / 32 ? scratch[slot][1][l] : 0.f);
+      slot ^= 1;
+    }
+    s1 *= inv_d;
+    s2 *= inv_d;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = lane + j * TPR;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) g[j][e] = r * (g[j][e] - s1 - xh[j][e] * s2);
+      if (v < nv) P::store(a.dx, row * a.D + (int64_t)v * VE, g[j]);
+    }
+  }
+  if (!sums) return;
+  float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D;
+  if constexpr (ROWS == 1) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = lane + j * TPR;
+      if (v < nv) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) out[v * VE + e] = dw[j][e], out[a.D + v * VE + e] = db[j][e];
+      }
+    }
+  } else {
+    // the CTA's rows side by side, added in order
+    __shared__ float acc[2][VPT * TPR * VE];
+    for (int k = 0; k < ROWS; ++k) {
+      if (threadIdx.x / TPR == k) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const int c = (lane + j * TPR) * VE + e;
+            acc[0][c] = dw[j][e] + (k > 0 ? acc[0][c] : 0.f);
+            acc[1][c] = db[j][e] + (k > 0 ? acc[1][c] : 0.f);
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.D; c += cta_threads(TPR)) out[c] = acc[0][c], out[a.D + c] = acc[1][c];
+  }
+}
+
+// rows too long for registers
 template <class ST>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_rows_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(kLongThreads) norm_grad_long_kernel(NormGradArgs a) {
   pdl_trigger();
   pdl_wait();
   __shared__ float scratch[32];
@@ -48,7 +326,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_rows_kernel(NormGradAr
   const float inv_d = 1.f / (float)a.D;
   const float mean = a.mean[i], rstd = a.rstd[i];
   float s1 = 0.f, s2 = 0.f;
-  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
     const float g = Stor<ST>::ld(a.dy, i * a.dy_stride + c) * Stor<ST>::ld(a.weight, c);
     const float xh = (Stor<ST>::ld(a.x, i * a.x_stride + c) - mean) * rstd;
     s1 += g;
@@ -56,27 +334,26 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_rows_kernel(NormGradAr
   }
   s1 = cta_sum(s1, scratch) * inv_d;
   s2 = cta_sum(s2, scratch) * inv_d;
-  for (int64_t c = threadIdx.x; c < a.D; c += blockDim.x) {
+  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
     const float g = Stor<ST>::ld(a.dy, i * a.dy_stride + c) * Stor<ST>::ld(a.weight, c);
     const float xh = (Stor<ST>::ld(a.x, i * a.x_stride + c) - mean) * rstd;
     Stor<ST>::st(a.dx, i * a.D + c, rstd * (g - s1 - xh * s2));
   }
 }
 
-// rows a slice of the weight gradient's first sum covers
-constexpr int64_t kSliceRows = 64;
-
-// ws[slice][0][c] = sum over the slice's rows of dy * xh, ws[slice][1][c] = of dy
+// ... and their sums of dw and db, a slice of rows a CTA
+constexpr int kSliceThreads = 256;
 template <class ST>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_slices_kernel(NormGradArgs a, int64_t col_blocks) {
+__global__ void __launch_bounds__(kSliceThreads)
+    norm_grad_slices_kernel(NormGradArgs a, int64_t col_blocks, int64_t slice_rows) {
   pdl_trigger();
   pdl_wait();
   const int64_t slice = blockIdx.x / col_blocks;
-  const int64_t c = (blockIdx.x % col_blocks) * kNormThreads + threadIdx.x;
+  const int64_t c = (blockIdx.x % col_blocks) * kSliceThreads + threadIdx.x;
   if (c >= a.D) return;
-  const int64_t i1 = min(a.N, (slice + 1) * kSliceRows);
+  const int64_t i1 = min(a.N, (slice + 1) * slice_rows);
   float dw = 0.f, db = 0.f;
-  for (int64_t i = slice * kSliceRows; i < i1; ++i) {
+  for (int64_t i = slice * slice_rows; i < i1; ++i) {
     const float dy = Stor<ST>::ld(a.dy, i * a.dy_stride + c);
     dw += dy * ((Stor<ST>::ld(a.x, i * a.x_stride + c) - a.mean[i]) * a.rstd[i]);
     db += dy;
@@ -85,50 +362,145 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_slices_kernel(NormGrad
   a.ws[(2 * slice + 1) * a.D + c] = db;
 }
 
-// the slices' sums, in order
-template <class ST>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_join_kernel(NormGradArgs a, int64_t slices) {
+// The partial sums of 32 columns, joined by 32 x 32 threads: warp k adds the
+// partials k, k + 32, ... of its columns, then the warps' sums are added in
+// order.  blockIdx.x < col_blocks: dw, else db.
+__global__ void __launch_bounds__(1024)
+    norm_grad_join_kernel(const float* ws, int64_t parts, int64_t D, float* dweight, float* dbias, bool bf16_io) {
   pdl_trigger();
   pdl_wait();
-  const int64_t c = (int64_t)blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= a.D) return;
-  float dw = 0.f, db = 0.f;
-  for (int64_t k = 0; k < slices; ++k) {
-    dw += a.ws[(2 * k) * a.D + c];
-    db += a.ws[(2 * k + 1) * a.D + c];
-  }
-  if (a.dweight) Stor<ST>::st(a.dweight, c, dw);
-  if (a.dbias) Stor<ST>::st(a.dbias, c, db);
+  __shared__ float acc[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t col_blocks = (D + 31) / 32;
+  const int which = blockIdx.x >= col_blocks;
+  float* out = which ? dbias : dweight;
+  if (out == nullptr) return;
+  const int64_t c = (blockIdx.x - which * col_blocks) * 32 + lane;
+  float s = 0.f;
+  if (c < D)
+    for (int64_t k = warp; k < parts; k += 32) s += ws[(2 * k + which) * D + c];
+  acc[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= D) return;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) s += acc[k][lane];
+  if (bf16_io) Stor<bf16>::st(out, c, s);
+  else Stor<float>::st(out, c, s);
+}
+
+// ---------------------------------------------------------------------------
+// Which variant: vectors of 16 bytes where every row of every array starts on
+// such a boundary, else single elements; the fewest threads a row with up to
+// 4 vectors (forward; 2 backward, whose sums take the registers) or 8 single
+// elements a thread.
+// ---------------------------------------------------------------------------
+bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides, int es) {
+  for (const void* p : bases)
+    if (((uintptr_t)p & 15) != 0) return false;
+  for (int64_t s : strides)
+    if ((s * es) % 16 != 0) return false;
+  return true;
+}
+
+template <class ST, int VE, int VPT, int TPR>
+cudaError_t launch_norm(const NormArgs& a, int sm, cudaStream_t s) {
+  constexpr int T = cta_threads(TPR), R = norm_resident(T, VPT * VE);
+  const int64_t grid = std::min<int64_t>(div_up(a.N, T / TPR), (int64_t)R * sm);
+  return launch_pdl(norm_kernel<ST, VE, VPT, TPR>, grid, T, 0, s, a);
 }
 
 template <class ST>
-cudaError_t grad_typed(const NormGradArgs& a, cudaStream_t s) {
-  if (a.dx != nullptr && a.N > 0) {
-    cudaError_t e = launch_pdl(norm_grad_rows_kernel<ST>, a.N, kNormThreads, 0, s, a);
+cudaError_t norm_typed(const NormArgs& a, int sm, cudaStream_t s) {
+  constexpr int VE = 16 / Stor<ST>::kBytes;
+  if (rows_aligned({a.x, a.y, a.weight, a.bias}, {a.D, a.x_stride}, Stor<ST>::kBytes)) {
+    const int64_t nv = a.D / VE;
+    if (nv <= 32) return launch_norm<ST, VE, 1, 32>(a, sm, s);
+    if (nv <= 64) return launch_norm<ST, VE, 2, 32>(a, sm, s);
+    if (nv <= 128) return launch_norm<ST, VE, 4, 32>(a, sm, s);
+    if (nv <= 256) return launch_norm<ST, VE, 2, 128>(a, sm, s);
+    if (nv <= 512) return launch_norm<ST, VE, 4, 128>(a, sm, s);
+    if (nv <= 1024) return launch_norm<ST, VE, 4, 256>(a, sm, s);
+    if (nv <= 2048) return launch_norm<ST, VE, 4, 512>(a, sm, s);
+  } else {
+    if (a.D <= 32) return launch_norm<ST, 1, 1, 32>(a, sm, s);
+    if (a.D <= 256) return launch_norm<ST, 1, 8, 32>(a, sm, s);
+    if (a.D <= 1024) return launch_norm<ST, 1, 8, 128>(a, sm, s);
+    if (a.D <= 2048) return launch_norm<ST, 1, 8, 256>(a, sm, s);
+    if (a.D <= 4096) return launch_norm<ST, 1, 8, 512>(a, sm, s);
+  }
+  return launch_pdl(norm_long_kernel<ST>, a.N, kLongThreads, 0, s, a);
+}
+
+// CTAs of a backward launch of T threads, R rows at a time
+int64_t grad_grid(int64_t N, int T, int R, int values, int sm) {
+  return std::min<int64_t>(div_up(N, R), (int64_t)grad_resident(T, values) * sm);
+}
+
+cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
+  if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
+  return launch_pdl(norm_grad_join_kernel, 2 * div_up(a.D, 32), 1024, 0, s, (const float*)a.ws, parts, a.D, a.dweight,
+                    a.dbias, a.bf16_io);
+}
+
+template <class ST, int VE, int VPT, int TPR>
+cudaError_t launch_grad(const NormGradArgs& a, int sm, cudaStream_t s) {
+  constexpr int T = cta_threads(TPR);
+  const int64_t grid = grad_grid(a.N, T, T / TPR, VPT * VE, sm);
+  const cudaError_t e = launch_pdl(norm_grad_kernel<ST, VE, VPT, TPR>, grid, T, 0, s, a);
+  return e == cudaSuccess ? join(a, grid, s) : e;
+}
+
+// rows of a slice of the long rows' first sum: enough slices to fill the SMs
+int64_t slice_rows(int64_t N, int64_t D, int sm) {
+  const int64_t want = std::max<int64_t>(1, 8 * (int64_t)sm / div_up(D, kSliceThreads));
+  return std::max<int64_t>(1, div_up(N, want));
+}
+
+template <class ST>
+cudaError_t grad_typed(const NormGradArgs& a, int sm, cudaStream_t s) {
+  if (a.N == 0) return join(a, 0, s);
+  constexpr int VE = 16 / Stor<ST>::kBytes;
+  if (rows_aligned({a.x, a.dy, a.dx, a.weight}, {a.D, a.x_stride, a.dy_stride}, Stor<ST>::kBytes)) {
+    const int64_t nv = a.D / VE;
+    if (nv <= 32) return launch_grad<ST, VE, 1, 32>(a, sm, s);
+    if (nv <= 64) return launch_grad<ST, VE, 2, 32>(a, sm, s);
+    if (nv <= 128) return launch_grad<ST, VE, 1, 128>(a, sm, s);
+    if (nv <= 256) return launch_grad<ST, VE, 2, 128>(a, sm, s);
+    if (nv <= 512) return launch_grad<ST, VE, 2, 256>(a, sm, s);
+    if (nv <= 1024) return launch_grad<ST, VE, 2, 512>(a, sm, s);
+  } else {
+    if (a.D <= 32) return launch_grad<ST, 1, 1, 32>(a, sm, s);
+    if (a.D <= 256) return launch_grad<ST, 1, 8, 32>(a, sm, s);
+    if (a.D <= 1024) return launch_grad<ST, 1, 8, 128>(a, sm, s);
+    if (a.D <= 2048) return launch_grad<ST, 1, 8, 256>(a, sm, s);
+    if (a.D <= 4096) return launch_grad<ST, 1, 8, 512>(a, sm, s);
+  }
+  if (a.dx != nullptr) {
+    const cudaError_t e = launch_pdl(norm_grad_long_kernel<ST>, a.N, kLongThreads, 0, s, a);
     if (e != cudaSuccess) return e;
   }
   if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
-  const int64_t slices = div_up(a.N, kSliceRows), col_blocks = div_up(a.D, kNormThreads);
-  if (slices > 0) {
-    cudaError_t e = launch_pdl(norm_grad_slices_kernel<ST>, slices * col_blocks, kNormThreads, 0, s, a, col_blocks);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(norm_grad_join_kernel<ST>, col_blocks, kNormThreads, 0, s, a, slices);
+  const int64_t col_blocks = div_up(a.D, kSliceThreads), rows = slice_rows(a.N, a.D, sm), slices = div_up(a.N, rows);
+  const cudaError_t e =
+      launch_pdl(norm_grad_slices_kernel<ST>, slices * col_blocks, kSliceThreads, 0, s, a, col_blocks, rows);
+  return e == cudaSuccess ? join(a, slices, s) : e;
 }
 
 }  // namespace
 
-cudaError_t run_layer_norm(const NormArgs& a, int, cudaStream_t s) {
-  return a.bf16_io ? launch_pdl(norm_rows_kernel<bf16>, a.N, kNormThreads, 0, s, a)
-                   : launch_pdl(norm_rows_kernel<float>, a.N, kNormThreads, 0, s, a);
+cudaError_t run_layer_norm(const NormArgs& a, int sm, cudaStream_t s) {
+  return a.bf16_io ? norm_typed<bf16>(a, sm, s) : norm_typed<float>(a, sm, s);
 }
 
-size_t layer_norm_backward_workspace(int64_t N, int64_t D, int) {
-  return (size_t)div_up(N, kSliceRows) * 2 * (size_t)D * sizeof(float);
+// the most partial sums any variant leaves: CTAs of 128 threads, or slices
+size_t layer_norm_backward_workspace(int64_t N, int64_t D, int sm) {
+  const int64_t parts = std::max(grad_grid(N, 128, 1, 1, sm), div_up(N, slice_rows(N, D, sm)));
+  return (size_t)parts * 2 * (size_t)D * sizeof(float);
 }
 
-cudaError_t run_layer_norm_backward(const NormGradArgs& a, int, cudaStream_t s) {
-  return a.bf16_io ? grad_typed<bf16>(a, s) : grad_typed<float>(a, s);
+cudaError_t run_layer_norm_backward(const NormGradArgs& a, int sm, cudaStream_t s) {
+  return a.bf16_io ? grad_typed<bf16>(a, sm, s) : grad_typed<float>(a, sm, s);
 }
 
 cudaError_t status_norm(unsigned int* word, bool clear) { return unit_status(word, clear); }
