@@ -52,7 +52,89 @@ __device__ __forceinline__ ClipItem clip_item(const ClipTable& t, uint32_t chunk
 }
 
 __device__ __forceinline__ float load_any(const void* p, int64_t i, bool bf) {
-  return bf ? Stor<bf16>::ld(static_cast<const float*>(p), i) : static_cast<const float*>(p)[i];
+  // plain loads: in place, the kernel that reads also writes
+  return bf ? Stor<bf16>::from_bits(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void store_any(void* p, int64_t i, bool bf, float v) {
+  if (bf) Stor<bf16>::st(static_cast<float*>(p), i, v);
+  else static_cast<float*>(p)[i] = v;
+}
+
+// the four float32 or eight bfloat16 values of a 16-byte vector
+template <bool BF>
+__device__ __forceinline__ float vec_squares(const uint4& r) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF) {
+      const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+      s = fmaf(lo, lo, s);
+      s = fmaf(hi, hi, s);
+    } else {
+      const float v = __uint_as_float(w[k]);
+      s = fmaf(v, v, s);
+    }
+  }
+  return s;
+}
+template <bool BF>
+__device__ __forceinline__ uint4 vec_scaled(const uint4& r, float f) {
+  uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF)
+      w[k] = Stor<bf16>::pack2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+    else
+      w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int kClipUnroll = 8;  // 16-byte loads a thread has in flight
+
+// sum of squares of n vectors, this thread's share
+template <bool BF>
+__device__ __forceinline__ float chunk_squares(const uint4* p, int n) {
+  float s = 0.f;
+  int k = threadIdx.x;
+  for (; k + (kClipUnroll - 1) * kClipThreads < n; k += kClipUnroll * kClipThreads) {
+    uint4 r[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) r[u] = __ldg(p + k + u * kClipThreads);
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) s += vec_squares<BF>(r[u]);
+  }
+  for (; k < n; k += kClipThreads) s += vec_squares<BF>(__ldg(p + k));
+  return s;
+}
+
+template <bool BF>
+__device__ __forceinline__ void chunk_scale(const uint4* p, uint4* o, int n, float f) {
+  int k = threadIdx.x;
+  for (; k + (kClipUnroll - 1) * kClipThreads < n; k += kClipUnroll * kClipThreads) {
+    uint4 r[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) r[u] = p[k + u * kClipThreads];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) o[k + u * kClipThreads] = vec_scaled<BF>(r[u], f);
+  }
+  for (; k < n; k += kClipThreads) o[k] = vec_scaled<BF>(p[k], f);
+}
+
+// A chunk as vectors with single elements around them: `lead` elements up to
+// the first 16-byte boundary, `vecs` vectors, the rest.
+struct ClipSpan {
+  int64_t lead, vecs, tail;  // tail: first element after the vectors
+};
+__device__ __forceinline__ ClipSpan clip_span(const ClipItem& it) {
+  const int es = it.bf16_io ? 2 : 4;
+  const uintptr_t at = (uintptr_t)it.grad + (uintptr_t)it.at * es;
+  ClipSpan s;
+  s.lead = min((int64_t)(((16 - (at & 15)) & 15) / es), it.n);
+  s.vecs = (it.n - s.lead) / (16 / es);
+  s.tail = s.lead + s.vecs * (16 / es);
+  return s;
 }
 
 // partials[CTA] = sum of squares over the CTA's chunks
@@ -63,10 +145,18 @@ __global__ void __launch_bounds__(kClipThreads) clip_squares_kernel(const __grid
   double total = 0.0;
   for (uint32_t chunk = blockIdx.x; chunk < t.first[t.count]; chunk += gridDim.x) {
     const ClipItem it = clip_item(t, chunk);
-    float s = 0.f;
-    for (int64_t k = threadIdx.x; k < it.n; k += kClipThreads) {
-      const float g = load_any(it.grad, it.at + k, it.bf16_io);
-      s += g * g;
+    const ClipSpan sp = clip_span(it);
+    const int es = it.bf16_io ? 2 : 4;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(it.grad) + (it.at + sp.lead) * es);
+    // float32 over at most kClipChunk / kClipThreads squares, float64 beyond
+    float s = it.bf16_io ? chunk_squares<true>(p, (int)sp.vecs) : chunk_squares<false>(p, (int)sp.vecs);
+    if (threadIdx.x < sp.lead) {
+      const float g = load_any(it.grad, it.at + threadIdx.x, it.bf16_io);
+      s = fmaf(g, g, s);
+    }
+    if (sp.tail + threadIdx.x < it.n) {
+      const float g = load_any(it.grad, it.at + sp.tail + threadIdx.x, it.bf16_io);
+      s = fmaf(g, g, s);
     }
     total += (double)s;
   }
@@ -90,14 +180,24 @@ __global__ void __launch_bounds__(kClipThreads)
   pdl_wait();
   const float n = *norm;
   const float scale = isfinite(n) ? fminf(1.f, max_norm / (n + eps)) : 1.f;
-  for (uint32_t chunk = blockIdx.x; chunk < t.first[t.count]; chunk += gridDim.x) {
-    const ClipItem it = clip_item(t, chunk);
+  // the squares walked the chunks upwards: downwards, the first ones here are
+  // the last ones read there and still in L2
+  const uint32_t chunks = t.first[t.count];
+  for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const ClipItem it = clip_item(t, chunks - 1 - k);
     if (scale == 1.f && it.out == it.grad) continue;
-    for (int64_t k = threadIdx.x; k < it.n; k += kClipThreads) {
-      const float g = load_any(it.grad, it.at + k, it.bf16_io) * scale;
-      if (it.bf16_io) Stor<bf16>::st(static_cast<float*>(it.out), it.at + k, g);
-      else static_cast<float*>(it.out)[it.at + k] = g;
-    }
+    const int es = it.bf16_io ? 2 : 4;
+    ClipSpan sp = clip_span(it);
+    // vectors need both sides on 16-byte boundaries at the same element
+    if ((((uintptr_t)it.grad ^ (uintptr_t)it.out) & 15) != 0) sp.lead = sp.vecs = sp.tail = 0;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(it.grad) + (it.at + sp.lead) * es);
+    uint4* o = reinterpret_cast<uint4*>(static_cast<unsigned char*>(it.out) + (it.at + sp.lead) * es);
+    if (it.bf16_io) chunk_scale<true>(p, o, (int)sp.vecs, scale);
+    else chunk_scale<false>(p, o, (int)sp.vecs, scale);
+    if (threadIdx.x < sp.lead)
+      store_any(it.out, it.at + threadIdx.x, it.bf16_io, load_any(it.grad, it.at + threadIdx.x, it.bf16_io) * scale);
+    for (int64_t e = sp.tail + threadIdx.x; e < it.n; e += kClipThreads)
+      store_any(it.out, it.at + e, it.bf16_io, load_any(it.grad, it.at + e, it.bf16_io) * scale);
   }
 }
 
