@@ -488,14 +488,14 @@ TcTerms terms_of(int planes) {
   return t;
 }
 
-template <bool A_MN, bool B_MN, class Epi>
+template <bool A_MN, bool B_MN, int GROUP, class Epi>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const TcShape& s, const Epi& epi, int sm_count,
                            cudaStream_t st) {
-  const auto kernel = tc_product_kernel<A_MN, B_MN, Epi>;
+  const auto kernel = tc_product_kernel<A_MN, B_MN, GROUP, Epi>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits;
-  return launch_pdl(kernel, std::min<int64_t>(tiles, sm_count), kTcThreads, kTcSmem, st, ma, mb, s, epi);
+  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, ma, mb, s, epi);
 }
 
 // rows of A walked together: as many as keep their `width` values in L2
@@ -508,8 +508,14 @@ bool in_place(const HeadArgs& a) {
   return a.bf16_io && ((uintptr_t)a.weight & 15) == 0 && a.weight_stride % 8 == 0;
 }
 
+// Stages summed by the tensor cores alone (tc.cuh): 512 values of k for
+// results that leave in float32; the bfloat16 gradients' own rounding is
+// larger than the whole sum's error.
+constexpr int kLogitsGroup = 8;
+
 template <class ST>
 struct HeadRun {
+  static constexpr int kGradGroup = Stor<ST>::kBytes == 4 ? kLogitsGroup : 0;
   const HeadArgs& a;
   const HeadPlan p;
   const HeadView w;
@@ -522,7 +528,7 @@ struct HeadRun {
       : a(args), p(plan), w(plan, args.ws), sm(sm_count), s(st), terms(terms_of(plan.planes)) {}
 
   cudaError_t rows() {
-    if (!encode_matrix_map(&hidden_k, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcM) ||
+    if (!encode_matrix_map(&hidden_k, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcRows) ||
         !encode_matrix_map(&hidden_mn, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcK))
       return cudaErrorNotSupported;
     cudaError_t e = launch_pdl(head_rows_kernel, 1, kRowsThreads, 0, s, a, w);
@@ -565,9 +571,9 @@ struct HeadRun {
       e = weight_piece(v0, len);
       if (e != cudaSuccess) break;
       CUtensorMap wk;
-      if (!weight_map(&wk, len, kTcN)) return cudaErrorNotSupported;
+      if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, (int)v0, (int)(v0 + len), c2};
-      e = launch_product<false, false>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
+      e = launch_product<false, false, kLogitsGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
     }
     if (e == cudaSuccess)
       e = launch_pdl(head_join_kernel, div_up(a.N, kJoinThreads / 32), kJoinThreads, 0, s, a, w, div_up(a.V, kTcN) * 2,
@@ -583,16 +589,16 @@ struct HeadRun {
       e = weight_piece(v0, len);
       if (e != cudaSuccess) break;
       CUtensorMap wk, wmn, dz_k, dz_mn;
-      if (!weight_map(&wk, len, kTcN) || !weight_map(&wmn, len, kTcK) ||
-          !encode_matrix_map(&dz_k, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcM) ||
+      if (!weight_map(&wk, len, kTcN / 2) || !weight_map(&wmn, len, kTcK) ||
+          !encode_matrix_map(&dz_k, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcRows) ||
           !encode_matrix_map(&dz_mn, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcK))
         return cudaErrorNotSupported;
-      if (p.planes == 1) {
+      if constexpr (Stor<ST>::kBytes == 2) {
         const DzEpi<1> epi{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
-        e = launch_product<false, false>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
+        e = launch_product<false, false, kGradGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
       } else {
         const DzEpi<3> epi{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
-        e = launch_product<false, false>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
+        e = launch_product<false, false, kGradGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
       }
       if (e == cudaSuccess && a.d_hidden) {
         TcShape t = {};
@@ -600,7 +606,7 @@ struct HeadRun {
         t.m = (int)a.N; t.n = (int)a.D; t.k = (int)len;
         t.b_k0 = p.packed ? 0 : (int)v0;
         t.splits = p.splits; t.band = 16; t.terms = terms;
-        e = launch_product<false, true>(dz_k, wmn, t, SumEpi{w.dh, p.Dh, dh_plane, v0 > 0}, sm, s);
+        e = launch_product<false, true, kGradGroup>(dz_k, wmn, t, SumEpi{w.dh, p.Dh, dh_plane, v0 > 0}, sm, s);
       }
       if (e == cudaSuccess && a.d_weight) {
         TcShape t = {};
@@ -608,7 +614,7 @@ struct HeadRun {
         t.m = (int)len; t.n = (int)a.D; t.k = (int)a.N;
         t.splits = 1; t.band = 16; t.terms = terms;
         const bool vec = (a.D * Stor<ST>::kBytes) % 16 == 0 && ((uintptr_t)a.d_weight & 15) == 0;
-        e = launch_product<true, true>(dz_mn, hidden_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, vec}, sm, s);
+        e = launch_product<true, true, kGradGroup>(dz_mn, hidden_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, vec}, sm, s);
       }
     }
     if (e == cudaSuccess && a.d_hidden)

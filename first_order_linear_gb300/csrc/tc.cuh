@@ -14,28 +14,42 @@
 // contiguous): the shared-memory descriptors and the instruction descriptor
 // say which, so no operand is ever transposed in memory.
 //
-// One CTA an SM: warps 0-7 run the epilogue (warp w reads TMEM lanes
-// 32 (w % 4) .. + 31 and the tile's column half w / 4), warp 8 issues the
-// copies, warp 9 the matrix instructions.  The accumulator is double-buffered
-// in TMEM (2 x 256 columns), so the epilogue of one tile runs under the
-// product of the next.  Every wait is bounded: a wait that gives up records
-// the timeout in the status word and raises a shared flag that ends all
-// roles; the copies in flight are then waited for (bounded) before TMEM is
-// freed.
+// Two CTAs (a cluster, one an SM) work on one 256 x 256 tile: each loads its
+// 128 rows of A and half of B's 256 rows, so a stage brings 64 KB for 256 x
+// 256 x 64 products instead of the 96 KB of two 128 x 256 tiles -- per SM 64
+// bytes a cycle at the tensor cores' full rate --, and the first CTA's
+// tcgen05.mma reads both CTAs' shared memory and writes both CTAs' TMEM.  In
+// each CTA warps 0-7 run the epilogue of its 128 rows (warp w reads TMEM lanes
+// 32 (w % 4) .. + 31 and column half w / 4), warp 8 issues the copies; warp 9
+// of the first CTA issues the matrix instructions.  The accumulator is
+// double-buffered in TMEM (2 x 256 columns), so an epilogue runs under the
+// next product.
+//
+// The accumulator of a tensor core drops bits where IEEE addition would
+// round (measured: the error of a sum grows with its number of k steps,
+// 1.7e-6 of a log-probability at k = 4096 against 3e-7 in plain float32).
+// GROUP > 0 therefore starts a new accumulator every GROUP stages and adds
+// the partial sums in float32 registers.
+//
+// Every wait is bounded: a wait that gives up records the timeout in the
+// status word and raises a shared flag that ends the CTA's roles (the other
+// CTA's waits then run out too); copies and matrix instructions in flight are
+// waited for (bounded) before TMEM is freed and the cluster ends together.
 #pragma once
 
 #include "tma.cuh"
 
 namespace rlca {
 
-constexpr int kTcM = 128;      // rows of a CTA's tile
-constexpr int kTcN = 256;      // columns of a tile
+constexpr int kTcM = 256;      // rows of a tile, half of them each CTA's
+constexpr int kTcN = 256;      // columns of a tile; each CTA copies half of B's rows
 constexpr int kTcK = 64;       // k per stage: one 128-byte swizzle row of bfloat16
-constexpr int kTcStages = 4;
+constexpr int kTcStages = 6;
+constexpr int kTcRows = kTcM / 2;  // rows a CTA loads and finishes
 constexpr int kTcEpiWarps = 8;
 constexpr int kTcThreads = 32 * (kTcEpiWarps + 2);
-constexpr int kTcABytes = kTcM * kTcK * 2;
-constexpr int kTcBBytes = kTcN * kTcK * 2;
+constexpr int kTcABytes = kTcRows * kTcK * 2;
+constexpr int kTcBBytes = kTcN / 2 * kTcK * 2;
 constexpr int kTcStageBytes = kTcABytes + kTcBBytes;
 constexpr size_t kTcSmem = (size_t)kTcStages * kTcStageBytes + 1024;  // + alignment of the ring
 
@@ -59,26 +73,30 @@ struct TcShape {
 
 // ---- tcgen05 ------------------------------------------------------------------
 __device__ __forceinline__ void tc_alloc(uint32_t* smem_dst, uint32_t cols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)), "r"(cols)
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)), "r"(cols)
                : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tc_free(uint32_t addr, uint32_t cols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// arrives on `bar` once every matrix instruction issued so far has completed
+// arrives on `bar` -- of both CTAs -- once every matrix instruction issued so
+// far has completed
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n"
       ".reg .pred p;\n"
       "setp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
       "}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
@@ -101,6 +119,21 @@ __device__ __forceinline__ void tc_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// ... 16 columns, added to v
+__device__ __forceinline__ void tc_add16(uint32_t addr, float* v) {
+  uint32_t r[16];
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
+}
+
 // Shared-memory matrix descriptor of a 128-byte-swizzled tile at `addr`
 // (1024-byte aligned but for the k offset inside a swizzle row).  K-major:
 // rows of 128 bytes, groups of 8 rows 1024 bytes apart.  MN-major: blocks of
@@ -115,26 +148,63 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
 template <bool MN>
 constexpr uint64_t kTcStepK = MN ? (2 * 1024) >> 4 : 32 >> 4;
 
-// bfloat16 x bfloat16 -> float32, M = 128, N = 256
+// bfloat16 x bfloat16 -> float32, M = 256, N = 256
 template <bool A_MN, bool B_MN>
 constexpr uint32_t kTcInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
                               ((uint32_t)(kTcN >> 3) << 17) | ((uint32_t)(kTcM >> 4) << 24);
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+// ---- the two CTAs of a cluster -----------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// cluster-wide address of the first CTA's copy of a shared variable
+__device__ __forceinline__ uint32_t in_first(const void* p) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// a copy into this CTA's shared memory, counted by the barrier at `bar`
+// (which may be the other CTA's)
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ bool tc_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 
 // a bounded wait that also ends when another role has given up
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (tc_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+      if (tc_try_wait(bar, parity)) return true;
     if (*stop) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
       atomicOr(&g_tu_status, kStatusWaitTimeout);
@@ -181,19 +251,23 @@ struct TcWalk {
   }
 };
 
-// Epi: struct State; begin(State&, tile, row, half) with row = the thread's
-// row of C and half = first column of its half tile; chunk(State&, col, v[32])
-// for the 32 columns from col on; end(State&).  m extent in walk.m.
-template <bool A_MN, bool B_MN, class Epi>
-__global__ void __launch_bounds__(kTcThreads, 1)
+// Epi: struct State; begin(State&, walk, tile, row, col0) with row = the
+// thread's row of C and col0 the first column of its half tile;
+// chunk(State&, col, v[32]) for the 32 columns from col on; end(State&).
+// Rows from walk.m on do not exist.
+template <bool A_MN, bool B_MN, int GROUP, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ TcShape s, const __grid_constant__ Epi epi) {
   extern __shared__ unsigned char tc_smem_raw[];
+  // of the first CTA: full, acc_empty; of both: empty, acc_full, drained
   __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int stop;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)tc_smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   pdl_trigger();
   if (warp == kTcEpiWarps + 1) tc_alloc(&tmem_base, 2 * kTcN);
@@ -204,7 +278,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kTcEpiWarps);
+      mbar_init(&acc_empty[i], 2 * kTcEpiWarps);
     }
     mbar_init(&drained, 1);
     stop = 0;
@@ -212,6 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   pdl_wait();
@@ -227,8 +302,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < walk.tiles && ok; t += gridDim.x) {
+      for (int64_t t = first; t < walk.tiles && ok; t += step) {
         const TcTile tile = walk.at(t, s);
+        const int m0 = s.a_m0 + tile.m0 + rank * kTcRows, n0 = s.b_n0 + tile.n0 + rank * (kTcN / 2);
         for (int term = 0; term < s.terms.n && ok; ++term) {
           const int pa = s.terms.a[term], pb = s.terms.b[term];
           for (int ks = tile.k_begin; ks < tile.k_end; ++ks) {
@@ -238,63 +314,74 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             unsigned char* sa = ring + stage * kTcStageBytes;
             unsigned char* sb = sa + kTcABytes;
-            mbar_arrive_expect_tx(&full[stage], kTcStageBytes);
+            const uint32_t bar = in_first(&full[stage]);
+            // both CTAs' bytes (the other's may land first: the phase ends
+            // with this arrival at the earliest)
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kTcStageBytes);
             const int k0 = ks * kTcK;
             if constexpr (A_MN) {
 #pragma unroll
-              for (int i = 0; i < kTcM / 64; ++i)
-                tma_load_3d(sa + i * kTcK * 128, &map_a, s.a_m0 + tile.m0 + 64 * i, k0, pa, &full[stage]);
+              for (int i = 0; i < kTcRows / 64; ++i)
+                tma_load_3d(sa + i * kTcK * 128, &map_a, m0 + 64 * i, k0, pa, bar);
             } else {
-              tma_load_3d(sa, &map_a, k0, s.a_m0 + tile.m0, pa, &full[stage]);
+              tma_load_3d(sa, &map_a, k0, m0, pa, bar);
             }
             if constexpr (B_MN) {
 #pragma unroll
-              for (int i = 0; i < kTcN / 64; ++i)
-                tma_load_3d(sb + i * kTcK * 128, &map_b, s.b_n0 + tile.n0 + 64 * i, s.b_k0 + k0, pb, &full[stage]);
+              for (int i = 0; i < kTcN / 2 / 64; ++i)
+                tma_load_3d(sb + i * kTcK * 128, &map_b, n0 + 64 * i, s.b_k0 + k0, pb, bar);
             } else {
-              tma_load_3d(sb, &map_b, s.b_k0 + k0, s.b_n0 + tile.n0, pb, &full[stage]);
+              tma_load_3d(sb, &map_b, s.b_k0 + k0, n0, pb, bar);
             }
             if (++stage == kTcStages) stage = 0, phase ^= 1;
           }
         }
       }
-      // Every copy that was issued lands before the CTA ends (when all went
-      // well the matrix instructions have waited for it too).  Stage i was
-      // last filled in `phase` if i < stage, else in the phase before, or
+      // Every copy that was issued lands before the cluster ends (when all
+      // went well the matrix instructions have waited for it too).  Stage i
+      // was last filled in `phase` if i < stage, else in the phase before, or
       // never: that wait returns at once.
-      for (int i = 0; i < kTcStages; ++i) mbar_wait_bounded(&full[i], i < stage ? phase : phase ^ 1);
+      if (rank == 0)
+        for (int i = 0; i < kTcStages; ++i) mbar_wait_bounded(&full[i], i < stage ? phase : phase ^ 1);
     }
   } else if (warp == kTcEpiWarps + 1) {
     // ---- matrix instructions ----
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < walk.tiles && ok; t += gridDim.x) {
+      for (int64_t t = first; t < walk.tiles && ok; t += step) {
         const TcTile tile = walk.at(t, s);
         const int steps = (tile.k_end - tile.k_begin) * s.terms.n;
-        if (steps == 0) continue;  // the epilogue takes zeros and waits for nothing
-        if (!tc_wait(&acc_empty[buf], acc_phase ^ 1, &stop)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + buf * kTcN;
-        for (int it = 0; it < steps; ++it) {
-          if (!tc_wait(&full[stage], phase, &stop)) {
+        // (no steps: the epilogue takes zeros and waits for nothing)
+        for (int at = 0; at < steps && ok;) {
+          const int group_end = GROUP > 0 ? min(at + GROUP, steps) : steps;
+          if (!tc_wait(&acc_empty[buf], acc_phase ^ 1, &stop)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(ring + stage * kTcStageBytes);
-          const uint64_t da = tc_desc<A_MN>(sa), db = tc_desc<B_MN>(sa + kTcABytes);
+          const uint32_t d = tmem + buf * kTcN;
+          for (bool fresh = true; at < group_end; ++at) {
+            if (!tc_wait(&full[stage], phase, &stop)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(ring + stage * kTcStageBytes);
+            const uint64_t da = tc_desc<A_MN>(sa), db = tc_desc<B_MN>(sa + kTcABytes);
 #pragma unroll
-          for (int k = 0; k < kTcK / 16; ++k)
-            tc_mma(d, da + k * kTcStepK<A_MN>, db + k * kTcStepK<B_MN>, kTcInstr<A_MN, B_MN>, it > 0 || k > 0);
-          tc_commit(&empty[stage]);
-          if (++stage == kTcStages) stage = 0, phase ^= 1;
+            for (int k = 0; k < kTcK / 16; ++k)
+              tc_mma(d, da + k * kTcStepK<A_MN>, db + k * kTcStepK<B_MN>, kTcInstr<A_MN, B_MN>, !fresh || k > 0);
+            fresh = false;
+            tc_commit(&empty[stage]);
+            if (++stage == kTcStages) stage = 0, phase ^= 1;
+          }
+          if (!ok) break;
+          tc_commit(&acc_full[buf]);
+          buf ^= 1;
+          if (buf == 0) acc_phase ^= 1;
         }
-        if (!ok) break;
-        tc_commit(&acc_full[buf]);
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1;
       }
       // whatever was issued completes before TMEM is freed
       tc_commit(&drained);
@@ -305,34 +392,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quarter = warp & 3, half = warp >> 2;
     int buf = 0;
     uint32_t acc_phase = 0;
-    for (int64_t t = blockIdx.x; t < walk.tiles; t += gridDim.x) {
+    const uint32_t src0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kTcN / 2);
+    // false once a wait has given up (one verdict for the warp: the TMEM
+    // loads need all its lanes)
+    const auto acc_ready = [&] {
+      if (!__all_sync(0xffffffffu, tc_wait(&acc_full[buf], acc_phase, &stop))) return false;
+      tc_fence_after();
+      return true;
+    };
+    const auto acc_done = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(in_first(&acc_empty[buf]));
+      buf ^= 1;
+      if (buf == 0) acc_phase ^= 1;
+    };
+    for (int64_t t = first; t < walk.tiles; t += step) {
       const TcTile tile = walk.at(t, s);
-      const bool zero = (tile.k_end - tile.k_begin) * s.terms.n == 0;
+      const int steps = (tile.k_end - tile.k_begin) * s.terms.n;
+      const int col0 = tile.n0 + half * (kTcN / 2);
       typename Epi::State st;
-      epi.begin(st, walk, tile, tile.m0 + quarter * 32 + lane, tile.n0 + half * (kTcN / 2));
-      if (!zero) {
-        // (one verdict for the warp: the TMEM loads need all its lanes)
-        if (!__all_sync(0xffffffffu, tc_wait(&acc_full[buf], acc_phase, &stop))) break;
-        tc_fence_after();
-      }
-      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTcN + half * (kTcN / 2);
-#pragma unroll 1
-      for (int c = 0; c < kTcN / 2; c += 32) {
-        float v[32];
-        if (zero) {
+      epi.begin(st, walk, tile, tile.m0 + rank * kTcRows + quarter * 32 + lane, col0);
+      bool ok = true;
+      if constexpr (GROUP > 0) {
+        float sum[kTcN / 64][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        } else {
-          tc_load32(src + c, v);
+        for (int c = 0; c < kTcN / 64; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+        for (int at = 0; at < steps; at += GROUP) {
+          ok = acc_ready();
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < kTcN / 64; ++c) {
+            tc_add16(src0 + buf * kTcN + 32 * c, sum[c]);
+            tc_add16(src0 + buf * kTcN + 32 * c + 16, sum[c] + 16);
+          }
+          acc_done();
         }
-        epi.chunk(st, tile.n0 + half * (kTcN / 2) + c, v);
-      }
-      if (!zero) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1;
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kTcN / 64; ++c) epi.chunk(st, col0 + 32 * c, sum[c]);
+      } else {
+        if (steps > 0 && !acc_ready()) break;
+#pragma unroll 1
+        for (int c = 0; c < kTcN / 2; c += 32) {
+          float v[32];
+          if (steps == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          } else {
+            tc_load32(src0 + buf * kTcN + c, v);
+          }
+          epi.chunk(st, col0 + c, v);
+        }
+        if (steps > 0) acc_done();
       }
       epi.end(st);
     }
@@ -340,6 +454,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
   if (warp == kTcEpiWarps + 1) tc_free(tmem, 2 * kTcN);
 }
