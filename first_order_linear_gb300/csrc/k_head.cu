@@ -34,6 +34,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
 
+// most pieces of the vocabulary that head_few_kernel leaves statistics of
+constexpr int kFewCtasPerSm = 2;
+int64_t few_pieces(int sm_count) { return kFewCtasPerSm * (int64_t)sm_count; }
+
 struct HeadPlan {
   int planes;       // bfloat16 planes of an operand
   bool packed;      // the weight is packed
@@ -83,7 +87,8 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
         1, std::min({(int64_t)sm_count / out_tiles, 1 + kSplitBytes / out_bytes, div_up(p.piece, kTcK)}));
     p.dh = take((size_t)p.splits * out_bytes);
   } else {
-    p.part = take((size_t)tiles * 2 * p.Np * sizeof(float4));
+    // (head_few_kernel: one piece a CTA, of at most 8 rows)
+    p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 8) * sizeof(float4));
     p.taken = take((size_t)p.Np * 4);
   }
   p.bytes = at;
@@ -115,60 +120,9 @@ struct HeadView {  // the workspace's arrays on the device
   }
 };
 
-// Numbers the rows that take part, in order (one CTA: a running count over
-// blocks of rows), and clears the results of those that do not.
-constexpr int kRowsThreads = 1024;
-__global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(HeadArgs a, HeadView w) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ int warps[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int base = 0;
-  for (int64_t i0 = 0; i0 < a.N; i0 += kRowsThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const int tok = i < a.N ? a.tokens[i] : -1;
-    const bool on = tok >= 0 && tok < a.V;
-    const unsigned vote = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) warps[warp] = __popc(vote);
-    __syncthreads();
-    int before = base, total = base;
-    for (int k = 0; k < 32; ++k) {
-      before += k < warp ? warps[k] : 0;
-      total += warps[k];
-    }
-    if (on) {
-      const int at = before + __popc(vote & ((1u << lane) - 1u));
-      w.rows[at] = (int)i;
-      w.tok[at] = tok;
-      if (a.d_logp != nullptr)
-        w.info[at] = make_float4(a.d_logp[i], a.d_entropy ? a.d_entropy[i] : 0.f, a.in_lse[i],
-                                 a.d_entropy ? a.in_entropy[i] : 0.f);
-    }
-    if (!on && i < a.N && a.logp != nullptr) {
-      a.logp[i] = 0.f;
-      a.lse[i] = 0.f;
-      if (a.entropy) a.entropy[i] = 0.f;
-    }
-    base = total;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) w.count[0] = base;
-}
-
 // ---------------------------------------------------------------------------
-// Packing: rows of 8-element groups, zeros past the width and from row
-// `valid` to the next whole tile.
+// Packing
 // ---------------------------------------------------------------------------
-constexpr int kPackThreads = 256;
-
-struct PackArgs {
-  const float* src;  // element type by the kernel
-  const int* map;    // row of src, or null: r0 + r
-  const int* valid;  // rows that exist, or null: `rows`
-  int64_t r0, rows, width, stride;
-  void* dst;  // planes x [dst_rows, pitch]
-  int64_t pitch, dst_rows;
-};
 
 // v as the sum of three bfloat16 values, each the rounding of the remainder:
 // exact to 24 bits (the remainders are exact in float32)
@@ -179,46 +133,155 @@ __device__ __forceinline__ void split3(float v, float& hi, float& mid, float& lo
   lo = r - mid;
 }
 
+// eight elements from column c of a row that starts at element `at`, zeros
+// from `width` on
+template <class ST>
+__device__ __forceinline__ void load8(const float* src, int64_t at, int64_t c, int64_t width, bool vec, float (&v)[8]) {
+  if (vec && c + 8 <= width) {
+    if constexpr (Stor<ST>::kBytes == 2) {
+      Stor<ST>::ld8(src, at + c, true, v);
+    } else {
+      Stor<ST>::ld4(src, at + c, true, v);
+      Stor<ST>::ld4(src, at + c + 4, true, v + 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < width ? Stor<ST>::ld(src, at + c + i) : 0.f;
+  }
+}
+
+// ... to element `to` of the packed planes, `plane` elements apart
+template <class ST>
+__device__ __forceinline__ void pack8(void* planes, int64_t to, int64_t plane, const float (&v)[8]) {
+  float* dst = static_cast<float*>(planes);  // Stor<bf16> counts in elements of two bytes
+  if constexpr (Stor<ST>::kBytes == 2) {
+    Stor<bf16>::st8(dst, to, v);
+  } else {
+    float h[8], m[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split3(v[i], h[i], m[i], l[i]);
+    Stor<bf16>::st8(dst, to, h);
+    Stor<bf16>::st8(dst, to + plane, m);
+    Stor<bf16>::st8(dst, to + 2 * plane, l);
+  }
+}
+
+template <class ST>
+__device__ __forceinline__ bool rows_of_vectors(const float* p, int64_t stride) {
+  return ((uintptr_t)p & 15) == 0 && (stride * Stor<ST>::kBytes) % 16 == 0;
+}
+
+constexpr int kPackThreads = 256;
+
+// Numbers the rows that take part, in order, gathers their tokens and factors,
+// packs their hidden rows, and clears the results of the other rows.  A CTA
+// takes rows_per_cta rows and counts the parts before them (and in all) by
+// itself: N tokens from L2 instead of a pass of its own and a wait.  With
+// pad, the packed rows are zeroed to the next whole stage of k: the gradient's
+// product over parts reads them.
+template <class ST>
+__global__ void __launch_bounds__(kPackThreads)
+    head_begin_kernel(HeadArgs a, HeadView w, int64_t rows_per_cta, int64_t Dp, int64_t Np, bool pad) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ int scratch[32], list[kPackThreads];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r0 = blockIdx.x * rows_per_cta, r1 = min(a.N, r0 + rows_per_cta);
+  int before = 0, all = 0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < a.N; i += kPackThreads) {
+    const int on = (unsigned)__ldg(a.tokens + i) < (unsigned)a.V;
+    all += on;
+    before += i < r0 ? on : 0;
+  }
+  before = cta_sum(before, scratch);
+  all = cta_sum(all, scratch);
+  if (blockIdx.x == 0 && threadIdx.x == 0) w.count[0] = all;
+
+  const int groups = (int)(Dp / 8);
+  const int64_t plane = Np * Dp;
+  const bool vec = rows_of_vectors<ST>(a.hidden, a.hidden_stride);
+  for (int64_t i0 = r0; i0 < r1; i0 += kPackThreads) {
+    const int64_t i = i0 + threadIdx.x;
+    const int tok = i < r1 ? a.tokens[i] : -1;
+    const bool on = (unsigned)tok < (unsigned)a.V;
+    const unsigned vote = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) scratch[warp] = __popc(vote);
+    __syncthreads();
+    int at = __popc(vote & ((1u << lane) - 1u)), n = 0;
+#pragma unroll
+    for (int k = 0; k < kPackThreads / 32; ++k) {
+      at += k < warp ? scratch[k] : 0;
+      n += scratch[k];
+    }
+    if (on) {
+      list[at] = (int)i;
+      w.rows[before + at] = (int)i;
+      w.tok[before + at] = tok;
+      if (a.d_logp != nullptr)
+        w.info[before + at] = make_float4(a.d_logp[i], a.d_entropy ? a.d_entropy[i] : 0.f, a.in_lse[i],
+                                          a.d_entropy ? a.in_entropy[i] : 0.f);
+    } else if (i < r1 && a.logp != nullptr) {
+      a.logp[i] = 0.f;
+      a.lse[i] = 0.f;
+      if (a.entropy) a.entropy[i] = 0.f;
+    }
+    __syncthreads();
+    constexpr int B = 4;  // groups a thread has in flight
+    for (int t0 = threadIdx.x; t0 < n * groups; t0 += B * kPackThreads) {
+      float v[B][8];
+      int64_t to[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const int t = min(t0 + u * kPackThreads, n * groups - 1);
+        const int r = t / groups, c = (t - r * groups) * 8;
+        load8<ST>(a.hidden, list[r] * a.hidden_stride, c, a.D, vec, v[u]);
+        to[u] = (int64_t)(before + r) * Dp + c;
+      }
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+        if (t0 + u * kPackThreads < n * groups) pack8<ST>(w.hidden, to[u], plane, v[u]);
+    }
+    before += n;
+    __syncthreads();
+  }
+  if (!pad) return;
+  const int64_t end = min(Np, ((int64_t)all + kTcK - 1) / kTcK * kTcK);
+  for (int64_t r = all + blockIdx.x; r < end; r += gridDim.x)
+    for (int c = threadIdx.x; c < groups; c += kPackThreads) {
+      const float v[8] = {};
+      pack8<ST>(w.hidden, r * Dp + c * 8, plane, v);
+    }
+}
+
+// the weight's rows [r0, r0 + rows) packed, zeros past the width
+struct PackArgs {
+  const float* src;
+  int64_t r0, rows, width, stride;
+  void* dst;  // planes x [dst_rows, pitch]
+  int64_t pitch, dst_rows;
+};
 template <class ST>
 __global__ void __launch_bounds__(kPackThreads) head_pack_kernel(PackArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int64_t groups = a.pitch / 8;
-  const int64_t valid = a.valid ? min((int64_t)*a.valid, a.rows) : a.rows;
-  const int64_t rows = min(a.dst_rows, (valid + kTcM - 1) / kTcM * kTcM);
-  const bool vec = ((uintptr_t)a.src & 15) == 0 && (a.stride * Stor<ST>::kBytes) % 16 == 0;
-  for (int64_t t = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; t < rows * groups;
-       t += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t r = t / groups, c = (t % groups) * 8;
-    float v[8];
-    if (r < valid && vec && c + 8 <= a.width) {
-      const int64_t at = (a.map ? (int64_t)a.map[r] : a.r0 + r) * a.stride + c;
-      if constexpr (Stor<ST>::kBytes == 2) {
-        Stor<ST>::ld8(a.src, at, true, v);
-      } else {
-        float (&lo)[4] = reinterpret_cast<float (&)[4]>(v[0]);
-        float (&hi)[4] = reinterpret_cast<float (&)[4]>(v[4]);
-        Stor<ST>::ld4(a.src, at, true, lo);
-        Stor<ST>::ld4(a.src, at + 4, true, hi);
-      }
-    } else {
-      const int64_t at = r < valid ? (a.map ? (int64_t)a.map[r] : a.r0 + r) * a.stride : 0;
+  const uint32_t groups = (uint32_t)(a.pitch / 8);
+  const bool vec = rows_of_vectors<ST>(a.src, a.stride);
+  constexpr int B = 4;
+  const int64_t total = a.rows * groups, step = (int64_t)gridDim.x * kPackThreads;
+  for (int64_t t0 = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; t0 < total; t0 += B * step) {
+    float v[B][8];
+    int64_t to[B];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r < valid && c + i < a.width ? Stor<ST>::ld(a.src, at + c + i) : 0.f;
+    for (int u = 0; u < B; ++u) {
+      const int64_t t = min(t0 + u * step, total - 1);
+      const int64_t r = t / groups, c = (t - r * groups) * 8;
+      load8<ST>(a.src, (a.r0 + r) * a.stride, c, a.width, vec, v[u]);
+      to[u] = r * a.pitch + c;
     }
-    float* dst = static_cast<float*>(a.dst);  // Stor<bf16> counts in elements of two bytes
-    const int64_t to = r * a.pitch + c;
-    if constexpr (Stor<ST>::kBytes == 2) {
-      Stor<bf16>::st8(dst, to, v);
-    } else {
-      float h[8], m[8], l[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split3(v[i], h[i], m[i], l[i]);
-      const int64_t plane = a.dst_rows * a.pitch;
-      Stor<bf16>::st8(dst, to, h);
-      Stor<bf16>::st8(dst, to + plane, m);
-      Stor<bf16>::st8(dst, to + 2 * plane, l);
-    }
+    for (int u = 0; u < B; ++u)
+      if (t0 + u * step < total) pack8<ST>(a.dst, to[u], a.dst_rows * a.pitch, v[u]);
   }
 }
 
@@ -229,6 +292,44 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// two float32 values in one 64-bit register: one instruction for both
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void pair_open(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 32 bytes at p (32-byte aligned): a whole sector from one thread
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// sixteen values as bfloat16
+__device__ __forceinline__ void store16(uint16_t* p, const float* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = Stor<bf16>::pack2(v[2 * i], v[2 * i + 1]);
+  store32(p, w);
 }
 
 // part[half tile][part] = (max of acc, sum e, sum e acc) with
@@ -261,20 +362,28 @@ struct StatsEpi {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : -3.402823466e38f;
     }
-    float top = v[0];
+    float top = st.top;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-    top = fmaxf(top, st.top);
-    // the first chunk: 2^-inf = 0 drops the empty sums (kept off inf - inf)
+    for (int i = 0; i < 32; i += 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(v[i]), "f"(v[i + 1]));
+    // the first chunk: 0 drops the empty sums (kept off inf - inf)
     const float f = st.top == -INFINITY ? 0.f : exp2_approx((st.top - top) * c2);
-    float s = st.s * f, t = st.t * f;
     const float off = -top * c2;
+    const uint64_t c22 = pair_of(c2, c2), off2 = pair_of(off, off);
+    uint64_t s2 = pair_of(st.s * f, 0.f), t2 = pair_of(st.t * f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float e = exp2_approx(fmaf(v[i], c2, off));
-      s += e;
-      t = fmaf(e, v[i], t);
+    for (int i = 0; i < 32; i += 2) {
+      const uint64_t z = pair_of(v[i], v[i + 1]);
+      float x0, x1;
+      pair_open(pair_fma(z, c22, off2), x0, x1);
+      const uint64_t e = pair_of(exp2_approx(x0), exp2_approx(x1));
+      s2 = pair_add(s2, e);
+      t2 = pair_fma(e, z, t2);
     }
+    float s, t, hi;
+    pair_open(s2, s, hi);
+    s += hi;
+    pair_open(t2, t, hi);
+    t += hi;
     st.top = top;
     st.s = s;
     st.t = t;
@@ -290,11 +399,6 @@ struct StatsEpi {
     if (st.live) part[(int64_t)((v0 + st.col0) / (kTcN / 2)) * Np + st.m] = make_float4(st.top, st.s, st.t, 0.f);
   }
 };
-
-// eight values as bfloat16 at p (16-byte aligned)
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  Stor<bf16>::st8(reinterpret_cast<float*>(p), 0, v);
-}
 
 // dz = p (a0 + a1 acc), plus g / temperature for the token taken, as one
 // bfloat16 (rounded once: the two products that read it run on bfloat16) or
@@ -331,27 +435,36 @@ struct DzEpi {
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
     const float c2 = inv_t * kLog2e;
     const int k = st.at - col;
+    const uint64_t c22 = pair_of(c2, c2), l2 = pair_of(st.lse2, st.lse2);
+    const uint64_t a02 = pair_of(st.a0, st.a0), a12 = pair_of(st.a1, st.a1);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float p = exp2_approx(fmaf(v[i], c2, st.lse2));
-      v[i] = st.live ? p * fmaf(st.a1, v[i], st.a0) : 0.f;
+    for (int i = 0; i < 32; i += 2) {
+      const uint64_t z = pair_of(v[i], v[i + 1]);
+      float x0, x1;
+      pair_open(pair_fma(z, c22, l2), x0, x1);
+      const uint64_t p = pair_of(exp2_approx(x0), exp2_approx(x1));
+      pair_open(pair_mul(p, pair_fma(a12, z, a02)), v[i], v[i + 1]);
     }
     if (k >= 0 && k < 32) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += i == k ? st.g : 0.f;
     }
-    if constexpr (PLANES == 1) {
+    if (!st.live) {  // whatever the packed row holds
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) store8(st.row + col + i, v + i);
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    }
+    if constexpr (PLANES == 1) {
+      store16(st.row + col, v);
+      store16(st.row + col + 16, v + 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        float h[8], m[8], l[8];
+      for (int i = 0; i < 32; i += 16) {
+        float h[16], m[16], l[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split3(v[i + j], h[j], m[j], l[j]);
-        store8(st.row + col + i, h);
-        store8(st.row + plane + col + i, m);
-        store8(st.row + 2 * plane + col + i, l);
+        for (int j = 0; j < 16; ++j) split3(v[i + j], h[j], m[j], l[j]);
+        store16(st.row + col + i, h);
+        store16(st.row + plane + col + i, m);
+        store16(st.row + 2 * plane + col + i, l);
       }
     }
   }
@@ -375,14 +488,17 @@ struct SumEpi {
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
     if (!st.live || col >= pitch) return;
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      float4* p = reinterpret_cast<float4*>(st.row + col + i);
-      float4 r = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int i = 0; i < 32; i += 8) {
+      uint32_t r[8];
       if (add) {
-        const float4 o = *p;
-        r.x += o.x, r.y += o.y, r.z += o.z, r.w += o.w;
+        const float4* o = reinterpret_cast<const float4*>(st.row + col + i);
+        const float4 lo = o[0], hi = o[1];
+        v[i] += lo.x, v[i + 1] += lo.y, v[i + 2] += lo.z, v[i + 3] += lo.w;
+        v[i + 4] += hi.x, v[i + 5] += hi.y, v[i + 6] += hi.z, v[i + 7] += hi.w;
       }
-      *p = r;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
+      store32(st.row + col + i, r);
     }
   }
   __device__ __forceinline__ void end(State&) const {}
@@ -393,7 +509,7 @@ template <class ST>
 struct OutEpi {
   float* out;  // [.., width], element type ST
   int64_t row0, width;
-  bool vec;  // rows start on 16-byte boundaries
+  bool vec, vec16;  // rows start on 32-byte, on 16-byte boundaries
 
   struct State {
     int64_t at;
@@ -406,17 +522,32 @@ struct OutEpi {
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
     if (!st.live) return;
     if (vec && col + 32 <= width) {
+      unsigned char* p = reinterpret_cast<unsigned char*>(out) + (st.at + col) * Stor<ST>::kBytes;
       if constexpr (Stor<ST>::kBytes == 2) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) Stor<ST>::st8(out, st.at + col + i, v + i);
+        store16(reinterpret_cast<uint16_t*>(p), v);
+        store16(reinterpret_cast<uint16_t*>(p) + 16, v + 16);
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) Stor<ST>::st4(out, st.at + col + i, v + i);
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t r[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
+          store32(p + 4 * i, r);
+        }
       }
     } else {
+      constexpr int E = 16 / Stor<ST>::kBytes;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < width) Stor<ST>::st(out, st.at + col + i, v[i]);
+      for (int i = 0; i < 32; i += E) {
+        if (vec16 && col + i + E <= width) {
+          if constexpr (E == 8) Stor<ST>::st8(out, st.at + col + i, v + i);
+          else Stor<ST>::st4(out, st.at + col + i, v + i);
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (col + i + j < width) Stor<ST>::st(out, st.at + col + i + j, v[i + j]);
+        }
+      }
     }
   }
   __device__ __forceinline__ void end(State&) const {}
@@ -425,53 +556,240 @@ struct OutEpi {
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-// joins a part's half tiles, one warp a part
-__global__ void __launch_bounds__(kJoinThreads)
-    head_join_kernel(HeadArgs a, HeadView w, int64_t halves, int64_t Np, float c2) {
-  pdl_trigger();
-  pdl_wait();
-  const int64_t m = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (m >= w.count[0]) return;
-  float top = -INFINITY;
-  for (int64_t k = lane; k < halves; k += 32) top = fmaxf(top, w.part[k * Np + m].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float s = 0.f, t = 0.f;
-  for (int64_t k = lane; k < halves; k += 32) {
-    const float4 p = w.part[k * Np + m];
-    const float f = exp2_approx((p.x - top) * c2);
-    s += p.y * f;
-    t += p.z * f;
+// partial statistics over some of a part's tokens: the largest value z (before
+// the temperature), the sum of e = 2^(c2 (z - top)), the sum of e z
+struct Stats {
+  float top, s, t;
+  __device__ __forceinline__ void add(float top2, float s2, float t2, float c2) {
+    if (s2 == 0.f) return;  // none
+    const float m = fmaxf(top, top2);
+    const float f = s == 0.f ? 0.f : exp2_approx((top - m) * c2), f2 = exp2_approx((top2 - m) * c2);
+    s = fmaf(s, f, s2 * f2);
+    t = fmaf(t, f, t2 * f2);
+    top = m;
   }
-  s = warp_sum(s);
-  t = warp_sum(t);
-  if (lane != 0) return;
-  const float inv_t = a.inv_temperature;
-  const float log_s = logf(s);
-  const int64_t i = w.rows[m];
-  a.lse[i] = fmaf(top, inv_t, log_s);
-  a.logp[i] = fmaf(w.taken[m] - top, inv_t, -log_s);
-  if (a.entropy) a.entropy[i] = fmaf(top - t / s, inv_t, log_s);
+};
+
+// the results of part m, from all its statistics
+__device__ __forceinline__ void finish(const HeadArgs& a, const HeadView& w, int64_t m, int64_t row, const Stats& st) {
+  const float inv_t = a.inv_temperature, log_s = logf(st.s);
+  a.lse[row] = fmaf(st.top, inv_t, log_s);
+  a.logp[row] = fmaf(w.taken[m] - st.top, inv_t, -log_s);
+  if (a.entropy) a.entropy[row] = fmaf(st.top - st.t / st.s, inv_t, log_s);
 }
 
-// d_hidden: the parts' rows rounded once, zeros for rows that take no part
-template <class ST>
-__global__ void __launch_bounds__(kJoinThreads) head_dh_out_kernel(HeadArgs a, HeadView w, int64_t Dh, int64_t plane, int splits) {
+// Joins the statistics of `pieces` pieces of the vocabulary: 32 parts a CTA,
+// neighbouring lanes on neighbouring parts; warp k takes the pieces k, k + 32,
+// ... four at a time, and the warps' results are joined in order.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    head_join_kernel(HeadArgs a, HeadView w, int64_t pieces, int64_t pitch, float c2) {
   pdl_trigger();
   pdl_wait();
-  const int64_t b = blockIdx.x;
-  if (b < w.count[0]) {
-    const int64_t row = w.rows[b];
-    for (int64_t c = threadIdx.x; c < a.D; c += kJoinThreads) {
-      float v = w.dh[b * Dh + c];
-      for (int k = 1; k < splits; ++k) v += w.dh[k * plane + b * Dh + c];
-      Stor<ST>::st(a.d_hidden, row * a.D + c, v);
+  __shared__ Stats acc[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
+  if ((int64_t)blockIdx.x * 32 >= w.count[0]) return;
+  const bool on = m < w.count[0];
+  Stats st = {-INFINITY, 0.f, 0.f};
+  if (on) {
+    for (int64_t k = warp; k < pieces; k += 4 * kJoinWarps) {
+      float4 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        p[u] = k + u * kJoinWarps < pieces ? __ldg(w.part + (k + u * kJoinWarps) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) st.add(p[u].x, p[u].y, p[u].z, c2);
     }
   }
-  const int tok = a.tokens[b];
-  if (tok < 0 || tok >= a.V)
-    for (int64_t c = threadIdx.x; c < a.D; c += kJoinThreads) Stor<ST>::st(a.d_hidden, b * a.D + c, 0.f);
+  acc[warp][lane] = st;
+  __syncthreads();
+  if (warp != 0 || !on) return;
+  for (int k = 1; k < kJoinWarps; ++k) st.add(acc[k][lane].top, acc[k][lane].s, acc[k][lane].t, c2);
+  finish(a, w, m, w.rows[m], st);
+}
+
+// ... with few parts: one CTA a part, its threads on the pieces.  identity:
+// part m is row m, whether it takes part or not.
+__global__ void __launch_bounds__(kJoinThreads)
+    head_join_few_kernel(HeadArgs a, HeadView w, int64_t pieces, int64_t pitch, float c2, bool identity) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int W = kJoinThreads / 32;
+  __shared__ Stats acc[W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t m = blockIdx.x;
+  if (!identity && m >= w.count[0]) return;
+  Stats st = {-INFINITY, 0.f, 0.f};
+  for (int64_t k = threadIdx.x; k < pieces; k += 4 * kJoinThreads) {
+    float4 p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      p[u] = k + u * kJoinThreads < pieces ? __ldg(w.part + (k + u * kJoinThreads) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) st.add(p[u].x, p[u].y, p[u].z, c2);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float top = __shfl_xor_sync(0xffffffffu, st.top, o), s = __shfl_xor_sync(0xffffffffu, st.s, o),
+                t = __shfl_xor_sync(0xffffffffu, st.t, o);
+    st.add(top, s, t, c2);
+  }
+  if (lane == 0) acc[warp] = st;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int k = 1; k < W; ++k) st.add(acc[k].top, acc[k].s, acc[k].t, c2);
+  const int64_t row = identity ? m : w.rows[m];
+  const bool on = (unsigned)a.tokens[row] < (unsigned)a.V;
+  if (on) {
+    finish(a, w, m, row, st);
+  } else {
+    a.lse[row] = a.logp[row] = 0.f;
+    if (a.entropy) a.entropy[row] = 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// A few rows (serving: one new token a sequence).  The weight is read once at
+// the rate of HBM, so nothing is to be gained from the tensor cores, whose
+// tiles of 256 rows would be almost empty: each warp forms the logits of R
+// tokens x NT rows at a time in float32, its lanes side by side on the width,
+// the hidden rows in shared memory.  The 32-lane sums of the R x NT logits
+// share their shuffles (each step halves the values a lane carries), which
+// leaves each lane with one logit, whose running statistics it keeps.
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 256;
+constexpr int kFewTokens = 4;  // R
+constexpr size_t kFewSmem = 96 * 1024;
+
+template <class ST, int VE, int NT>
+__global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
+    head_few_kernel(HeadArgs a, HeadView w, int64_t Ds, float c2) {
+  extern __shared__ __align__(16) float few_hidden[];  // [NT][Ds], zeros past D
+  constexpr int R = kFewTokens, C = R * NT, W = kFewThreads / 32;
+  constexpr int kLog = C == 4 ? 2 : C == 8 ? 3 : C == 16 ? 4 : 5;  // log2 C
+  __shared__ Stats acc[W][C];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t t = threadIdx.x; t < NT * Ds; t += kFewThreads) {
+    const int64_t r = t / Ds, c = t - r * Ds;
+    few_hidden[t] = r < a.N && c < a.D ? Stor<ST>::ld(a.hidden, r * a.hidden_stride + c) : 0.f;
+  }
+  __syncthreads();
+  const int mine = lane >> (5 - kLog);           // the logit this lane ends up with:
+  const int my_tok = mine / NT, my_row = mine % NT;  // token my_tok of the R, row my_row
+  const int64_t taken_tok = my_row < a.N ? a.tokens[my_row] : -1;
+  Stats st = {-INFINITY, 0.f, 0.f};
+  const int64_t nv = a.D / VE;
+  for (int64_t v0 = ((int64_t)blockIdx.x * W + warp) * R; v0 < a.V; v0 += (int64_t)gridDim.x * W * R) {
+    float z[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) z[i] = 0.f;
+    const float* base[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      base[r] = reinterpret_cast<const float*>(reinterpret_cast<const unsigned char*>(a.weight) +
+                                               min(v0 + r, a.V - 1) * a.weight_stride * Stor<ST>::kBytes);
+#pragma unroll (NT <= 2 ? 4 : 2)
+    for (int64_t j = lane; j < nv; j += 32) {
+      float x[R][VE];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if constexpr (VE == 8) Stor<ST>::ld8(base[r], j * VE, true, x[r]);
+        else if constexpr (VE == 4) Stor<ST>::ld4(base[r], j * VE, true, x[r]);
+        else x[r][0] = Stor<ST>::ld(base[r], j);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float h[VE];
+        if constexpr (VE >= 4) {
+#pragma unroll
+          for (int e = 0; e < VE; e += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(few_hidden + n * Ds + j * VE + e);
+            h[e] = q.x, h[e + 1] = q.y, h[e + 2] = q.z, h[e + 3] = q.w;
+          }
+        } else {
+          h[0] = few_hidden[n * Ds + j];
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) z[r * NT + n] = fmaf(x[r][e], h[e], z[r * NT + n]);
+      }
+    }
+    int n = C;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (n > 1) {
+        n /= 2;
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i)
+          if (i < n) {
+            const float give = up ? z[i] : z[i + n], keep = up ? z[i + n] : z[i];
+            z[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+      } else {
+        z[0] += __shfl_xor_sync(0xffffffffu, z[0], o);
+      }
+    }
+    if (v0 + my_tok < a.V) {
+      st.add(z[0], 1.f, z[0], c2);
+      if (v0 + my_tok == taken_tok && (lane & ((32 >> kLog) - 1)) == 0) w.taken[my_row] = z[0];
+    }
+  }
+  if ((lane & ((32 >> kLog) - 1)) == 0) acc[warp][mine] = st;
+  __syncthreads();
+  if (threadIdx.x < NT) {
+    Stats all = {-INFINITY, 0.f, 0.f};
+    for (int k = 0; k < W; ++k)
+      for (int r = 0; r < R; ++r) {
+        const Stats& q = acc[k][r * NT + threadIdx.x];
+        all.add(q.top, q.s, q.t, c2);
+      }
+    w.part[(int64_t)blockIdx.x * NT + threadIdx.x] = make_float4(all.top, all.s, all.t, 0.f);
+  }
+}
+
+// d_hidden: the splits' sums in order, rounded once; zeros for rows that take
+// no part.  One thread four columns of part b and of row b.
+template <class ST>
+__global__ void __launch_bounds__(kJoinThreads)
+    head_dh_out_kernel(HeadArgs a, HeadView w, int64_t Dh, int64_t plane, int splits, bool vec) {
+  pdl_trigger();
+  pdl_wait();
+  const int groups = (int)((a.D + 3) / 4);
+  const int64_t parts = w.count[0];
+  for (int64_t t = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; t < a.N * groups;
+       t += (int64_t)gridDim.x * kJoinThreads) {
+    const int64_t b = t / groups, c = (t - b * groups) * 4;
+    const auto put = [&](int64_t row, const float4& v) {
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      if (vec) {
+        Stor<ST>::st4(a.d_hidden, row * a.D + c, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < a.D) Stor<ST>::st(a.d_hidden, row * a.D + c + i, f[i]);
+      }
+    };
+    if (b < parts) {
+      const float* src = w.dh + b * Dh + c;
+      float4 v = *reinterpret_cast<const float4*>(src);
+      for (int k0 = 1; k0 < splits; k0 += 8) {
+        float4 q[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          q[u] = k0 + u < splits ? *reinterpret_cast<const float4*>(src + (k0 + u) * plane) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v.x += q[u].x, v.y += q[u].y, v.z += q[u].z, v.w += q[u].w;
+      }
+      put(w.rows[b], v);
+    }
+    if ((unsigned)a.tokens[b] >= (unsigned)a.V) put(b, make_float4(0.f, 0.f, 0.f, 0.f));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -488,12 +806,32 @@ TcTerms terms_of(int planes) {
   return t;
 }
 
+// Rows that head_few_kernel takes: up to 8, if their float32 copies fit two
+// CTAs' shared memory an SM.
+bool few(int64_t N, int64_t D) {
+  const int64_t nt = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;
+  return N <= 8 && (size_t)(nt * round_up(D, 4) * 4) <= kFewSmem;
+}
+int64_t few_grid(int64_t V, int sm_count) {
+  return std::min<int64_t>(div_up(V, kFewTokens * (kFewThreads / 32)), few_pieces(sm_count));
+}
+
 template <bool A_MN, bool B_MN, int GROUP, class Epi>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const TcShape& s, const Epi& epi, int sm_count,
                            cudaStream_t st) {
   const auto kernel = tc_product_kernel<A_MN, B_MN, GROUP, Epi>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
   if (e != cudaSuccess) return e;
+  if (GROUP > 0) {
+    // the warpgroups' register shares are taken from the launch's registers:
+    // a kernel built with fewer would wait for the rest for ever
+    static const bool enough = [&] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
+             f.numRegs * kTcThreads >= 32 * (kTcEpiWarps * kTcEpiRegs + 4 * kTcIssueRegs);
+    }();
+    if (!enough) return cudaErrorInvalidConfiguration;
+  }
   const int64_t tiles = div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits;
   return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, ma, mb, s, epi);
 }
@@ -511,7 +849,10 @@ bool in_place(const HeadArgs& a) {
 // Stages summed by the tensor cores alone (tc.cuh): 512 values of k for
 // results that leave in float32; the bfloat16 gradients' own rounding is
 // larger than the whole sum's error.
-constexpr int kLogitsGroup = 8;
+#ifndef TCG
+#define TCG 8
+#endif
+constexpr int kLogitsGroup = TCG;
 
 template <class ST>
 struct HeadRun {
@@ -531,24 +872,17 @@ struct HeadRun {
     if (!encode_matrix_map(&hidden_k, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcRows) ||
         !encode_matrix_map(&hidden_mn, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcK))
       return cudaErrorNotSupported;
-    cudaError_t e = launch_pdl(head_rows_kernel, 1, kRowsThreads, 0, s, a, w);
-    if (e != cudaSuccess) return e;
-    PackArgs k = {};
-    k.src = a.hidden; k.map = w.rows; k.valid = w.count; k.rows = a.N; k.width = a.D; k.stride = a.hidden_stride;
-    k.dst = w.hidden; k.pitch = p.Dp; k.dst_rows = p.Np;
-    return pack(k);
+    const int64_t rows_per_cta = std::max<int64_t>(2, div_up(a.N, 2 * (int64_t)sm));
+    return launch_pdl(head_begin_kernel<ST>, div_up(a.N, rows_per_cta), kPackThreads, 0, s, a, w, rows_per_cta, p.Dp,
+                      p.Np, a.d_logp != nullptr);
   }
-  cudaError_t pack(const PackArgs& k) {
-    const int64_t grid = std::min<int64_t>(div_up(k.dst_rows * (k.pitch / 8), kPackThreads), 8 * (int64_t)sm);
-    return launch_pdl(head_pack_kernel<ST>, grid, kPackThreads, 0, s, k);
-  }
-  // the weight's rows from v0 on, as an operand with boxes of box_rows; rows and columns of it in *y0
+  // the weight's rows from v0 on, packed where the copies cannot read them in place
   cudaError_t weight_piece(int64_t v0, int64_t len) {
     if (!p.packed) return cudaSuccess;
     PackArgs k = {};
     k.src = a.weight; k.r0 = v0; k.rows = len; k.width = a.D; k.stride = a.weight_stride;
     k.dst = w.weight; k.pitch = p.Dp; k.dst_rows = p.pitch;
-    return pack(k);
+    return launch_pdl(head_pack_kernel<ST>, std::min<int64_t>(div_up(len * (p.Dp / 8), 4 * kPackThreads), 8 * (int64_t)sm), kPackThreads, 0, s, k);
   }
   bool weight_map(CUtensorMap* m, int64_t len, int box_rows) {
     if (p.packed) return encode_matrix_map(m, w.weight, p.Dp, len, p.planes, p.Dp, p.pitch * p.Dp, box_rows);
@@ -575,10 +909,35 @@ struct HeadRun {
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, (int)v0, (int)(v0 + len), c2};
       e = launch_product<false, false, kLogitsGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
     }
-    if (e == cudaSuccess)
-      e = launch_pdl(head_join_kernel, div_up(a.N, kJoinThreads / 32), kJoinThreads, 0, s, a, w, div_up(a.V, kTcN) * 2,
-                     p.Np, c2);
-    return e;
+    return e == cudaSuccess ? join(div_up(a.V, kTcN) * 2, p.Np, false) : e;
+  }
+  // (at few parts, few CTAs would run the whole column of pieces each)
+  cudaError_t join(int64_t pieces, int64_t pitch, bool identity) {
+    const float c2 = a.inv_temperature * kLog2e;
+    if (identity || a.N <= 256)
+      return launch_pdl(head_join_few_kernel, a.N, kJoinThreads, 0, s, a, w, pieces, pitch, c2, identity);
+    return launch_pdl(head_join_kernel, div_up(a.N, 32), 32 * kJoinWarps, 0, s, a, w, pieces, pitch, c2);
+  }
+
+  template <int VE, int NT>
+  cudaError_t few_rows() {
+    const auto kernel = head_few_kernel<ST, VE, NT>;
+    const int64_t Ds = round_up(a.D, 4);
+    const size_t smem = (size_t)NT * Ds * 4;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = few_grid(a.V, sm);
+    e = launch_pdl(kernel, grid, kFewThreads, smem, s, a, w, Ds, a.inv_temperature * kLog2e);
+    return e == cudaSuccess ? join(grid, NT, true) : e;
+  }
+  template <int VE>
+  cudaError_t few_rows() {
+    return a.N <= 1 ? few_rows<VE, 1>() : a.N <= 2 ? few_rows<VE, 2>() : a.N <= 4 ? few_rows<VE, 4>() : few_rows<VE, 8>();
+  }
+  cudaError_t forward_few() {
+    constexpr int VE = 16 / Stor<ST>::kBytes;
+    const bool vec = ((uintptr_t)a.weight & 15) == 0 && (a.weight_stride * Stor<ST>::kBytes) % 16 == 0 && a.D % VE == 0;
+    return vec ? few_rows<VE>() : few_rows<1>();
   }
 
   cudaError_t backward() {
@@ -613,12 +972,15 @@ struct HeadRun {
         t.count = w.count; t.count_axis = 2;
         t.m = (int)len; t.n = (int)a.D; t.k = (int)a.N;
         t.splits = 1; t.band = 16; t.terms = terms;
-        const bool vec = (a.D * Stor<ST>::kBytes) % 16 == 0 && ((uintptr_t)a.d_weight & 15) == 0;
-        e = launch_product<true, true, kGradGroup>(dz_mn, hidden_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, vec}, sm, s);
+        const uintptr_t rows = (uintptr_t)a.d_weight | (uintptr_t)(a.D * Stor<ST>::kBytes);
+        e = launch_product<true, true, kGradGroup>(dz_mn, hidden_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, rows % 32 == 0, rows % 16 == 0}, sm, s);
       }
     }
-    if (e == cudaSuccess && a.d_hidden)
-      e = launch_pdl(head_dh_out_kernel<ST>, a.N, kJoinThreads, 0, s, a, w, p.Dh, dh_plane, p.splits);
+    if (e == cudaSuccess && a.d_hidden) {
+      const bool vec = a.D % 4 == 0 && ((uintptr_t)a.d_hidden & 15) == 0;
+      const int64_t grid = std::min<int64_t>(div_up(a.N * div_up(a.D, 4), kJoinThreads), 16 * (int64_t)sm);
+      e = launch_pdl(head_dh_out_kernel<ST>, grid, kJoinThreads, 0, s, a, w, p.Dh, dh_plane, p.splits, vec);
+    }
     return e;
   }
 };
@@ -634,6 +996,7 @@ size_t head_workspace(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backwa
 
 cudaError_t run_token_logprob(const HeadArgs& a, int sm_count, cudaStream_t s) {
   const HeadPlan p = plan_head(a.N, a.D, a.V, a.bf16_io, false, !in_place(a), sm_count);
+  if (few(a.N, a.D)) return a.bf16_io ? HeadRun<bf16>(a, p, sm_count, s).forward_few() : HeadRun<float>(a, p, sm_count, s).forward_few();
   return a.bf16_io ? HeadRun<bf16>(a, p, sm_count, s).forward() : HeadRun<float>(a, p, sm_count, s).forward();
 }
 

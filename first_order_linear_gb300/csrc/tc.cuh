@@ -29,7 +29,7 @@
 // round (measured: the error of a sum grows with its number of k steps,
 // 1.7e-6 of a log-probability at k = 4096 against 3e-7 in plain float32).
 // GROUP > 0 therefore starts a new accumulator every GROUP stages and adds
-// the partial sums in float32 registers.
+// the partial sums in float32 registers (about 4% of the product's time).
 //
 // Every wait is bounded: a wait that gives up records the timeout in the
 // status word and raises a shared flag that ends the CTA's roles (the other
@@ -44,10 +44,17 @@ namespace rlca {
 constexpr int kTcM = 256;      // rows of a tile, half of them each CTA's
 constexpr int kTcN = 256;      // columns of a tile; each CTA copies half of B's rows
 constexpr int kTcK = 64;       // k per stage: one 128-byte swizzle row of bfloat16
-constexpr int kTcStages = 6;
+#ifndef TCS
+#define TCS 6
+#endif
+constexpr int kTcStages = TCS;
 constexpr int kTcRows = kTcM / 2;  // rows a CTA loads and finishes
 constexpr int kTcEpiWarps = 8;
-constexpr int kTcThreads = 32 * (kTcEpiWarps + 2);
+constexpr int kTcThreads = 32 * (kTcEpiWarps + 4);  // two warps idle: register shares go by four warps
+// registers a thread: 168 at launch (384 threads), then 208 for the epilogue's
+// 256 threads and 88 for the other 128 -- the same 64,512 in all
+constexpr int kTcEpiRegs = 208, kTcIssueRegs = 88;
+static_assert(32 * (kTcEpiWarps * kTcEpiRegs + 4 * kTcIssueRegs) <= 168 * kTcThreads, "shares within the launch's registers");
 constexpr int kTcABytes = kTcRows * kTcK * 2;
 constexpr int kTcBBytes = kTcN / 2 * kTcK * 2;
 constexpr int kTcStageBytes = kTcABytes + kTcBBytes;
@@ -101,22 +108,26 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// 32 columns of this warp's 32 TMEM lanes: one row a thread
+// Starts the load of 32 columns of this warp's 32 TMEM lanes (one row a
+// thread); the values are there after tc_load_wait.
 __device__ __forceinline__ void tc_load32(uint32_t addr, float (&v)[32]) {
-  uint32_t r[32];
   __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+// waits for this thread's loads so far; v passes through so that its uses stay behind the wait
+__device__ __forceinline__ void tc_load_wait(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 // ... 16 columns, added to v
@@ -153,6 +164,16 @@ template <bool A_MN, bool B_MN>
 constexpr uint32_t kTcInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
                               ((uint32_t)(kTcN >> 3) << 17) | ((uint32_t)(kTcM >> 4) << 24);
 
+// ---- registers of a warpgroup (all its warps together) -------------------------
+template <int N>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---- the two CTAs of a cluster -----------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -169,8 +190,10 @@ __device__ __forceinline__ uint32_t in_first(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
   return r;
 }
+// (what the arrival hands over is TMEM, ordered by the tcgen05 fences; a
+// release at cluster scope would wait for the epilogue's stores to memory)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // a copy into this CTA's shared memory, counted by the barrier at `bar`
@@ -183,28 +206,14 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ bool tc_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n"
-      ".reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 // a bounded wait that also ends when another role has given up
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
-  if (tc_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-      if (tc_try_wait(bar, parity)) return true;
+      if (mbar_try_wait(bar, parity)) return true;
     if (*stop) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
       atomicOr(&g_tu_status, kStatusWaitTimeout);
@@ -251,6 +260,16 @@ struct TcWalk {
   }
 };
 
+// End of the accumulation that starts at step `at` of terms x stages steps.
+// All terms but the last are at most 2^-8 of it: they share one accumulator,
+// whose dropped bits are that much smaller.
+template <int GROUP>
+__device__ __forceinline__ int tc_group_end(int at, int stages, int terms) {
+  if (GROUP == 0) return stages * terms;
+  const int lead = stages * (terms - 1);
+  return at < lead ? lead : min(at + GROUP, stages * terms);
+}
+
 // Epi: struct State; begin(State&, walk, tile, row, col0) with row = the
 // thread's row of C and col0 the first column of its half tile;
 // chunk(State&, col, v[32]) for the 32 columns from col on; end(State&).
@@ -292,8 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   const TcWalk walk(s);
 
-  if (warp == kTcEpiWarps) {
+  // (without partial sums the launch's 168 registers are enough)
+  if (warp >= kTcEpiWarps + 2) {
+    // ---- idle ----
+    if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
+  } else if (warp == kTcEpiWarps) {
     // ---- copies ----
+    if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
     if (lane == 0) {
       // operands written by earlier kernels' ordinary stores, read by copies
       asm volatile("fence.proxy.async;" ::: "memory");
@@ -346,6 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == kTcEpiWarps + 1) {
     // ---- matrix instructions ----
+    if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
     if (lane == 0 && rank == 0) {
       int stage = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
@@ -355,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const int steps = (tile.k_end - tile.k_begin) * s.terms.n;
         // (no steps: the epilogue takes zeros and waits for nothing)
         for (int at = 0; at < steps && ok;) {
-          const int group_end = GROUP > 0 ? min(at + GROUP, steps) : steps;
+          const int group_end = tc_group_end<GROUP>(at, tile.k_end - tile.k_begin, s.terms.n);
           if (!tc_wait(&acc_empty[buf], acc_phase ^ 1, &stop)) {
             ok = false;
             break;
@@ -389,6 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ---- epilogue ----
+    if constexpr (GROUP > 0) regs_take<kTcEpiRegs>();
     const int quarter = warp & 3, half = warp >> 2;
     int buf = 0;
     uint32_t acc_phase = 0;
@@ -420,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         for (int c = 0; c < kTcN / 64; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-        for (int at = 0; at < steps; at += GROUP) {
+        for (int at = 0; at < steps; at = tc_group_end<GROUP>(at, tile.k_end - tile.k_begin, s.terms.n)) {
           ok = acc_ready();
           if (!ok) break;
 #pragma unroll
@@ -435,18 +461,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         for (int c = 0; c < kTcN / 64; ++c) epi.chunk(st, col0 + 32 * c, sum[c]);
       } else {
         if (steps > 0 && !acc_ready()) break;
+        const uint32_t src = src0 + buf * kTcN;
+        float v[32], w[32];  // one is worked on while the other is loaded
+        if (steps > 0) {
+          tc_load32(src, v);
 #pragma unroll 1
-        for (int c = 0; c < kTcN / 2; c += 32) {
-          float v[32];
-          if (steps == 0) {
+          for (int c = 0; c < kTcN / 2; c += 64) {
+            tc_load_wait(v);
+            tc_load32(src + c + 32, w);
+            epi.chunk(st, col0 + c, v);
+            tc_load_wait(w);
+            if (c + 64 < kTcN / 2) tc_load32(src + c + 64, v);
+            else acc_done();
+            epi.chunk(st, col0 + c + 32, w);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kTcN / 2; c += 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          } else {
-            tc_load32(src0 + buf * kTcN + c, v);
+            epi.chunk(st, col0 + c, v);
           }
-          epi.chunk(st, col0 + c, v);
         }
-        if (steps > 0) acc_done();
       }
       epi.end(st);
     }

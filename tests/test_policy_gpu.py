@@ -140,6 +140,14 @@ def test_head(N, D, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(), dict(mask=0.5, junk=True), dict(strided=True), dict(shift=True)])
+@pytest.mark.parametrize("N,D,V", [(1, 1024, 9001), (2, 100, 300), (4, 64, 31), (5, 256, 1003), (7, 129, 77),
+                                   (8, 512, 2500), (8, 4096, 1000), (9, 512, 2500)])
+def test_head_few_rows(N, D, V, kw, dtype):
+    check_head(N, D, V, DT[dtype], seed=N + D, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("mask,junk", [(0.4, False), (0.4, True), (0.95, True), (1.1, True)])
 @pytest.mark.parametrize("N,D,V", [(9, 24, 40), (200, 128, 700), (385, 72, 300)])
 def test_head_rows_that_take_no_part(N, D, V, mask, junk, dtype):
