@@ -174,14 +174,16 @@ __device__ __forceinline__ bool rows_of_vectors(const float* p, int64_t stride) 
 constexpr int kPackThreads = 256;
 
 // Numbers the rows that take part, in order, gathers their tokens and factors,
-// packs their hidden rows, and clears the results of the other rows.  A CTA
+// packs their hidden rows (unless all take part and can be read in place), and
+// clears the results of the other rows.  A CTA
 // takes rows_per_cta rows and counts the parts before them (and in all) by
 // itself: N tokens from L2 instead of a pass of its own and a wait.  With
 // pad, the packed rows are zeroed to the next whole stage of k: the gradient's
 // product over parts reads them.
 template <class ST>
 __global__ void __launch_bounds__(kPackThreads)
-    head_begin_kernel(HeadArgs a, HeadView w, int64_t rows_per_cta, int64_t Dp, int64_t Np, bool pad) {
+    head_begin_kernel(HeadArgs a, HeadView w, int64_t rows_per_cta, int64_t Dp, int64_t Np, bool pad,
+                      bool in_place) {
   pdl_trigger();
   pdl_wait();
   __shared__ int scratch[32], list[kPackThreads];
@@ -198,6 +200,8 @@ __global__ void __launch_bounds__(kPackThreads)
   all = cta_sum(all, scratch);
   if (blockIdx.x == 0 && threadIdx.x == 0) w.count[0] = all;
 
+  // all rows take part and the copies can read them where they lie
+  const bool pack = !(in_place && all == a.N);
   const int groups = (int)(Dp / 8);
   const int64_t plane = Np * Dp;
   const bool vec = rows_of_vectors<ST>(a.hidden, a.hidden_stride);
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(kPackThreads)
     }
     __syncthreads();
     constexpr int B = 4;  // groups a thread has in flight
-    for (int t0 = threadIdx.x; t0 < n * groups; t0 += B * kPackThreads) {
+    for (int t0 = threadIdx.x; pack && t0 < n * groups; t0 += B * kPackThreads) {
       float v[B][8];
       int64_t to[B];
 #pragma unroll
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kPackThreads)
     before += n;
     __syncthreads();
   }
-  if (!pad) return;
+  if (!pad || !pack) return;
   const int64_t end = min(Np, ((int64_t)all + kTcK - 1) / kTcK * kTcK);
   for (int64_t r = all + blockIdx.x; r < end; r += gridDim.x)
     for (int c = threadIdx.x; c < groups; c += kPackThreads) {
@@ -817,10 +821,11 @@ int64_t few_grid(int64_t V, int sm_count) {
 }
 
 template <bool A_MN, bool B_MN, int GROUP, class Epi>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const TcShape& s, const Epi& epi, int sm_count,
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& other, const TcShape& s, const Epi& epi, int sm_count,
                            cudaStream_t st) {
   const auto kernel = tc_product_kernel<A_MN, B_MN, GROUP, Epi>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+  static std::atomic<uint64_t> allowed;
+  cudaError_t e = allow_smem(kernel, kTcSmem, allowed);
   if (e != cudaSuccess) return e;
   if (GROUP > 0) {
     // the warpgroups' register shares are taken from the launch's registers:
@@ -833,7 +838,7 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const T
     if (!enough) return cudaErrorInvalidConfiguration;
   }
   const int64_t tiles = div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits;
-  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, ma, mb, s, epi);
+  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, ma, mb, other, s, epi);
 }
 
 // rows of A walked together: as many as keep their `width` values in L2
@@ -863,7 +868,10 @@ struct HeadRun {
   const int sm;
   const cudaStream_t s;
   const TcTerms terms;
-  CUtensorMap hidden_k, hidden_mn;  // the parts' rows as a K-major and an MN-major operand
+  // the parts' rows as a K-major and an MN-major operand: packed, and where
+  // they lie (for when all rows take part)
+  CUtensorMap hidden_k, hidden_mn, in_place_k, in_place_mn;
+  bool hidden_ok = false;  // the copies can read the hidden rows where they lie
 
   HeadRun(const HeadArgs& args, const HeadPlan& plan, int sm_count, cudaStream_t st)
       : a(args), p(plan), w(plan, args.ws), sm(sm_count), s(st), terms(terms_of(plan.planes)) {}
@@ -872,9 +880,15 @@ struct HeadRun {
     if (!encode_matrix_map(&hidden_k, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcRows) ||
         !encode_matrix_map(&hidden_mn, w.hidden, p.Dp, p.Np, p.planes, p.Dp, p.Np * p.Dp, kTcK))
       return cudaErrorNotSupported;
-    const int64_t rows_per_cta = std::max<int64_t>(2, div_up(a.N, 2 * (int64_t)sm));
+    hidden_ok = a.bf16_io && ((uintptr_t)a.hidden & 15) == 0 && a.hidden_stride % 8 == 0;
+    in_place_k = hidden_k, in_place_mn = hidden_mn;
+    if (hidden_ok &&
+        (!encode_matrix_map(&in_place_k, a.hidden, a.D, a.N, 1, a.hidden_stride, a.N * a.hidden_stride, kTcRows) ||
+         !encode_matrix_map(&in_place_mn, a.hidden, a.D, a.N, 1, a.hidden_stride, a.N * a.hidden_stride, kTcK)))
+      return cudaErrorNotSupported;
+    const int64_t rows_per_cta = std::max<int64_t>(2, div_up(a.N, 4 * (int64_t)sm));
     return launch_pdl(head_begin_kernel<ST>, div_up(a.N, rows_per_cta), kPackThreads, 0, s, a, w, rows_per_cta, p.Dp,
-                      p.Np, a.d_logp != nullptr);
+                      p.Np, a.d_logp != nullptr, hidden_ok);
   }
   // the weight's rows from v0 on, packed where the copies cannot read them in place
   cudaError_t weight_piece(int64_t v0, int64_t len) {
@@ -893,6 +907,7 @@ struct HeadRun {
     t.count = w.count; t.count_axis = 1;
     t.m = (int)a.N; t.n = (int)len; t.k = (int)a.D;
     t.b_n0 = p.packed ? 0 : (int)v0;
+    t.other = hidden_ok ? 1 : 0; t.full = (int)a.N;
     t.splits = 1; t.band = band_of(p.Dp, p.planes); t.terms = terms;
     return t;
   }
@@ -907,7 +922,7 @@ struct HeadRun {
       CUtensorMap wk;
       if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, (int)v0, (int)(v0 + len), c2};
-      e = launch_product<false, false, kLogitsGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
+      e = launch_product<false, false, kLogitsGroup>(hidden_k, wk, in_place_k, logits_shape(v0, len), epi, sm, s);
     }
     return e == cudaSuccess ? join(div_up(a.V, kTcN) * 2, p.Np, false) : e;
   }
@@ -924,7 +939,8 @@ struct HeadRun {
     const auto kernel = head_few_kernel<ST, VE, NT>;
     const int64_t Ds = round_up(a.D, 4);
     const size_t smem = (size_t)NT * Ds * 4;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_smem(kernel, kFewSmem, allowed);
     if (e != cudaSuccess) return e;
     const int64_t grid = few_grid(a.V, sm);
     e = launch_pdl(kernel, grid, kFewThreads, smem, s, a, w, Ds, a.inv_temperature * kLog2e);
@@ -954,10 +970,10 @@ struct HeadRun {
         return cudaErrorNotSupported;
       if constexpr (Stor<ST>::kBytes == 2) {
         const DzEpi<1> epi{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
-        e = launch_product<false, false, kGradGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
+        e = launch_product<false, false, kGradGroup>(hidden_k, wk, in_place_k, logits_shape(v0, len), epi, sm, s);
       } else {
         const DzEpi<3> epi{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
-        e = launch_product<false, false, kGradGroup>(hidden_k, wk, logits_shape(v0, len), epi, sm, s);
+        e = launch_product<false, false, kGradGroup>(hidden_k, wk, in_place_k, logits_shape(v0, len), epi, sm, s);
       }
       if (e == cudaSuccess && a.d_hidden) {
         TcShape t = {};
@@ -965,15 +981,16 @@ struct HeadRun {
         t.m = (int)a.N; t.n = (int)a.D; t.k = (int)len;
         t.b_k0 = p.packed ? 0 : (int)v0;
         t.splits = p.splits; t.band = 16; t.terms = terms;
-        e = launch_product<false, true, kGradGroup>(dz_k, wmn, t, SumEpi{w.dh, p.Dh, dh_plane, v0 > 0}, sm, s);
+        e = launch_product<false, true, kGradGroup>(dz_k, wmn, wmn, t, SumEpi{w.dh, p.Dh, dh_plane, v0 > 0}, sm, s);
       }
       if (e == cudaSuccess && a.d_weight) {
         TcShape t = {};
         t.count = w.count; t.count_axis = 2;
         t.m = (int)len; t.n = (int)a.D; t.k = (int)a.N;
         t.splits = 1; t.band = 16; t.terms = terms;
+        t.other = hidden_ok ? 2 : 0; t.full = (int)a.N;
         const uintptr_t rows = (uintptr_t)a.d_weight | (uintptr_t)(a.D * Stor<ST>::kBytes);
-        e = launch_product<true, true, kGradGroup>(dz_mn, hidden_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, rows % 32 == 0, rows % 16 == 0}, sm, s);
+        e = launch_product<true, true, kGradGroup>(dz_mn, hidden_mn, in_place_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, rows % 32 == 0, rows % 16 == 0}, sm, s);
       }
     }
     if (e == cudaSuccess && a.d_hidden) {

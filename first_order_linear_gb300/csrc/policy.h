@@ -3,6 +3,7 @@
 // and the kernels.  Arguments are checked by the entry points.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>  // CUtensorMap
@@ -25,6 +26,20 @@ cudaError_t launch_pdl(void (*kernel)(P...), int64_t grid, int block, size_t sme
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Opts a kernel in to `bytes` of dynamic shared memory on the current device,
+// the first time it is launched there.
+template <class K>
+cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 constexpr int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -75,6 +75,8 @@ struct TcShape {
   int a_m0, b_n0, b_k0;
   int splits;      // the k axis in this many parts (each its own output)
   int band;        // row tiles walked together before the next column tile
+  // where *count == full, map_other stands for A's (other = 1) or B's (2)
+  int other, full;
   TcTerms terms;
 };
 
@@ -229,10 +231,10 @@ struct TcTile {
 };
 
 struct TcWalk {
-  int m, k, mt, nt, k_stages, per_split;
+  int count, m, k, mt, nt, k_stages, per_split;
   int64_t tiles;
   __device__ TcWalk(const TcShape& s) {
-    const int count = s.count_axis ? *s.count : 0;
+    count = s.count ? *s.count : 0;
     m = s.count_axis == 1 ? min(count, s.m) : s.m;
     k = s.count_axis == 2 ? min(count, s.k) : s.k;
     mt = (m + kTcM - 1) / kTcM;
@@ -277,7 +279,7 @@ __device__ __forceinline__ int tc_group_end(int at, int stages, int terms) {
 template <bool A_MN, bool B_MN, int GROUP, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ TcShape s, const __grid_constant__ Epi epi) {
+                      const __grid_constant__ CUtensorMap map_other, const __grid_constant__ TcShape s, const __grid_constant__ Epi epi) {
   extern __shared__ unsigned char tc_smem_raw[];
   // of the first CTA: full, acc_empty; of both: empty, acc_full, drained
   __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drained;
@@ -321,8 +323,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (lane == 0) {
       // operands written by earlier kernels' ordinary stores, read by copies
       asm volatile("fence.proxy.async;" ::: "memory");
-      tma_prefetch_map(&map_a);
-      tma_prefetch_map(&map_b);
+      const bool other = s.other != 0 && walk.count == s.full;
+      const CUtensorMap* ma = other && s.other == 1 ? &map_other : &map_a;
+      const CUtensorMap* mb = other && s.other == 2 ? &map_other : &map_b;
+      tma_prefetch_map(ma);
+      tma_prefetch_map(mb);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -346,16 +351,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             if constexpr (A_MN) {
 #pragma unroll
               for (int i = 0; i < kTcRows / 64; ++i)
-                tma_load_3d(sa + i * kTcK * 128, &map_a, m0 + 64 * i, k0, pa, bar);
+                tma_load_3d(sa + i * kTcK * 128, ma, m0 + 64 * i, k0, pa, bar);
             } else {
-              tma_load_3d(sa, &map_a, k0, m0, pa, bar);
+              tma_load_3d(sa, ma, k0, m0, pa, bar);
             }
             if constexpr (B_MN) {
 #pragma unroll
               for (int i = 0; i < kTcN / 2 / 64; ++i)
-                tma_load_3d(sb + i * kTcK * 128, &map_b, n0 + 64 * i, s.b_k0 + k0, pb, bar);
+                tma_load_3d(sb + i * kTcK * 128, mb, n0 + 64 * i, s.b_k0 + k0, pb, bar);
             } else {
-              tma_load_3d(sb, &map_b, s.b_k0 + k0, n0, pb, bar);
+              tma_load_3d(sb, mb, s.b_k0 + k0, n0, pb, bar);
             }
             if (++stage == kTcStages) stage = 0, phase ^= 1;
           }

@@ -18,6 +18,7 @@ arithmetic, outputs rounded once).
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 
 import torch
 
@@ -121,7 +122,9 @@ def rlca_workspace_size(estimator: int, E: int, T: int, num_actions: int = 0, fl
 
 
 def _workspace(estimator, E, T, A, flags, device, workspace):
-    need = rlca_workspace_size(estimator, E, T, A, flags, device)
+    need = _ws_sizes.get((estimator, E, T, A, flags, device.index))
+    if need is None:
+        need = rlca_workspace_size(estimator, E, T, A, flags, device)
     if need == 0:
         return None, 0
     if workspace is None:
@@ -431,26 +434,31 @@ def rlca_affine_scan(alpha, beta, carry=None, *, reverse=True, out=None, time_ma
 
 # ---- the policy update around the scans ------------------------------------
 # Matrices here are 2-D with contiguous rows at any row stride (a slice of a
-# wider buffer works); everything else is contiguous as above.
+# wider buffer works); everything else is contiguous as above.  Small calls
+# cost more on the host than on the device, so the checks take one combined
+# test on the common path, small float32 outputs of a call share one
+# allocation, and the device is only switched when it is not the current one.
 
-def _check_matrix(t, name, dtypes, shape, device):
+def _check_matrix(t, name, dtype, shape, device):
     """Checks a matrix input and returns its row stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape) if shape else '2 dimensions'}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    got = t.shape
+    if len(got) != 2 or (shape is not None and got != shape):
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple(shape) if shape else '2 dimensions'}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    rows, width = t.shape
-    if width > 1 and t.stride(1) != 1:
+    rows, width = got
+    row_stride, stride = t.stride()
+    if width > 1 and stride != 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
         return width
-    if t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)} below width {width})")
-    return t.stride(0)
+    if row_stride < width:
+        raise ValueError(f"{name}: rows overlap (row stride {row_stride} below width {width})")
+    return row_stride
 
 
 def _out(t, name, dtype, shape, device, want=True):
@@ -461,24 +469,56 @@ def _out(t, name, dtype, shape, device, want=True):
     return t
 
 
+def _out_rows(bufs, names, wants, n, device):
+    """float32 [n] output buffers: those given (checked), and the wanted others from one allocation."""
+    new = [k for k, (b, w) in enumerate(zip(bufs, wants)) if b is None and w]
+    for k, b in enumerate(bufs):
+        if b is not None:
+            _check(b, names[k], _F, (n,), device)
+    if new:
+        for k, row in zip(new, torch.empty((len(new), n), dtype=torch.float32, device=device).unbind(0)):
+            bufs[k] = row
+    return bufs
+
+
+class _Here:
+    """The device guard of a call whose device is the current one already."""
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_here = _Here()
+
+
+def _on(device):
+    return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _raw_stream(device, stream):
+    # the handle of the current stream without building a Stream object
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def rlca_layer_norm(x, weight, bias=None, *, eps=1e-5, y=None, mean=None, rstd=None, stream=None):
     """Layer norm of the rows of ``x`` [N, D]: ``(y, mean, rstd)``, the
     statistics float32 for :func:`rlca_layer_norm_backward`."""
     lib = _lib.load()
     fdt = _fdt(x, "x")
     dev = x.device
-    stride = _check_matrix(x, "x", (fdt,), None, dev)
+    stride = _check_matrix(x, "x", fdt, None, dev)
     N, D = x.shape
     _check(weight, "weight", (fdt,), (D,), dev)
     _check(bias, "bias", (fdt,), (D,), dev, required=False)
     y = _out(y, "y", fdt, (N, D), dev)
-    mean = _out(mean, "mean", torch.float32, (N,), dev)
-    rstd = _out(rstd, "rstd", torch.float32, (N,), dev)
+    mean, rstd = _out_rows([mean, rstd], ("mean", "rstd"), (True, True), N, dev)
     _require_cuda(dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("rlca_layer_norm", lib.rlca_layer_norm(
-            _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), N, D, stride, eps, _fflag(fdt),
-            _stream(dev, stream)))
+            x.data_ptr(), weight.data_ptr(), _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), N, D, stride,
+            eps, _fflag(fdt), _raw_stream(dev, stream)))
         _hold(dev, stream, y, mean, rstd)
     return y, mean, rstd
 
@@ -490,23 +530,27 @@ def rlca_layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None
     lib = _lib.load()
     fdt = _fdt(x, "x")
     dev = x.device
-    x_stride = _check_matrix(x, "x", (fdt,), None, dev)
+    x_stride = _check_matrix(x, "x", fdt, None, dev)
     N, D = x.shape
-    dy_stride = _check_matrix(dy, "dy", (fdt,), (N, D), dev)
+    dy_stride = _check_matrix(dy, "dy", fdt, (N, D), dev)
     _check(weight, "weight", (fdt,), (D,), dev)
     _check(mean, "mean", _F, (N,), dev)
     _check(rstd, "rstd", _F, (N,), dev)
     dx = _out(dx, "dx", fdt, (N, D), dev, want_dx)
-    dweight = _out(dweight, "dweight", fdt, (D,), dev, want_dweight)
-    dbias = _out(dbias, "dbias", fdt, (D,), dev, want_dbias)
+    if dweight is None and dbias is None and want_dweight and want_dbias:
+        dweight, dbias = torch.empty((2, D), dtype=fdt, device=dev).unbind(0)
+    else:
+        dweight = _out(dweight, "dweight", fdt, (D,), dev, want_dweight)
+        dbias = _out(dbias, "dbias", fdt, (D,), dev, want_dbias)
     if dx is None and dweight is None and dbias is None:
         raise ValueError("no output wanted")
     _require_cuda(dev)
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(_lib.RLCA_EST_LAYER_NORM_BACKWARD, N, D, 0, _fflag(fdt), dev, workspace)
+    flags = _fflag(fdt)
+    with _on(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_LAYER_NORM_BACKWARD, N, D, 0, flags, dev, workspace)
         check("rlca_layer_norm_backward", lib.rlca_layer_norm_backward(
-            _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), N, D,
-            dy_stride, x_stride, _fflag(fdt), _ptr(ws), wsb, _stream(dev, stream)))
+            dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dx), _ptr(dweight),
+            _ptr(dbias), N, D, dy_stride, x_stride, flags, _ptr(ws), wsb, _raw_stream(dev, stream)))
         _hold(dev, stream, ws, dx, dweight, dbias)
     return dx, dweight, dbias
 
@@ -514,15 +558,16 @@ def rlca_layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None
 def _check_head(hidden, weight, tokens, temperature):
     fdt = _fdt(hidden, "hidden")
     dev = hidden.device
-    hidden_stride = _check_matrix(hidden, "hidden", (fdt,), None, dev)
+    hidden_stride = _check_matrix(hidden, "hidden", fdt, None, dev)
     N, D = hidden.shape
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be a 2-D tensor [V, D]")
-    weight_stride = _check_matrix(weight, "weight", (fdt,), (weight.shape[0], D), dev)
+    weight_stride = _check_matrix(weight, "weight", fdt, None, dev)
+    V, width = weight.shape
+    if width != D:
+        raise ValueError(f"weight: shape {(V, width)}, expected (vocabulary, {D})")
     _check(tokens, "tokens", _I32, (N,), dev)
     if not temperature > 0.0:
         raise ValueError(f"temperature {temperature} must be positive")
-    return fdt, dev, N, D, weight.shape[0], hidden_stride, weight_stride
+    return fdt, dev, N, D, V, hidden_stride, weight_stride
 
 
 def rlca_token_logprob(hidden, weight, tokens, *, temperature=1.0, logp=None, lse=None, entropy=None,
@@ -534,15 +579,14 @@ def rlca_token_logprob(hidden, weight, tokens, *, temperature=1.0, logp=None, ls
     [0, V) takes no part: its results are 0."""
     lib = _lib.load()
     fdt, dev, N, D, V, hs, wst = _check_head(hidden, weight, tokens, temperature)
-    logp = _out(logp, "logp", torch.float32, (N,), dev)
-    lse = _out(lse, "lse", torch.float32, (N,), dev)
-    entropy = _out(entropy, "entropy", torch.float32, (N,), dev, want_entropy)
+    logp, lse, entropy = _out_rows([logp, lse, entropy], ("logp", "lse", "entropy"), (True, True, want_entropy), N, dev)
     _require_cuda(dev)
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(_lib.RLCA_EST_TOKEN_LOGPROB, N, D, V, _fflag(fdt), dev, workspace)
+    flags = _fflag(fdt)
+    with _on(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_TOKEN_LOGPROB, N, D, V, flags, dev, workspace)
         check("rlca_token_logprob", lib.rlca_token_logprob(
-            _ptr(hidden), _ptr(weight), _ptr(tokens), _ptr(logp), _ptr(lse), _ptr(entropy), N, D, V, hs, wst,
-            1.0 / temperature, _fflag(fdt), _ptr(ws), wsb, _stream(dev, stream)))
+            hidden.data_ptr(), weight.data_ptr(), tokens.data_ptr(), logp.data_ptr(), lse.data_ptr(), _ptr(entropy), N,
+            D, V, hs, wst, 1.0 / temperature, flags, _ptr(ws), wsb, _raw_stream(dev, stream)))
         _hold(dev, stream, ws, logp, lse, entropy)
     return logp, lse, entropy
 
@@ -555,24 +599,35 @@ def rlca_token_logprob_backward(hidden, weight, tokens, lse, d_logp, *, entropy=
     ``(d_hidden, d_weight)``, None for one not wanted (at least one is)."""
     lib = _lib.load()
     fdt, dev, N, D, V, hs, wst = _check_head(hidden, weight, tokens, temperature)
-    for name, t, required in (("lse", lse, True), ("d_logp", d_logp, True), ("entropy", entropy, False),
-                              ("d_entropy", d_entropy, False)):
-        _check(t, name, _F, (N,), dev, required=required)
+    rows = (N,)
+    _check(lse, "lse", _F, rows, dev)
+    _check(d_logp, "d_logp", _F, rows, dev)
     if (entropy is None) != (d_entropy is None):
         raise ValueError("entropy and d_entropy come together")
+    if entropy is not None:
+        _check(entropy, "entropy", _F, rows, dev)
+        _check(d_entropy, "d_entropy", _F, rows, dev)
     d_hidden = _out(d_hidden, "d_hidden", fdt, (N, D), dev, want_d_hidden)
     d_weight = _out(d_weight, "d_weight", fdt, (V, D), dev, want_d_weight)
     if d_hidden is None and d_weight is None:
         raise ValueError("no output wanted")
     _require_cuda(dev)
-    with torch.cuda.device(dev):
-        ws, wsb = _workspace(_lib.RLCA_EST_TOKEN_LOGPROB_BACKWARD, N, D, V, _fflag(fdt), dev, workspace)
+    flags = _fflag(fdt)
+    with _on(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_TOKEN_LOGPROB_BACKWARD, N, D, V, flags, dev, workspace)
         check("rlca_token_logprob_backward", lib.rlca_token_logprob_backward(
-            _ptr(hidden), _ptr(weight), _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(d_logp), _ptr(d_entropy),
-            _ptr(d_hidden), _ptr(d_weight), N, D, V, hs, wst, 1.0 / temperature, _fflag(fdt), _ptr(ws), wsb,
-            _stream(dev, stream)))
+            hidden.data_ptr(), weight.data_ptr(), tokens.data_ptr(), lse.data_ptr(), _ptr(entropy), d_logp.data_ptr(),
+            _ptr(d_entropy), _ptr(d_hidden), _ptr(d_weight), N, D, V, hs, wst, 1.0 / temperature, flags, _ptr(ws), wsb,
+            _raw_stream(dev, stream)))
         _hold(dev, stream, ws, d_hidden, d_weight)
     return d_hidden, d_weight
+
+
+_GRAD_FLAGS = {torch.float32: 0, torch.bfloat16: _lib.RLCA_BF16}
+
+
+def _address(a):
+    return a.buffer_info()[0]
 
 
 def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, norm=None, workspace=None, stream=None):
@@ -586,8 +641,11 @@ def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, nor
     grads = list(grads)
     if norm is None and not grads:
         raise ValueError("no gradients and no norm buffer: the device is unknown")
-    dev = grads[0].device if grads else norm.device
     n = len(grads)
+    for k, g in enumerate(grads):
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"grads[{k}] must be a torch.Tensor")
+    dev = grads[0].device if grads else norm.device
     if norm_only:
         out = None
     elif out is None:
@@ -596,19 +654,29 @@ def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, nor
         out = list(out)
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors, expected {n}")
+    flags = []
     for k, g in enumerate(grads):
-        _check(g, f"grads[{k}]", (_fdt(g, f"grads[{k}]"),), g.shape, dev)
-        if out is not None and out[k] is not g:
-            _check(out[k], f"out[{k}]", (g.dtype,), g.shape, dev)
+        dt = g.dtype
+        f = _GRAD_FLAGS.get(dt)
+        if f is None or g.device != dev or not g.is_contiguous():
+            _check(g, f"grads[{k}]", (_fdt(g, f"grads[{k}]"),), g.shape, dev)  # names the fault
+        flags.append(f)
+        if out is not None:
+            o = out[k]
+            if o is not g and not (isinstance(o, torch.Tensor) and o.dtype is dt and o.shape == g.shape
+                                   and o.device == dev and o.is_contiguous()):
+                _check(o, f"out[{k}]", (dt,), g.shape, dev)
     norm = _out(norm, "norm", torch.float32, (), dev)
     _require_cuda(dev)
-    gp = (C.c_void_p * n)(*[g.data_ptr() for g in grads])
-    op = None if out is None else (C.c_void_p * n)(*[o.data_ptr() for o in out])
-    sizes = (C.c_int64 * n)(*[g.numel() for g in grads])
-    dtypes = (C.c_uint32 * n)(*[_fflag(g.dtype) for g in grads])
-    with torch.cuda.device(dev):
+    # host arrays that the call reads before it returns
+    gp = array("Q", [g.data_ptr() for g in grads])
+    op = None if out is None else array("Q", [o.data_ptr() for o in out])
+    sizes = array("q", [g.numel() for g in grads])
+    dtypes = array("I", flags)
+    with _on(dev):
         ws, wsb = _workspace(_lib.RLCA_EST_CLIP_GRADS, n, 1, 0, 0, dev, workspace)
-        check("rlca_clip_grads", lib.rlca_clip_grads(gp, op, sizes, dtypes, n, max_norm, eps, _ptr(norm), _ptr(ws), wsb,
-                                                     _stream(dev, stream)))
+        check("rlca_clip_grads", lib.rlca_clip_grads(
+            _address(gp), None if op is None else _address(op), _address(sizes), _address(dtypes), n, max_norm, eps,
+            norm.data_ptr(), _ptr(ws), wsb, _raw_stream(dev, stream)))
         _hold(dev, stream, ws, norm, *(out or ()))
     return out, norm
