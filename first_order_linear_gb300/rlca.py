@@ -436,8 +436,8 @@ def rlca_affine_scan(alpha, beta, carry=None, *, reverse=True, out=None, time_ma
 # Matrices here are 2-D with contiguous rows at any row stride (a slice of a
 # wider buffer works); everything else is contiguous as above.  Small calls
 # cost more on the host than on the device, so the checks take one combined
-# test on the common path, small float32 outputs of a call share one
-# allocation, and the device is only switched when it is not the current one.
+# test on the common path and the device is only switched when it is not the
+# current one.
 
 def _check_matrix(t, name, dtype, shape, device):
     """Checks a matrix input and returns its row stride in elements."""
@@ -463,22 +463,10 @@ def _check_matrix(t, name, dtype, shape, device):
 
 def _out(t, name, dtype, shape, device, want=True):
     """An output buffer: the one given (checked), a new one, or None."""
-    if t is None and want:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, (dtype,), shape, device, required=False)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device) if want else None
+    _check(t, name, (dtype,), shape, device)
     return t
-
-
-def _out_rows(bufs, names, wants, n, device):
-    """float32 [n] output buffers: those given (checked), and the wanted others from one allocation."""
-    new = [k for k, (b, w) in enumerate(zip(bufs, wants)) if b is None and w]
-    for k, b in enumerate(bufs):
-        if b is not None:
-            _check(b, names[k], _F, (n,), device)
-    if new:
-        for k, row in zip(new, torch.empty((len(new), n), dtype=torch.float32, device=device).unbind(0)):
-            bufs[k] = row
-    return bufs
 
 
 class _Here:
@@ -513,7 +501,8 @@ def rlca_layer_norm(x, weight, bias=None, *, eps=1e-5, y=None, mean=None, rstd=N
     _check(weight, "weight", (fdt,), (D,), dev)
     _check(bias, "bias", (fdt,), (D,), dev, required=False)
     y = _out(y, "y", fdt, (N, D), dev)
-    mean, rstd = _out_rows([mean, rstd], ("mean", "rstd"), (True, True), N, dev)
+    mean = _out(mean, "mean", torch.float32, (N,), dev)
+    rstd = _out(rstd, "rstd", torch.float32, (N,), dev)
     _require_cuda(dev)
     with _on(dev):
         check("rlca_layer_norm", lib.rlca_layer_norm(
@@ -537,11 +526,8 @@ def rlca_layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None
     _check(mean, "mean", _F, (N,), dev)
     _check(rstd, "rstd", _F, (N,), dev)
     dx = _out(dx, "dx", fdt, (N, D), dev, want_dx)
-    if dweight is None and dbias is None and want_dweight and want_dbias:
-        dweight, dbias = torch.empty((2, D), dtype=fdt, device=dev).unbind(0)
-    else:
-        dweight = _out(dweight, "dweight", fdt, (D,), dev, want_dweight)
-        dbias = _out(dbias, "dbias", fdt, (D,), dev, want_dbias)
+    dweight = _out(dweight, "dweight", fdt, (D,), dev, want_dweight)
+    dbias = _out(dbias, "dbias", fdt, (D,), dev, want_dbias)
     if dx is None and dweight is None and dbias is None:
         raise ValueError("no output wanted")
     _require_cuda(dev)
@@ -579,7 +565,9 @@ def rlca_token_logprob(hidden, weight, tokens, *, temperature=1.0, logp=None, ls
     [0, V) takes no part: its results are 0."""
     lib = _lib.load()
     fdt, dev, N, D, V, hs, wst = _check_head(hidden, weight, tokens, temperature)
-    logp, lse, entropy = _out_rows([logp, lse, entropy], ("logp", "lse", "entropy"), (True, True, want_entropy), N, dev)
+    logp = _out(logp, "logp", torch.float32, (N,), dev)
+    lse = _out(lse, "lse", torch.float32, (N,), dev)
+    entropy = _out(entropy, "entropy", torch.float32, (N,), dev, want_entropy)
     _require_cuda(dev)
     flags = _fflag(fdt)
     with _on(dev):
