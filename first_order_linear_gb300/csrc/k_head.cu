@@ -29,6 +29,8 @@ namespace {
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // dz of one piece of the vocabulary
 constexpr int64_t kPackBytes = int64_t(128) << 20;   // packed weight of one piece
 constexpr int64_t kSplitBytes = int64_t(64) << 20;   // d_hidden's partial sums beyond the first
+constexpr int64_t kWholeStages = 20;                  // k stages of a d_hidden sum that is not split
+constexpr int64_t kSplitStages = 8;                   // ... and at least this many a split
 constexpr int64_t kBandBytes = int64_t(48) << 20;    // hidden rows walked together (well inside L2)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -81,11 +83,17 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
     p.info = take((size_t)N * sizeof(float4));
     p.dz = take((size_t)p.planes * p.Np * p.pitch * 2);
     // d_hidden has few tiles when there are few rows: its sum over tokens is
-    // then split until the tiles fill the SMs
+    // then split until the tiles fill the CTA pairs -- unless a whole sum is
+    // no longer than the kernel that joins the splits (0.27 us a stage
+    // against 5 to 6 us)
     const int64_t out_tiles = (int64_t)p.row_tiles * p.d_tiles, out_bytes = p.Np * p.Dh * 4;
-    p.splits = (int)std::max<int64_t>(
-        1, std::min({(int64_t)sm_count / out_tiles, 1 + kSplitBytes / out_bytes, div_up(p.piece, kTcK)}));
-    p.dh = take((size_t)p.splits * out_bytes);
+    const int64_t stages = div_up(p.piece, kTcK);
+    p.splits = 1;
+    if (stages > kWholeStages || piece_tiles < tiles)
+      p.splits = (int)std::max<int64_t>(
+          1, std::min({(int64_t)sm_count / 2 / out_tiles, 1 + kSplitBytes / out_bytes, div_up(stages, kSplitStages)}));
+    // (one piece, not split: the product writes d_hidden itself)
+    if (p.splits > 1 || piece_tiles < tiles) p.dh = take((size_t)p.splits * out_bytes);
   } else {
     // (head_few_kernel: one piece a CTA, of at most 8 rows)
     p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 8) * sizeof(float4));
@@ -225,12 +233,22 @@ __global__ void __launch_bounds__(kPackThreads)
       if (a.d_logp != nullptr)
         w.info[before + at] = make_float4(a.d_logp[i], a.d_entropy ? a.d_entropy[i] : 0.f, a.in_lse[i],
                                           a.d_entropy ? a.in_entropy[i] : 0.f);
-    } else if (i < r1 && a.logp != nullptr) {
-      a.logp[i] = 0.f;
-      a.lse[i] = 0.f;
-      if (a.entropy) a.entropy[i] = 0.f;
+    } else if (i < r1) {
+      list[kPackThreads - 1 - ((int)(i - i0) - at)] = (int)i;  // from the end: those that do not
+      if (a.logp != nullptr) {
+        a.logp[i] = 0.f;
+        a.lse[i] = 0.f;
+        if (a.entropy) a.entropy[i] = 0.f;
+      }
     }
     __syncthreads();
+    if (a.d_hidden != nullptr) {
+      const int off = (int)min((int64_t)kPackThreads, r1 - i0) - n;
+      for (int r = 0; r < off; ++r) {
+        const int64_t to = list[kPackThreads - 1 - r] * a.D;
+        for (int64_t c = threadIdx.x; c < a.D; c += kPackThreads) Stor<ST>::st(a.d_hidden, to + c, 0.f);
+      }
+    }
     constexpr int B = 4;  // groups a thread has in flight
     for (int t0 = threadIdx.x; pack && t0 < n * groups; t0 += B * kPackThreads) {
       float v[B][8];
@@ -475,45 +493,95 @@ struct DzEpi {
   __device__ __forceinline__ void end(State&) const {}
 };
 
-// float32 sums, set by the first piece and added to by the others
-struct SumEpi {
-  float* out;  // splits x [rows, pitch]
+// 32 values from column `col` on to the row that starts at element `at` of a
+// matrix of `width` columns, rounded once; align: what the rows' starts are
+// multiples of, in bytes (32, 16, or less)
+template <class ST>
+__device__ __forceinline__ void store_row32(float* out, int64_t at, int64_t col, int64_t width, int align, const float* v) {
+  if (align >= 32 && col + 32 <= width) {
+    unsigned char* p = reinterpret_cast<unsigned char*>(out) + (at + col) * Stor<ST>::kBytes;
+    if constexpr (Stor<ST>::kBytes == 2) {
+      store16(reinterpret_cast<uint16_t*>(p), v);
+      store16(reinterpret_cast<uint16_t*>(p) + 16, v + 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
+        store32(p + 4 * i, r);
+      }
+    }
+  } else {
+    constexpr int E = 16 / Stor<ST>::kBytes;
+#pragma unroll
+    for (int i = 0; i < 32; i += E) {
+      if (align >= 16 && col + i + E <= width) {
+        if constexpr (E == 8) Stor<ST>::st8(out, at + col + i, v + i);
+        else Stor<ST>::st4(out, at + col + i, v + i);
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (col + i + j < width) Stor<ST>::st(out, at + col + i + j, v[i + j]);
+      }
+    }
+  }
+}
+
+// d_hidden.  The sum over the pieces of the vocabulary is kept in float32
+// (`sums`, one plane a split), set by the first piece and added to by the
+// others; without splits the last piece writes the result itself, to the
+// part's row.
+template <class ST>
+struct DhEpi {
+  float* sums;  // splits x [rows, pitch]
   int64_t pitch, plane;
-  bool add;
+  bool first, last;
+  float* out;  // [N, width], type ST
+  const int* rows;
+  int64_t width;
+  int align;
 
   struct State {
-    float* row;
+    float* sum;
+    int64_t at;
     bool live;
   };
   __device__ __forceinline__ void begin(State& st, const TcWalk& w, const TcTile& t, int row, int) const {
     st.live = row < w.m;
-    st.row = out + t.split * plane + (int64_t)row * pitch;
+    st.sum = sums + t.split * plane + (int64_t)row * pitch;
+    st.at = last && st.live ? rows[row] * width : 0;
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
     if (!st.live || col >= pitch) return;
+    if (!first) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      uint32_t r[8];
-      if (add) {
-        const float4* o = reinterpret_cast<const float4*>(st.row + col + i);
-        const float4 lo = o[0], hi = o[1];
-        v[i] += lo.x, v[i + 1] += lo.y, v[i + 2] += lo.z, v[i + 3] += lo.w;
-        v[i + 4] += hi.x, v[i + 5] += hi.y, v[i + 6] += hi.z, v[i + 7] += hi.w;
+      for (int i = 0; i < 32; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(st.sum + col + i);
+        v[i] += o.x, v[i + 1] += o.y, v[i + 2] += o.z, v[i + 3] += o.w;
       }
+    }
+    if (last) {
+      store_row32<ST>(out, st.at, col, width, align, v);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
-      store32(st.row + col + i, r);
+      for (int i = 0; i < 32; i += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
+        store32(st.sum + col + i, r);
+      }
     }
   }
   __device__ __forceinline__ void end(State&) const {}
 };
 
-// the result, rounded once
+// d_weight, rounded once
 template <class ST>
 struct OutEpi {
   float* out;  // [.., width], element type ST
   int64_t row0, width;
-  bool vec, vec16;  // rows start on 32-byte, on 16-byte boundaries
+  int align;
 
   struct State {
     int64_t at;
@@ -524,35 +592,7 @@ struct OutEpi {
     st.at = (row0 + row) * width;
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
-    if (!st.live) return;
-    if (vec && col + 32 <= width) {
-      unsigned char* p = reinterpret_cast<unsigned char*>(out) + (st.at + col) * Stor<ST>::kBytes;
-      if constexpr (Stor<ST>::kBytes == 2) {
-        store16(reinterpret_cast<uint16_t*>(p), v);
-        store16(reinterpret_cast<uint16_t*>(p) + 16, v + 16);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t r[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
-          store32(p + 4 * i, r);
-        }
-      }
-    } else {
-      constexpr int E = 16 / Stor<ST>::kBytes;
-#pragma unroll
-      for (int i = 0; i < 32; i += E) {
-        if (vec16 && col + i + E <= width) {
-          if constexpr (E == 8) Stor<ST>::st8(out, st.at + col + i, v + i);
-          else Stor<ST>::st4(out, st.at + col + i, v + i);
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j)
-            if (col + i + j < width) Stor<ST>::st(out, st.at + col + i + j, v[i + j]);
-        }
-      }
-    }
+    if (st.live) store_row32<ST>(out, st.at, col, width, align, v);
   }
   __device__ __forceinline__ void end(State&) const {}
 };
@@ -757,42 +797,36 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
   }
 }
 
-// d_hidden: the splits' sums in order, rounded once; zeros for rows that take
-// no part.  One thread four columns of part b and of row b.
+// d_hidden where its sum was split: the splits' sums in order, rounded once.
+// One thread four columns of a part.
 template <class ST>
 __global__ void __launch_bounds__(kJoinThreads)
     head_dh_out_kernel(HeadArgs a, HeadView w, int64_t Dh, int64_t plane, int splits, bool vec) {
   pdl_trigger();
   pdl_wait();
   const int groups = (int)((a.D + 3) / 4);
-  const int64_t parts = w.count[0];
-  for (int64_t t = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; t < a.N * groups;
-       t += (int64_t)gridDim.x * kJoinThreads) {
+  const int64_t total = (int64_t)w.count[0] * groups;
+  for (int64_t t = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kJoinThreads) {
     const int64_t b = t / groups, c = (t - b * groups) * 4;
-    const auto put = [&](int64_t row, const float4& v) {
-      const float f[4] = {v.x, v.y, v.z, v.w};
-      if (vec) {
-        Stor<ST>::st4(a.d_hidden, row * a.D + c, f);
-      } else {
+    const float* src = w.dh + b * Dh + c;
+    float4 v = *reinterpret_cast<const float4*>(src);
+    for (int k0 = 1; k0 < splits; k0 += 8) {
+      float4 q[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < a.D) Stor<ST>::st(a.d_hidden, row * a.D + c + i, f[i]);
-      }
-    };
-    if (b < parts) {
-      const float* src = w.dh + b * Dh + c;
-      float4 v = *reinterpret_cast<const float4*>(src);
-      for (int k0 = 1; k0 < splits; k0 += 8) {
-        float4 q[8];
+      for (int u = 0; u < 8; ++u)
+        q[u] = k0 + u < splits ? *reinterpret_cast<const float4*>(src + (k0 + u) * plane) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          q[u] = k0 + u < splits ? *reinterpret_cast<const float4*>(src + (k0 + u) * plane) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v.x += q[u].x, v.y += q[u].y, v.z += q[u].z, v.w += q[u].w;
-      }
-      put(w.rows[b], v);
+      for (int u = 0; u < 8; ++u) v.x += q[u].x, v.y += q[u].y, v.z += q[u].z, v.w += q[u].w;
     }
-    if ((unsigned)a.tokens[b] >= (unsigned)a.V) put(b, make_float4(0.f, 0.f, 0.f, 0.f));
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    const int64_t to = w.rows[b] * a.D + c;
+    if (vec) {
+      Stor<ST>::st4(a.d_hidden, to, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < a.D) Stor<ST>::st(a.d_hidden, to + i, f[i]);
+    }
   }
 }
 
@@ -820,14 +854,15 @@ int64_t few_grid(int64_t V, int sm_count) {
   return std::min<int64_t>(div_up(V, kFewTokens * (kFewThreads / 32)), few_pieces(sm_count));
 }
 
-template <bool A_MN, bool B_MN, int GROUP, class Epi>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& other, const TcShape& s, const Epi& epi, int sm_count,
-                           cudaStream_t st) {
-  const auto kernel = tc_product_kernel<A_MN, B_MN, GROUP, Epi>;
+int64_t tiles_of(const TcShape& s) { return div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits; }
+
+template <class Job1, class Job2>
+cudaError_t launch_product(const Job1& j1, const Job2& j2, int64_t tiles, int sm_count, cudaStream_t st) {
+  void (*const kernel)(const Job1, const Job2) = tc_product_kernel<Job1, Job2>;
   static std::atomic<uint64_t> allowed;
   cudaError_t e = allow_smem(kernel, kTcSmem, allowed);
   if (e != cudaSuccess) return e;
-  if (GROUP > 0) {
+  if (Job1::GROUP > 0) {
     // the warpgroups' register shares are taken from the launch's registers:
     // a kernel built with fewer would wait for the rest for ever
     static const bool enough = [&] {
@@ -837,8 +872,26 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const C
     }();
     if (!enough) return cudaErrorInvalidConfiguration;
   }
-  const int64_t tiles = div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits;
-  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, ma, mb, other, s, epi);
+  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, j1, j2);
+}
+template <class Job>
+cudaError_t launch_product(const Job& j, int sm_count, cudaStream_t st) {
+  return launch_product(j, TcNoJob{}, tiles_of(j.s), sm_count, st);
+}
+
+// Whether two products run faster dealt out together than one after the
+// other: stages of the busiest cluster either way (the first product's tiles
+// take k1 stages, the second's k2), a launch costing as much as kLaunchStages.
+constexpr int64_t kLaunchStages = 24;
+bool together(int64_t tiles1, int64_t k1, int64_t tiles2, int64_t k2, int64_t clusters) {
+  const int64_t apart = div_up(tiles1, clusters) * k1 + div_up(tiles2, clusters) * k2 + kLaunchStages;
+  int64_t most = 0;
+  for (int64_t c = 0; c < clusters; ++c) {
+    const int64_t n1 = c < tiles1 ? div_up(tiles1 - c, clusters) : 0;
+    const int64_t n = c < tiles1 + tiles2 ? div_up(tiles1 + tiles2 - c, clusters) : 0;
+    most = std::max(most, n1 * k1 + (n - n1) * k2);
+  }
+  return most <= apart;
 }
 
 // rows of A walked together: as many as keep their `width` values in L2
@@ -854,10 +907,7 @@ bool in_place(const HeadArgs& a) {
 // Stages summed by the tensor cores alone (tc.cuh): 512 values of k for
 // results that leave in float32; the bfloat16 gradients' own rounding is
 // larger than the whole sum's error.
-#ifndef TCG
-#define TCG 8
-#endif
-constexpr int kLogitsGroup = TCG;
+constexpr int kLogitsGroup = 8;
 
 template <class ST>
 struct HeadRun {
@@ -922,7 +972,8 @@ struct HeadRun {
       CUtensorMap wk;
       if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, (int)v0, (int)(v0 + len), c2};
-      e = launch_product<false, false, kLogitsGroup>(hidden_k, wk, in_place_k, logits_shape(v0, len), epi, sm, s);
+      e = launch_product(TcJob<false, false, kLogitsGroup, StatsEpi>{hidden_k, wk, in_place_k, logits_shape(v0, len), epi},
+                         sm, s);
     }
     return e == cudaSuccess ? join(div_up(a.V, kTcN) * 2, p.Np, false) : e;
   }
@@ -956,6 +1007,12 @@ struct HeadRun {
     return vec ? few_rows<VE>() : few_rows<1>();
   }
 
+  // what the starts of an output's rows are multiples of (32, 16, or neither: 1)
+  int align_of(const float* out) const {
+    const uintptr_t rows = (uintptr_t)out | (uintptr_t)(a.D * Stor<ST>::kBytes);
+    return rows % 32 == 0 ? 32 : rows % 16 == 0 ? 16 : 1;
+  }
+
   cudaError_t backward() {
     cudaError_t e = rows();
     const int64_t dz_plane = p.Np * p.pitch, dh_plane = p.Np * p.Dh;
@@ -968,32 +1025,37 @@ struct HeadRun {
           !encode_matrix_map(&dz_k, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcRows) ||
           !encode_matrix_map(&dz_mn, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcK))
         return cudaErrorNotSupported;
-      if constexpr (Stor<ST>::kBytes == 2) {
-        const DzEpi<1> epi{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
-        e = launch_product<false, false, kGradGroup>(hidden_k, wk, in_place_k, logits_shape(v0, len), epi, sm, s);
+      using Dz = DzEpi<Stor<ST>::kBytes == 2 ? 1 : 3>;
+      const Dz dz{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
+      e = launch_product(TcJob<false, false, kGradGroup, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
+      if (e != cudaSuccess) break;
+      // d_hidden's sum over this piece's tokens, and its tokens' d_weight
+      TcShape sh = {}, sw = {};
+      sh.count = sw.count = w.count;
+      sh.terms = sw.terms = terms;
+      sh.band = sw.band = 16;
+      sh.count_axis = 1;
+      sh.m = (int)a.N; sh.n = (int)a.D; sh.k = (int)len;
+      sh.b_k0 = p.packed ? 0 : (int)v0;
+      sh.splits = p.splits;
+      sw.count_axis = 2;
+      sw.m = (int)len; sw.n = (int)a.D; sw.k = (int)a.N;
+      sw.splits = 1;
+      sw.other = hidden_ok ? 2 : 0; sw.full = (int)a.N;
+      const TcJob<false, true, kGradGroup, DhEpi<ST>> jh{
+          dz_k, wmn, wmn, sh,
+          {w.dh, p.Dh, dh_plane, v0 == 0, p.splits == 1 && v0 + len == a.V, a.d_hidden, w.rows, a.D, align_of(a.d_hidden)}};
+      const TcJob<true, true, kGradGroup, OutEpi<ST>> jw{
+          dz_mn, hidden_mn, in_place_mn, sw, {a.d_weight, v0, a.D, align_of(a.d_weight)}};
+      if (a.d_hidden && a.d_weight &&
+          together(tiles_of(sh), div_up(div_up(len, kTcK), p.splits), tiles_of(sw), div_up(a.N, kTcK), sm / 2)) {
+        e = launch_product(jh, jw, tiles_of(sh) + tiles_of(sw), sm, s);
       } else {
-        const DzEpi<3> epi{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
-        e = launch_product<false, false, kGradGroup>(hidden_k, wk, in_place_k, logits_shape(v0, len), epi, sm, s);
-      }
-      if (e == cudaSuccess && a.d_hidden) {
-        TcShape t = {};
-        t.count = w.count; t.count_axis = 1;
-        t.m = (int)a.N; t.n = (int)a.D; t.k = (int)len;
-        t.b_k0 = p.packed ? 0 : (int)v0;
-        t.splits = p.splits; t.band = 16; t.terms = terms;
-        e = launch_product<false, true, kGradGroup>(dz_k, wmn, wmn, t, SumEpi{w.dh, p.Dh, dh_plane, v0 > 0}, sm, s);
-      }
-      if (e == cudaSuccess && a.d_weight) {
-        TcShape t = {};
-        t.count = w.count; t.count_axis = 2;
-        t.m = (int)len; t.n = (int)a.D; t.k = (int)a.N;
-        t.splits = 1; t.band = 16; t.terms = terms;
-        t.other = hidden_ok ? 2 : 0; t.full = (int)a.N;
-        const uintptr_t rows = (uintptr_t)a.d_weight | (uintptr_t)(a.D * Stor<ST>::kBytes);
-        e = launch_product<true, true, kGradGroup>(dz_mn, hidden_mn, in_place_mn, t, OutEpi<ST>{a.d_weight, v0, a.D, rows % 32 == 0, rows % 16 == 0}, sm, s);
+        if (a.d_hidden) e = launch_product(jh, sm, s);
+        if (e == cudaSuccess && a.d_weight) e = launch_product(jw, sm, s);
       }
     }
-    if (e == cudaSuccess && a.d_hidden) {
+    if (e == cudaSuccess && a.d_hidden && p.splits > 1) {
       const bool vec = a.D % 4 == 0 && ((uintptr_t)a.d_hidden & 15) == 0;
       const int64_t grid = std::min<int64_t>(div_up(a.N * div_up(a.D, 4), kJoinThreads), 16 * (int64_t)sm);
       e = launch_pdl(head_dh_out_kernel<ST>, grid, kJoinThreads, 0, s, a, w, p.Dh, dh_plane, p.splits, vec);

@@ -37,6 +37,8 @@
 // waited for (bounded) before TMEM is freed and the cluster ends together.
 #pragma once
 
+#include <type_traits>
+
 #include "tma.cuh"
 
 namespace rlca {
@@ -44,10 +46,7 @@ namespace rlca {
 constexpr int kTcM = 256;      // rows of a tile, half of them each CTA's
 constexpr int kTcN = 256;      // columns of a tile; each CTA copies half of B's rows
 constexpr int kTcK = 64;       // k per stage: one 128-byte swizzle row of bfloat16
-#ifndef TCS
-#define TCS 6
-#endif
-constexpr int kTcStages = TCS;
+constexpr int kTcStages = 6;
 constexpr int kTcRows = kTcM / 2;  // rows a CTA loads and finishes
 constexpr int kTcEpiWarps = 8;
 constexpr int kTcThreads = 32 * (kTcEpiWarps + 4);  // two warps idle: register shares go by four warps
@@ -272,46 +271,246 @@ __device__ __forceinline__ int tc_group_end(int at, int stages, int terms) {
   return at < lead ? lead : min(at + GROUP, stages * terms);
 }
 
-// Epi: struct State; begin(State&, walk, tile, row, col0) with row = the
-// thread's row of C and col0 the first column of its half tile;
+// One product.  Epi: struct State; begin(State&, walk, tile, row, col0) with
+// row = the thread's row of C and col0 the first column of its half tile;
 // chunk(State&, col, v[32]) for the 32 columns from col on; end(State&).
 // Rows from walk.m on do not exist.
-template <bool A_MN, bool B_MN, int GROUP, class Epi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
-    tc_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_other, const __grid_constant__ TcShape s, const __grid_constant__ Epi epi) {
-  extern __shared__ unsigned char tc_smem_raw[];
+template <bool A_MN_, bool B_MN_, int GROUP_, class Epi_>
+struct TcJob {
+  using Epi = Epi_;
+  static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+  static constexpr int GROUP = GROUP_;
+  CUtensorMap a, b, other;
+  TcShape s;
+  Epi epi;
+};
+struct TcNoJob {};
+
+// what a CTA's roles share
+struct TcShared {
   // of the first CTA: full, acc_empty; of both: empty, acc_full, drained
-  __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drained;
-  __shared__ uint32_t tmem_base;
-  __shared__ volatile int stop;
+  uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drained;
+  uint32_t tmem_base;
+  volatile int stop;
+};
+
+// the ring of stages as a role sees it
+struct TcRing {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kTcStages) stage = 0, phase ^= 1;
+  }
+};
+// ... and the two accumulators
+struct TcAcc {
+  int buf = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    buf ^= 1;
+    if (buf == 0) phase ^= 1;
+  }
+};
+
+// Copies of one tile; false once a wait has given up.
+template <class Job>
+__device__ __forceinline__ bool tc_copy_tile(const Job& job, const TcWalk& walk, int64_t t, int rank, TcShared& sh,
+                                             unsigned char* ring, TcRing& r) {
+  const TcShape& s = job.s;
+  const bool other = s.other != 0 && walk.count == s.full;
+  const CUtensorMap* ma = other && s.other == 1 ? &job.other : &job.a;
+  const CUtensorMap* mb = other && s.other == 2 ? &job.other : &job.b;
+  const TcTile tile = walk.at(t, s);
+  const int m0 = s.a_m0 + tile.m0 + rank * kTcRows, n0 = s.b_n0 + tile.n0 + rank * (kTcN / 2);
+  for (int term = 0; term < s.terms.n; ++term) {
+    const int pa = s.terms.a[term], pb = s.terms.b[term];
+    for (int ks = tile.k_begin; ks < tile.k_end; ++ks) {
+      if (!tc_wait(&sh.empty[r.stage], r.phase ^ 1, &sh.stop)) return false;
+      unsigned char* sa = ring + r.stage * kTcStageBytes;
+      unsigned char* sb = sa + kTcABytes;
+      const uint32_t bar = in_first(&sh.full[r.stage]);
+      // both CTAs' bytes (the other's may land first: the phase ends with
+      // this arrival at the earliest)
+      if (rank == 0) mbar_arrive_expect_tx(&sh.full[r.stage], 2 * kTcStageBytes);
+      const int k0 = ks * kTcK;
+      if constexpr (Job::A_MN) {
+#pragma unroll
+        for (int i = 0; i < kTcRows / 64; ++i) tma_load_3d(sa + i * kTcK * 128, ma, m0 + 64 * i, k0, pa, bar);
+      } else {
+        tma_load_3d(sa, ma, k0, m0, pa, bar);
+      }
+      if constexpr (Job::B_MN) {
+#pragma unroll
+        for (int i = 0; i < kTcN / 2 / 64; ++i)
+          tma_load_3d(sb + i * kTcK * 128, mb, n0 + 64 * i, s.b_k0 + k0, pb, bar);
+      } else {
+        tma_load_3d(sb, mb, s.b_k0 + k0, n0, pb, bar);
+      }
+      r.next();
+    }
+  }
+  return true;
+}
+
+// Matrix instructions of one tile; false once a wait has given up.
+template <class Job>
+__device__ __forceinline__ bool tc_mma_tile(const Job& job, const TcWalk& walk, int64_t t, uint32_t tmem, TcShared& sh,
+                                            unsigned char* ring, TcRing& r, TcAcc& acc) {
+  const TcTile tile = walk.at(t, job.s);
+  const int stages = tile.k_end - tile.k_begin, steps = stages * job.s.terms.n;
+  // (no steps: the epilogue takes zeros and waits for nothing)
+  for (int at = 0; at < steps;) {
+    const int group_end = tc_group_end<Job::GROUP>(at, stages, job.s.terms.n);
+    if (!tc_wait(&sh.acc_empty[acc.buf], acc.phase ^ 1, &sh.stop)) return false;
+    tc_fence_after();
+    const uint32_t d = tmem + acc.buf * kTcN;
+    for (bool fresh = true; at < group_end; ++at) {
+      if (!tc_wait(&sh.full[r.stage], r.phase, &sh.stop)) return false;
+      tc_fence_after();
+      const uint32_t sa = smem_u32(ring + r.stage * kTcStageBytes);
+      const uint64_t da = tc_desc<Job::A_MN>(sa), db = tc_desc<Job::B_MN>(sa + kTcABytes);
+#pragma unroll
+      for (int k = 0; k < kTcK / 16; ++k)
+        tc_mma(d, da + k * kTcStepK<Job::A_MN>, db + k * kTcStepK<Job::B_MN>, kTcInstr<Job::A_MN, Job::B_MN>,
+               !fresh || k > 0);
+      fresh = false;
+      tc_commit(&sh.empty[r.stage]);
+      r.next();
+    }
+    tc_commit(&sh.acc_full[acc.buf]);
+    acc.next();
+  }
+  return true;
+}
+
+// Epilogue of one tile by the eight epilogue warps; false once a wait has
+// given up (one verdict for the warp: the TMEM loads need all its lanes).
+template <class Job>
+__device__ __forceinline__ bool tc_finish_tile(const Job& job, const TcWalk& walk, int64_t t, int rank, uint32_t tmem,
+                                               TcShared& sh, TcAcc& acc) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
+  const uint32_t src0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kTcN / 2);
+  const auto ready = [&] {
+    if (!__all_sync(0xffffffffu, tc_wait(&sh.acc_full[acc.buf], acc.phase, &sh.stop))) return false;
+    tc_fence_after();
+    return true;
+  };
+  const auto done = [&] {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_cluster(in_first(&sh.acc_empty[acc.buf]));
+    acc.next();
+  };
+  const TcTile tile = walk.at(t, job.s);
+  const int stages = tile.k_end - tile.k_begin, steps = stages * job.s.terms.n;
+  const int col0 = tile.n0 + half * (kTcN / 2);
+  typename Job::Epi::State st;
+  job.epi.begin(st, walk, tile, tile.m0 + rank * kTcRows + quarter * 32 + lane, col0);
+  if constexpr (Job::GROUP > 0) {
+    float sum[kTcN / 64][32];
+#pragma unroll
+    for (int c = 0; c < kTcN / 64; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+    for (int at = 0; at < steps; at = tc_group_end<Job::GROUP>(at, stages, job.s.terms.n)) {
+      if (!ready()) return false;
+#pragma unroll
+      for (int c = 0; c < kTcN / 64; ++c) {
+        tc_add16(src0 + acc.buf * kTcN + 32 * c, sum[c]);
+        tc_add16(src0 + acc.buf * kTcN + 32 * c + 16, sum[c] + 16);
+      }
+      done();
+    }
+#pragma unroll
+    for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c]);
+  } else {
+    float v[32], w[32];  // one is worked on while the other is loaded
+    if (steps > 0) {
+      if (!ready()) return false;
+      const uint32_t src = src0 + acc.buf * kTcN;
+      tc_load32(src, v);
+#pragma unroll 1
+      for (int c = 0; c < kTcN / 2; c += 64) {
+        tc_load_wait(v);
+        tc_load32(src + c + 32, w);
+        job.epi.chunk(st, col0 + c, v);
+        tc_load_wait(w);
+        if (c + 64 < kTcN / 2) tc_load32(src + c + 64, v);
+        else done();
+        job.epi.chunk(st, col0 + c + 32, w);
+      }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < kTcN / 2; c += 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        job.epi.chunk(st, col0 + c, v);
+      }
+    }
+  }
+  job.epi.end(st);
+  return true;
+}
+
+// The tiles of one product, or of two that do not depend on each other (the
+// second's after the first's), dealt to the clusters in turn.
+template <class Job1, class Job2>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    tc_product_kernel(const __grid_constant__ Job1 j1, const __grid_constant__ Job2 j2) {
+  constexpr bool two = !std::is_same_v<Job2, TcNoJob>;
+  constexpr int GROUP = Job1::GROUP;
+  extern __shared__ unsigned char tc_smem_raw[];
+  __shared__ __align__(8) TcShared sh;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)tc_smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   pdl_trigger();
-  if (warp == kTcEpiWarps + 1) tc_alloc(&tmem_base, 2 * kTcN);
+  if (warp == kTcEpiWarps + 1) tc_alloc(&sh.tmem_base, 2 * kTcN);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTcStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 2 * kTcEpiWarps);
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_empty[i], 2 * kTcEpiWarps);
     }
-    mbar_init(&drained, 1);
-    stop = 0;
+    mbar_init(&sh.drained, 1);
+    sh.stop = 0;
     mbar_fence_init();
+  }
+  if (threadIdx.x == 32 * kTcEpiWarps) {
+    tma_prefetch_map(&j1.a);
+    tma_prefetch_map(&j1.b);
+    if constexpr (two) {
+      tma_prefetch_map(&j2.a);
+      tma_prefetch_map(&j2.b);
+    }
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = sh.tmem_base;
   pdl_wait();
-  const TcWalk walk(s);
+  const TcWalk w1(j1.s);
+  const auto second = [&] {
+    if constexpr (two) return TcWalk(j2.s);
+    else return w1;
+  };
+  const TcWalk w2 = second();
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1, end = w1.tiles + (two ? w2.tiles : 0);
+  // f(job, walk, tile) for this cluster's tiles until it returns false
+  const auto each_tile = [&](auto&& f) {
+    for (int64_t t = first; t < end; t += step) {
+      if (t < w1.tiles) {
+        if (!f(j1, w1, t)) return;
+      } else if constexpr (two) {
+        if (!f(j2, w2, t - w1.tiles)) return;
+      }
+    }
+  };
 
   // (without partial sums the launch's 168 registers are enough)
   if (warp >= kTcEpiWarps + 2) {
@@ -323,174 +522,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (lane == 0) {
       // operands written by earlier kernels' ordinary stores, read by copies
       asm volatile("fence.proxy.async;" ::: "memory");
-      const bool other = s.other != 0 && walk.count == s.full;
-      const CUtensorMap* ma = other && s.other == 1 ? &map_other : &map_a;
-      const CUtensorMap* mb = other && s.other == 2 ? &map_other : &map_b;
-      tma_prefetch_map(ma);
-      tma_prefetch_map(mb);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int64_t t = first; t < walk.tiles && ok; t += step) {
-        const TcTile tile = walk.at(t, s);
-        const int m0 = s.a_m0 + tile.m0 + rank * kTcRows, n0 = s.b_n0 + tile.n0 + rank * (kTcN / 2);
-        for (int term = 0; term < s.terms.n && ok; ++term) {
-          const int pa = s.terms.a[term], pb = s.terms.b[term];
-          for (int ks = tile.k_begin; ks < tile.k_end; ++ks) {
-            if (!tc_wait(&empty[stage], phase ^ 1, &stop)) {
-              ok = false;
-              break;
-            }
-            unsigned char* sa = ring + stage * kTcStageBytes;
-            unsigned char* sb = sa + kTcABytes;
-            const uint32_t bar = in_first(&full[stage]);
-            // both CTAs' bytes (the other's may land first: the phase ends
-            // with this arrival at the earliest)
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kTcStageBytes);
-            const int k0 = ks * kTcK;
-            if constexpr (A_MN) {
-#pragma unroll
-              for (int i = 0; i < kTcRows / 64; ++i)
-                tma_load_3d(sa + i * kTcK * 128, ma, m0 + 64 * i, k0, pa, bar);
-            } else {
-              tma_load_3d(sa, ma, k0, m0, pa, bar);
-            }
-            if constexpr (B_MN) {
-#pragma unroll
-              for (int i = 0; i < kTcN / 2 / 64; ++i)
-                tma_load_3d(sb + i * kTcK * 128, mb, n0 + 64 * i, s.b_k0 + k0, pb, bar);
-            } else {
-              tma_load_3d(sb, mb, s.b_k0 + k0, n0, pb, bar);
-            }
-            if (++stage == kTcStages) stage = 0, phase ^= 1;
-          }
-        }
-      }
+      TcRing r;
+      each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_copy_tile(job, w, t, rank, sh, ring, r); });
       // Every copy that was issued lands before the cluster ends (when all
       // went well the matrix instructions have waited for it too).  Stage i
-      // was last filled in `phase` if i < stage, else in the phase before, or
-      // never: that wait returns at once.
+      // was last filled in r.phase if i < r.stage, else in the phase before,
+      // or never: that wait returns at once.
       if (rank == 0)
-        for (int i = 0; i < kTcStages; ++i) mbar_wait_bounded(&full[i], i < stage ? phase : phase ^ 1);
+        for (int i = 0; i < kTcStages; ++i) mbar_wait_bounded(&sh.full[i], i < r.stage ? r.phase : r.phase ^ 1);
     }
   } else if (warp == kTcEpiWarps + 1) {
     // ---- matrix instructions ----
     if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
     if (lane == 0 && rank == 0) {
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int64_t t = first; t < walk.tiles && ok; t += step) {
-        const TcTile tile = walk.at(t, s);
-        const int steps = (tile.k_end - tile.k_begin) * s.terms.n;
-        // (no steps: the epilogue takes zeros and waits for nothing)
-        for (int at = 0; at < steps && ok;) {
-          const int group_end = tc_group_end<GROUP>(at, tile.k_end - tile.k_begin, s.terms.n);
-          if (!tc_wait(&acc_empty[buf], acc_phase ^ 1, &stop)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + buf * kTcN;
-          for (bool fresh = true; at < group_end; ++at) {
-            if (!tc_wait(&full[stage], phase, &stop)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sa = smem_u32(ring + stage * kTcStageBytes);
-            const uint64_t da = tc_desc<A_MN>(sa), db = tc_desc<B_MN>(sa + kTcABytes);
-#pragma unroll
-            for (int k = 0; k < kTcK / 16; ++k)
-              tc_mma(d, da + k * kTcStepK<A_MN>, db + k * kTcStepK<B_MN>, kTcInstr<A_MN, B_MN>, !fresh || k > 0);
-            fresh = false;
-            tc_commit(&empty[stage]);
-            if (++stage == kTcStages) stage = 0, phase ^= 1;
-          }
-          if (!ok) break;
-          tc_commit(&acc_full[buf]);
-          buf ^= 1;
-          if (buf == 0) acc_phase ^= 1;
-        }
-      }
+      TcRing r;
+      TcAcc acc;
+      each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_mma_tile(job, w, t, tmem, sh, ring, r, acc); });
       // whatever was issued completes before TMEM is freed
-      tc_commit(&drained);
-      mbar_wait_bounded(&drained, 0);
+      tc_commit(&sh.drained);
+      mbar_wait_bounded(&sh.drained, 0);
     }
   } else {
     // ---- epilogue ----
     if constexpr (GROUP > 0) regs_take<kTcEpiRegs>();
-    const int quarter = warp & 3, half = warp >> 2;
-    int buf = 0;
-    uint32_t acc_phase = 0;
-    const uint32_t src0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kTcN / 2);
-    // false once a wait has given up (one verdict for the warp: the TMEM
-    // loads need all its lanes)
-    const auto acc_ready = [&] {
-      if (!__all_sync(0xffffffffu, tc_wait(&acc_full[buf], acc_phase, &stop))) return false;
-      tc_fence_after();
-      return true;
-    };
-    const auto acc_done = [&] {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(in_first(&acc_empty[buf]));
-      buf ^= 1;
-      if (buf == 0) acc_phase ^= 1;
-    };
-    for (int64_t t = first; t < walk.tiles; t += step) {
-      const TcTile tile = walk.at(t, s);
-      const int steps = (tile.k_end - tile.k_begin) * s.terms.n;
-      const int col0 = tile.n0 + half * (kTcN / 2);
-      typename Epi::State st;
-      epi.begin(st, walk, tile, tile.m0 + rank * kTcRows + quarter * 32 + lane, col0);
-      bool ok = true;
-      if constexpr (GROUP > 0) {
-        float sum[kTcN / 64][32];
-#pragma unroll
-        for (int c = 0; c < kTcN / 64; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-        for (int at = 0; at < steps; at = tc_group_end<GROUP>(at, tile.k_end - tile.k_begin, s.terms.n)) {
-          ok = acc_ready();
-          if (!ok) break;
-#pragma unroll
-          for (int c = 0; c < kTcN / 64; ++c) {
-            tc_add16(src0 + buf * kTcN + 32 * c, sum[c]);
-            tc_add16(src0 + buf * kTcN + 32 * c + 16, sum[c] + 16);
-          }
-          acc_done();
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < kTcN / 64; ++c) epi.chunk(st, col0 + 32 * c, sum[c]);
-      } else {
-        if (steps > 0 && !acc_ready()) break;
-        const uint32_t src = src0 + buf * kTcN;
-        float v[32], w[32];  // one is worked on while the other is loaded
-        if (steps > 0) {
-          tc_load32(src, v);
-#pragma unroll 1
-          for (int c = 0; c < kTcN / 2; c += 64) {
-            tc_load_wait(v);
-            tc_load32(src + c + 32, w);
-            epi.chunk(st, col0 + c, v);
-            tc_load_wait(w);
-            if (c + 64 < kTcN / 2) tc_load32(src + c + 64, v);
-            else acc_done();
-            epi.chunk(st, col0 + c + 32, w);
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kTcN / 2; c += 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            epi.chunk(st, col0 + c, v);
-          }
-        }
-      }
-      epi.end(st);
-    }
+    TcAcc acc;
+    each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_finish_tile(job, w, t, rank, tmem, sh, acc); });
   }
   __syncwarp();
   tc_fence_before();
