@@ -16,6 +16,7 @@
 
 #include "policy.h"
 #include "reduce.cuh"
+#include "tma.cuh"
 
 namespace rlca {
 
@@ -316,6 +317,124 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
   }
 }
 
+// The same for rows of a CTA of their own, fed by bulk copies: thread 0 keeps
+// kRingRows - 1 rows of x and dy on their way into shared memory, so what is
+// in flight does not depend on the registers that the columns' sums leave.  A
+// stage is filled again after the barrier that follows its reads (the one the
+// row's sums need anyway).  A wait that gives up is recorded in the status
+// word; the rows are then walked without further copies or waits.
+constexpr int kRingRows = 4;
+
+template <class ST, int VE, int VPT, int TPR>
+__global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_ring_kernel(NormGradArgs a) {
+  using P = Pack<ST, VE>;
+  extern __shared__ __align__(128) unsigned char ring_rows[];  // [kRingRows][x, dy][D]
+  __shared__ __align__(8) uint64_t full[kRingRows];
+  __shared__ float scratch[2][2][32];
+  const int lane = threadIdx.x, warp = lane >> 5, l = lane & 31;
+  const int nv = (int)(a.D / VE);
+  const uint32_t row_bytes = (uint32_t)(a.D * Stor<ST>::kBytes);
+  const float inv_d = 1.f / (float)a.D;
+  const int64_t step = gridDim.x;
+  pdl_trigger();
+  if (lane == 0) {
+    for (int i = 0; i < kRingRows; ++i) mbar_init(&full[i], 1);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_wait();
+
+  const auto fill = [&](int stage, int64_t row) {
+    unsigned char* to = ring_rows + (size_t)stage * 2 * row_bytes;
+    mbar_arrive_expect_tx(&full[stage], 2 * row_bytes);
+    bulk_load(to, reinterpret_cast<const unsigned char*>(a.x) + row * a.x_stride * Stor<ST>::kBytes, row_bytes, &full[stage]);
+    bulk_load(to + row_bytes, reinterpret_cast<const unsigned char*>(a.dy) + row * a.dy_stride * Stor<ST>::kBytes, row_bytes,
+              &full[stage]);
+  };
+  int64_t row = blockIdx.x;
+  if (lane == 0) {
+    for (int i = 0; i < kRingRows - 1; ++i)
+      if (row + i * step < a.N) fill(i, row + i * step);
+  }
+  typename P::Raw w[VPT];
+  float dw[VPT][VE], db[VPT][VE];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = lane + j * TPR;
+    w[j] = v < nv ? P::load(a.weight, (int64_t)v * VE) : P::zero();
+#pragma unroll
+    for (int e = 0; e < VE; ++e) dw[j][e] = db[j][e] = 0.f;
+  }
+  float mean = 0.f, rstd = 0.f;
+  if (row < a.N) mean = a.mean[row], rstd = a.rstd[row];
+  int stage = 0, slot = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (; row < a.N; row += step) {
+    // the stage before this one was read in the last round
+    if (lane == 0 && ok && row + (kRingRows - 1) * step < a.N)
+      fill(stage == 0 ? kRingRows - 1 : stage - 1, row + (kRingRows - 1) * step);
+    if (ok) ok = mbar_wait_bounded(&full[stage], phase);
+    const unsigned char* at = ring_rows + (size_t)stage * 2 * row_bytes;
+    float xh[VPT][VE], g[VPT][VE];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = lane + j * TPR;
+      const bool on = v < nv;
+      typename P::Raw x = P::zero(), dy = P::zero();
+      if (on) {
+        x = *reinterpret_cast<const typename P::Raw*>(at + v * 16);
+        dy = *reinterpret_cast<const typename P::Raw*>(at + row_bytes + v * 16);
+      }
+      float fw[VE];
+      P::open(x, xh[j]);
+      P::open(dy, g[j]);
+      P::open(w[j], fw);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        xh[j][e] = on ? (xh[j][e] - mean) * rstd : 0.f;
+        dw[j][e] = fmaf(g[j][e], xh[j][e], dw[j][e]);
+        db[j][e] += g[j][e];
+        g[j][e] *= fw[e];
+        s1 += g[j][e];
+        s2 = fmaf(g[j][e], xh[j][e], s2);
+      }
+    }
+    const float r = rstd;
+    if (row + step < a.N) mean = a.mean[row + step], rstd = a.rstd[row + step];
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (l == 0) scratch[slot][0][warp] = s1, scratch[slot][1][warp] = s2;
+    __syncthreads();
+    s1 = warp_sum(l < TPR / 32 ? scratch[slot][0][l] : 0.f) * inv_d;
+    s2 = warp_sum(l < TPR / 32 ? scratch[slot][1][l] : 0.f) * inv_d;
+    slot ^= 1;
+    if (++stage == kRingRows) stage = 0, phase ^= 1;
+    if (a.dx == nullptr) continue;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = lane + j * TPR;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) g[j][e] = r * (g[j][e] - s1 - xh[j][e] * s2);
+      if (v < nv) P::store(a.dx, row * a.D + (int64_t)v * VE, g[j]);
+    }
+  }
+  // (copies still on their way after a wait gave up land before the CTA ends)
+  if (!ok && lane == 0)
+    for (int i = 0; i < kRingRows; ++i) mbar_wait_bounded(&full[i], i < stage ? phase ^ 1 : phase);
+  if (a.dweight == nullptr && a.dbias == nullptr) return;
+  float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = lane + j * TPR;
+    if (v < nv) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) out[v * VE + e] = dw[j][e], out[a.D + v * VE + e] = db[j][e];
+    }
+  }
+}
+
 // rows too long for registers
 template <class ST>
 __global__ void __launch_bounds__(kLongThreads) norm_grad_long_kernel(NormGradArgs a) {
@@ -377,8 +496,16 @@ __global__ void __launch_bounds__(1024)
   if (out == nullptr) return;
   const int64_t c = (blockIdx.x - which * col_blocks) * 32 + lane;
   float s = 0.f;
-  if (c < D)
-    for (int64_t k = warp; k < parts; k += 32) s += ws[(2 * k + which) * D + c];
+  if (c < D) {
+    constexpr int B = 8;  // loads in flight
+    for (int64_t k0 = warp; k0 < parts; k0 += 32 * B) {
+      float v[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) v[u] = k0 + 32 * u < parts ? __ldg(ws + (2 * (k0 + 32 * u) + which) * D + c) : 0.f;
+#pragma unroll
+      for (int u = 0; u < B; ++u) s += v[u];
+    }
+  }
   acc[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= D) return;
@@ -432,9 +559,12 @@ cudaError_t norm_typed(const NormArgs& a, int sm, cudaStream_t s) {
   return launch_pdl(norm_long_kernel<ST>, a.N, kLongThreads, 0, s, a);
 }
 
-// CTAs of a backward launch of T threads, R rows at a time
+// CTAs of a backward launch of T threads, R rows at a time: those that fit
+// the SMs, but four rounds of rows each where that still gives every SM one
+// (each CTA leaves 2 D partial sums to be joined)
 int64_t grad_grid(int64_t N, int T, int R, int values, int sm) {
-  return std::min<int64_t>(div_up(N, R), (int64_t)grad_resident(T, values) * sm);
+  const int64_t rounds = div_up(N, R);
+  return std::min({rounds, (int64_t)grad_resident(T, values) * sm, std::max<int64_t>(sm, div_up(rounds, 4))});
 }
 
 cudaError_t join(const NormGradArgs& a, int64_t parts, cudaStream_t s) {
@@ -448,6 +578,18 @@ cudaError_t launch_grad(const NormGradArgs& a, int sm, cudaStream_t s) {
   constexpr int T = cta_threads(TPR);
   const int64_t grid = grad_grid(a.N, T, T / TPR, VPT * VE, sm);
   const cudaError_t e = launch_pdl(norm_grad_kernel<ST, VE, VPT, TPR>, grid, T, 0, s, a);
+  return e == cudaSuccess ? join(a, grid, s) : e;
+}
+
+template <class ST, int VE, int VPT, int TPR>
+cudaError_t launch_grad_ring(const NormGradArgs& a, int sm, cudaStream_t s) {
+  const size_t smem = (size_t)kRingRows * 2 * a.D * Stor<ST>::kBytes;
+  const auto kernel = norm_grad_ring_kernel<ST, VE, VPT, TPR>;
+  static std::atomic<uint64_t> allowed;
+  cudaError_t e = allow_smem(kernel, (size_t)kRingRows * 2 * TPR * VPT * 16, allowed);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = grad_grid(a.N, TPR, 1, VPT * VE, sm);
+  e = launch_pdl(kernel, grid, TPR, smem, s, a);
   return e == cudaSuccess ? join(a, grid, s) : e;
 }
 
@@ -465,10 +607,10 @@ cudaError_t grad_typed(const NormGradArgs& a, int sm, cudaStream_t s) {
     const int64_t nv = a.D / VE;
     if (nv <= 32) return launch_grad<ST, VE, 1, 32>(a, sm, s);
     if (nv <= 64) return launch_grad<ST, VE, 2, 32>(a, sm, s);
-    if (nv <= 128) return launch_grad<ST, VE, 1, 128>(a, sm, s);
-    if (nv <= 256) return launch_grad<ST, VE, 2, 128>(a, sm, s);
-    if (nv <= 512) return launch_grad<ST, VE, 2, 256>(a, sm, s);
-    if (nv <= 1024) return launch_grad<ST, VE, 2, 512>(a, sm, s);
+    if (nv <= 128) return launch_grad_ring<ST, VE, 1, 128>(a, sm, s);
+    if (nv <= 256) return launch_grad_ring<ST, VE, 2, 128>(a, sm, s);
+    if (nv <= 512) return launch_grad_ring<ST, VE, 2, 256>(a, sm, s);
+    if (nv <= 1024) return launch_grad_ring<ST, VE, 2, 512>(a, sm, s);
   } else {
     if (a.D <= 32) return launch_grad<ST, 1, 1, 32>(a, sm, s);
     if (a.D <= 256) return launch_grad<ST, 1, 8, 32>(a, sm, s);
