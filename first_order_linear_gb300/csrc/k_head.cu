@@ -29,7 +29,7 @@ namespace {
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // dz of one piece of the vocabulary
 constexpr int64_t kPackBytes = int64_t(128) << 20;   // packed weight of one piece
 constexpr int64_t kSplitBytes = int64_t(64) << 20;   // d_hidden's partial sums beyond the first
-constexpr int64_t kWholeStages = 20;                  // k stages of a d_hidden sum that is not split
+constexpr int64_t kWholeStages = 24;                  // k stages (times terms) of a d_hidden sum that is not split
 constexpr int64_t kSplitStages = 8;                   // ... and at least this many a split
 constexpr int64_t kBandBytes = int64_t(48) << 20;    // hidden rows walked together (well inside L2)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -49,6 +49,7 @@ struct HeadPlan {
   int64_t piece;    // tokens per piece (whole tiles unless it is the whole vocabulary)
   int64_t pitch;    // of dz and of the column of partial statistics: piece in whole tiles
   int row_tiles, d_tiles, splits;
+  bool two_dz;      // dz as two bfloat16 values (their sum), the second's rows after the first's
   size_t count, rows, tok, info, hidden, weight, part, taken, dz, dh;  // byte offsets
   size_t bytes;
 };
@@ -62,6 +63,7 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
   p.Dh = round_up(D, 32);
   p.row_tiles = (int)(p.Np / kTcM);
   p.d_tiles = (int)div_up(D, kTcN);
+  p.two_dz = backward && bf16_io && N <= kTcRows;
   const int64_t tiles = div_up(V, kTcN);
   int64_t piece_tiles = tiles;
   if (packed) piece_tiles = std::min(piece_tiles, std::max<int64_t>(1, kPackBytes / (2 * p.planes * p.Dp * kTcN)));
@@ -84,16 +86,16 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
     p.dz = take((size_t)p.planes * p.Np * p.pitch * 2);
     // d_hidden has few tiles when there are few rows: its sum over tokens is
     // then split until the tiles fill the CTA pairs -- unless a whole sum is
-    // no longer than the kernel that joins the splits (0.27 us a stage
+    // hardly longer than the kernel that joins the splits (0.27 us a stage
     // against 5 to 6 us)
     const int64_t out_tiles = (int64_t)p.row_tiles * p.d_tiles, out_bytes = p.Np * p.Dh * 4;
     const int64_t stages = div_up(p.piece, kTcK);
     p.splits = 1;
-    if (stages > kWholeStages || piece_tiles < tiles)
+    if ((p.two_dz ? 2 : 1) * stages > kWholeStages || piece_tiles < tiles)
       p.splits = (int)std::max<int64_t>(
           1, std::min({(int64_t)sm_count / 2 / out_tiles, 1 + kSplitBytes / out_bytes, div_up(stages, kSplitStages)}));
     // (one piece, not split: the product writes d_hidden itself)
-    if (p.splits > 1 || piece_tiles < tiles) p.dh = take((size_t)p.splits * out_bytes);
+    if (p.splits > 1 || piece_tiles < tiles) p.dh = take((size_t)(p.two_dz ? 2 : 1) * p.splits * out_bytes);
   } else {
     // (head_few_kernel: one piece a CTA, of at most 8 rows)
     p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 8) * sizeof(float4));
@@ -226,14 +228,14 @@ __global__ void __launch_bounds__(kPackThreads)
       at += k < warp ? scratch[k] : 0;
       n += scratch[k];
     }
-    if (on) {
+    if (on && in_range(before + at, a.N)) {
       list[at] = (int)i;
       w.rows[before + at] = (int)i;
       w.tok[before + at] = tok;
       if (a.d_logp != nullptr)
         w.info[before + at] = make_float4(a.d_logp[i], a.d_entropy ? a.d_entropy[i] : 0.f, a.in_lse[i],
                                           a.d_entropy ? a.in_entropy[i] : 0.f);
-    } else if (i < r1) {
+    } else if (!on && i < r1) {
       list[kPackThreads - 1 - ((int)(i - i0) - at)] = (int)i;  // from the end: those that do not
       if (a.logp != nullptr) {
         a.logp[i] = 0.f;
@@ -360,7 +362,7 @@ struct StatsEpi {
   float4* part;
   float* taken;
   const int* tok;
-  int64_t Np;
+  int64_t Np, halves;
   int v0, v_end;  // tokens of this piece
   float c2;
 
@@ -414,34 +416,42 @@ struct StatsEpi {
       float z = v[0];
 #pragma unroll
       for (int i = 1; i < 32; ++i) z = i == k ? v[i] : z;
-      taken[st.m] = z;
+      if (in_range(st.m, Np)) taken[st.m] = z;
     }
   }
   __device__ __forceinline__ void end(State& st) const {
-    if (st.live) part[(int64_t)((v0 + st.col0) / (kTcN / 2)) * Np + st.m] = make_float4(st.top, st.s, st.t, 0.f);
+    const int64_t at = (int64_t)((v0 + st.col0) / (kTcN / 2)) * Np + st.m;
+    if (st.live && in_range(at, halves * Np)) part[at] = make_float4(st.top, st.s, st.t, 0.f);
   }
 };
 
-// dz = p (a0 + a1 acc), plus g / temperature for the token taken, as one
-// bfloat16 (rounded once: the two products that read it run on bfloat16) or
-// as three planes
+// dz = p (a0 + a1 acc), plus g / temperature for the token taken: as three
+// planes where the operands are float32; for bfloat16 operands as one
+// bfloat16, rounded once because the two products that read it run on
+// bfloat16 -- its error of 2^-9 a term is as large as the rounding of the
+// gradients themselves, and adds to it.  Up to 128 rows a second bfloat16
+// takes what the first left over, in rows 128 further on: half of each 256-row
+// tile would be empty otherwise, and with few rows the errors of single terms
+// (the tokens taken) do not average out.
 template <int PLANES>
 struct DzEpi {
   uint16_t* dz;
-  int64_t pitch, plane;
+  int64_t pitch, plane, size;  // size: of all planes
   const float4* info;
   const int* tok;
   int v0;
   float inv_t;
+  bool two;
 
   struct State {
     float lse2, a0, a1, g;
     int at;
-    bool live;
+    bool live, skip;
     uint16_t* row;
   };
   __device__ __forceinline__ void begin(State& st, const TcWalk& w, const TcTile&, int row, int) const {
     st.live = row < w.m;
+    st.skip = two && row >= kTcRows;  // the second values' rows
     st.row = dz + (int64_t)row * pitch;
     st.at = -1;
     st.lse2 = st.a0 = st.a1 = st.g = 0.f;
@@ -455,6 +465,7 @@ struct DzEpi {
     }
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
+    if (st.skip) return;
     const float c2 = inv_t * kLog2e;
     const int k = st.at - col;
     const uint64_t c22 = pair_of(c2, c2), l2 = pair_of(st.lse2, st.lse2);
@@ -475,9 +486,17 @@ struct DzEpi {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0.f;
     }
+    const int64_t at = (st.row - dz) + col;
+    if (!span_in_range(at, 32 + (two ? kTcRows * pitch : (PLANES - 1) * plane), size)) return;
     if constexpr (PLANES == 1) {
       store16(st.row + col, v);
       store16(st.row + col + 16, v + 16);
+      if (two) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+        store16(st.row + kTcRows * pitch + col, v);
+        store16(st.row + kTcRows * pitch + col + 16, v + 16);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 32; i += 16) {
@@ -531,16 +550,18 @@ __device__ __forceinline__ void store_row32(float* out, int64_t at, int64_t col,
 // d_hidden.  The sum over the pieces of the vocabulary is kept in float32
 // (`sums`, one plane a split), set by the first piece and added to by the
 // others; without splits the last piece writes the result itself, to the
-// part's row.
+// part's row.  halves: rows 128 on are the sums with dz's second values, a
+// plane of their own.
 template <class ST>
 struct DhEpi {
-  float* sums;  // splits x [rows, pitch]
-  int64_t pitch, plane;
+  float* sums;  // planes x [rows, pitch], `size` in all
+  int64_t pitch, plane, size;
   bool first, last;
   float* out;  // [N, width], type ST
   const int* rows;
-  int64_t width;
+  int64_t N, width;
   int align;
+  bool halves;
 
   struct State {
     float* sum;
@@ -548,12 +569,14 @@ struct DhEpi {
     bool live;
   };
   __device__ __forceinline__ void begin(State& st, const TcWalk& w, const TcTile& t, int row, int) const {
-    st.live = row < w.m;
-    st.sum = sums + t.split * plane + (int64_t)row * pitch;
-    st.at = last && st.live ? rows[row] * width : 0;
+    const int part = halves ? row % kTcRows : row;
+    st.live = part < w.count;
+    st.sum = sums + (halves ? 2 * t.split + row / kTcRows : t.split) * plane + (int64_t)part * pitch;
+    st.at = last && st.live ? rows[part] * width : 0;
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
     if (!st.live || col >= pitch) return;
+    if (!(first && last) && !span_in_range(st.sum - sums + col, 32, size)) return;
     if (!first) {
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
@@ -562,7 +585,7 @@ struct DhEpi {
       }
     }
     if (last) {
-      store_row32<ST>(out, st.at, col, width, align, v);
+      if (in_range(st.at, N * width)) store_row32<ST>(out, st.at, col, width, align, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
@@ -579,8 +602,8 @@ struct DhEpi {
 // d_weight, rounded once
 template <class ST>
 struct OutEpi {
-  float* out;  // [.., width], element type ST
-  int64_t row0, width;
+  float* out;  // [V, width], element type ST
+  int64_t row0, width, V;
   int align;
 
   struct State {
@@ -592,7 +615,7 @@ struct OutEpi {
     st.at = (row0 + row) * width;
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
-    if (st.live) store_row32<ST>(out, st.at, col, width, align, v);
+    if (st.live && in_range(st.at, V * width)) store_row32<ST>(out, st.at, col, width, align, v);
   }
   __device__ __forceinline__ void end(State&) const {}
 };
@@ -971,7 +994,7 @@ struct HeadRun {
       if (e != cudaSuccess) break;
       CUtensorMap wk;
       if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
-      const StatsEpi epi{w.part, w.taken, w.tok, p.Np, (int)v0, (int)(v0 + len), c2};
+      const StatsEpi epi{w.part, w.taken, w.tok, p.Np, div_up(a.V, kTcN) * 2, (int)v0, (int)(v0 + len), c2};
       e = launch_product(TcJob<false, false, kLogitsGroup, StatsEpi>{hidden_k, wk, in_place_k, logits_shape(v0, len), epi},
                          sm, s);
     }
@@ -1015,27 +1038,36 @@ struct HeadRun {
 
   cudaError_t backward() {
     cudaError_t e = rows();
-    const int64_t dz_plane = p.Np * p.pitch, dh_plane = p.Np * p.Dh;
+    // (with two values: planes of kTcRows rows in one tile)
+    const int64_t dz_rows = p.two_dz ? kTcRows : p.Np, dz_plane = dz_rows * p.pitch, dh_plane = p.Np * p.Dh;
+    const int dz_planes = p.two_dz ? 2 : p.planes;
+    // d_hidden's sum takes the second values as rows of their own where the
+    // splits' sums are joined anyway, else as a second term; d_weight as a
+    // second term
+    const bool halves = p.two_dz && p.splits > 1;
+    TcTerms dz_terms = terms;
+    if (p.two_dz) dz_terms.n = 2, dz_terms.a[0] = 1, dz_terms.a[1] = 0;
     for (int64_t v0 = 0; v0 < a.V && e == cudaSuccess; v0 += p.piece) {
       const int64_t len = std::min(p.piece, a.V - v0);
       e = weight_piece(v0, len);
       if (e != cudaSuccess) break;
       CUtensorMap wk, wmn, dz_k, dz_mn;
       if (!weight_map(&wk, len, kTcN / 2) || !weight_map(&wmn, len, kTcK) ||
-          !encode_matrix_map(&dz_k, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcRows) ||
-          !encode_matrix_map(&dz_mn, w.dz, len, p.Np, p.planes, p.pitch, dz_plane, kTcK))
+          !encode_matrix_map(&dz_k, w.dz, len, halves ? p.Np : dz_rows, halves ? 1 : dz_planes, p.pitch, dz_plane, kTcRows) ||
+          !encode_matrix_map(&dz_mn, w.dz, len, dz_rows, dz_planes, p.pitch, dz_plane, kTcK))
         return cudaErrorNotSupported;
       using Dz = DzEpi<Stor<ST>::kBytes == 2 ? 1 : 3>;
-      const Dz dz{w.dz, p.pitch, dz_plane, w.info, w.tok, (int)v0, a.inv_temperature};
+      const Dz dz{w.dz, p.pitch, dz_plane, dz_planes * dz_plane, w.info, w.tok, (int)v0, a.inv_temperature, p.two_dz};
       e = launch_product(TcJob<false, false, kGradGroup, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
       if (e != cudaSuccess) break;
       // d_hidden's sum over this piece's tokens, and its tokens' d_weight
       TcShape sh = {}, sw = {};
       sh.count = sw.count = w.count;
-      sh.terms = sw.terms = terms;
+      sw.terms = dz_terms;
+      sh.terms = halves ? terms : dz_terms;
       sh.band = sw.band = 16;
-      sh.count_axis = 1;
-      sh.m = (int)a.N; sh.n = (int)a.D; sh.k = (int)len;
+      sh.count_axis = halves ? 0 : 1;
+      sh.m = halves ? kTcM : (int)a.N; sh.n = (int)a.D; sh.k = (int)len;
       sh.b_k0 = p.packed ? 0 : (int)v0;
       sh.splits = p.splits;
       sw.count_axis = 2;
@@ -1044,11 +1076,13 @@ struct HeadRun {
       sw.other = hidden_ok ? 2 : 0; sw.full = (int)a.N;
       const TcJob<false, true, kGradGroup, DhEpi<ST>> jh{
           dz_k, wmn, wmn, sh,
-          {w.dh, p.Dh, dh_plane, v0 == 0, p.splits == 1 && v0 + len == a.V, a.d_hidden, w.rows, a.D, align_of(a.d_hidden)}};
+          {w.dh, p.Dh, dh_plane, (halves ? 2 : 1) * p.splits * dh_plane, v0 == 0, p.splits == 1 && v0 + len == a.V, a.d_hidden,
+           w.rows, a.N, a.D, align_of(a.d_hidden), halves}};
       const TcJob<true, true, kGradGroup, OutEpi<ST>> jw{
-          dz_mn, hidden_mn, in_place_mn, sw, {a.d_weight, v0, a.D, align_of(a.d_weight)}};
+          dz_mn, hidden_mn, in_place_mn, sw, {a.d_weight, v0, a.D, a.V, align_of(a.d_weight)}};
       if (a.d_hidden && a.d_weight &&
-          together(tiles_of(sh), div_up(div_up(len, kTcK), p.splits), tiles_of(sw), div_up(a.N, kTcK), sm / 2)) {
+          together(tiles_of(sh), div_up(div_up(len, kTcK), p.splits) * sh.terms.n, tiles_of(sw), div_up(a.N, kTcK) * sw.terms.n,
+                   sm / 2)) {
         e = launch_product(jh, jw, tiles_of(sh) + tiles_of(sw), sm, s);
       } else {
         if (a.d_hidden) e = launch_product(jh, sm, s);
@@ -1058,7 +1092,7 @@ struct HeadRun {
     if (e == cudaSuccess && a.d_hidden && p.splits > 1) {
       const bool vec = a.D % 4 == 0 && ((uintptr_t)a.d_hidden & 15) == 0;
       const int64_t grid = std::min<int64_t>(div_up(a.N * div_up(a.D, 4), kJoinThreads), 16 * (int64_t)sm);
-      e = launch_pdl(head_dh_out_kernel<ST>, grid, kJoinThreads, 0, s, a, w, p.Dh, dh_plane, p.splits, vec);
+      e = launch_pdl(head_dh_out_kernel<ST>, grid, kJoinThreads, 0, s, a, w, p.Dh, dh_plane, (halves ? 2 : 1) * p.splits, vec);
     }
     return e;
   }

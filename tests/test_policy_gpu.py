@@ -169,6 +169,12 @@ def test_head_several_pieces_of_the_vocabulary(dtype):
     check_head(3000, 40, 70001, DT[dtype], seed=3, mask=0.2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_head_many_rows(dtype):
+    """More rows than the first kernel's CTAs take in one round."""
+    check_head(200003, 8, 20, DT[dtype], seed=8, mask=0.3, junk=True)
+
+
 def test_head_on_another_stream():
     check_head(150, 96, 600, torch.bfloat16, seed=5, stream=torch.cuda.Stream())
 
