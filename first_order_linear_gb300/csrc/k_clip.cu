@@ -12,19 +12,22 @@ namespace {
 constexpr int kClipThreads = 256;
 // elements of one tensor that one CTA takes at a time
 constexpr int64_t kClipChunk = 32768;
-// tensors of one launch: their table travels as a kernel parameter (of at
-// most 32,764 bytes), so a call writes no device memory for it
-constexpr int kClipTensors = 1000;
+// Tensors of one launch: their table travels as a kernel parameter (of at
+// most 32,764 bytes), so a call writes no device memory for it.  Up to 64
+// tensors take a small table: copying 28 KB of parameters twice costs the
+// host 3 us.
+constexpr int kClipTensors = 1000, kClipFewTensors = 64;
 
+template <int CAP>
 struct ClipTable {
-  const void* grad[kClipTensors];
-  void* out[kClipTensors];
-  int64_t size[kClipTensors];  // elements; negative: bfloat16
+  const void* grad[CAP];
+  void* out[CAP];
+  int64_t size[CAP];  // elements; negative: bfloat16
   // first chunk of each tensor (chunks of all tensors are numbered in a row)
-  uint32_t first[kClipTensors + 1];
+  uint32_t first[CAP + 1];
   int count;
 };
-static_assert(sizeof(ClipTable) <= 32764 - 64, "kernel parameters");
+static_assert(sizeof(ClipTable<kClipTensors>) <= 32764 - 64, "kernel parameters");
 
 struct ClipItem {
   const void* grad;
@@ -34,7 +37,8 @@ struct ClipItem {
 };
 
 // the piece of a tensor that chunk `chunk` of the launch is
-__device__ __forceinline__ ClipItem clip_item(const ClipTable& t, uint32_t chunk) {
+template <int CAP>
+__device__ __forceinline__ ClipItem clip_item(const ClipTable<CAP>& t, uint32_t chunk) {
   int lo = 0, hi = t.count;  // first[lo] <= chunk < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -138,7 +142,9 @@ __device__ __forceinline__ ClipSpan clip_span(const ClipItem& it) {
 }
 
 // partials[CTA] = sum of squares over the CTA's chunks
-__global__ void __launch_bounds__(kClipThreads) clip_squares_kernel(const __grid_constant__ ClipTable t, double* partials) {
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads)
+    clip_squares_kernel(const __grid_constant__ ClipTable<CAP> t, double* partials) {
   pdl_trigger();
   pdl_wait();
   __shared__ double scratch[32];
@@ -164,21 +170,32 @@ __global__ void __launch_bounds__(kClipThreads) clip_squares_kernel(const __grid
   if (threadIdx.x == 0) partials[blockIdx.x] = total;
 }
 
+// The norm from all partial sums, in the same order by every CTA that asks.
+__device__ __forceinline__ float norm_of(const double* partials, int64_t n) {
+  __shared__ double scratch[32];
+  double total = 0.0;
+  for (int64_t k = threadIdx.x; k < n; k += kClipThreads) total += __ldg(partials + k);
+  total = cta_sum(total, scratch);
+  return (float)sqrt(total);
+}
+
 __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const double* partials, int64_t n, float* norm) {
   pdl_trigger();
   pdl_wait();
-  __shared__ double scratch[32];
-  double total = 0.0;
-  for (int64_t k = threadIdx.x; k < n; k += kClipThreads) total += partials[k];
-  total = cta_sum(total, scratch);
-  if (threadIdx.x == 0) *norm = (float)sqrt(total);
+  const float v = norm_of(partials, n);
+  if (threadIdx.x == 0) *norm = v;
 }
 
+// Each CTA forms the norm by itself (at most 8 doubles an SM, from L2) rather
+// than wait for a kernel that does; the first writes it.
+template <int CAP>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_scale_kernel(const __grid_constant__ ClipTable t, const float* norm, float max_norm, float eps) {
+    clip_scale_kernel(const __grid_constant__ ClipTable<CAP> t, const double* partials, int64_t parts, float* norm,
+                      float max_norm, float eps) {
   pdl_trigger();
   pdl_wait();
-  const float n = *norm;
+  const float n = norm_of(partials, parts);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float scale = isfinite(n) ? fminf(1.f, max_norm / (n + eps)) : 1.f;
   // the squares walked the chunks upwards: downwards, the first ones here are
   // the last ones read there and still in L2
@@ -209,14 +226,17 @@ size_t clip_workspace(int64_t count, int sm_count) {
   return (size_t)std::max<int64_t>(1, div_up(count, kClipTensors)) * (size_t)clip_grid(sm_count) * sizeof(double);
 }
 
-cudaError_t run_clip_grads(const ClipArgs& a, int sm_count, cudaStream_t s) {
+namespace {
+
+template <int CAP>
+cudaError_t clip_with_tables(const ClipArgs& a, int sm_count, cudaStream_t s) {
   const int grid = clip_grid(sm_count);
-  // the next table of up to kClipTensors tensors (empty ones left out); a
+  // the next table of up to CAP tensors (empty ones left out); a
   // device's memory holds far fewer than 2^32 chunks
-  const auto fill = [&](int64_t k, ClipTable& t) {
+  const auto fill = [&](int64_t k, ClipTable<CAP>& t) {
     t.count = 0;
     int64_t chunks = 0;
-    for (; k < a.count && t.count < kClipTensors; ++k) {
+    for (; k < a.count && t.count < CAP; ++k) {
       if (a.sizes[k] == 0) continue;
       t.grad[t.count] = a.grads[k];
       t.out[t.count] = a.outs ? a.outs[k] : nullptr;
@@ -227,26 +247,34 @@ cudaError_t run_clip_grads(const ClipArgs& a, int sm_count, cudaStream_t s) {
     t.first[t.count] = (uint32_t)chunks;
     return k;
   };
-  ClipTable t;
+  ClipTable<CAP> t;
   int64_t partials = 0;
   for (int64_t k = 0; k < a.count;) {
     k = fill(k, t);
     if (t.count == 0) continue;
     const int64_t g = std::min<int64_t>(grid, t.first[t.count]);
-    const cudaError_t e = launch_pdl(clip_squares_kernel, g, kClipThreads, 0, s, t, a.ws + partials);
+    const cudaError_t e = launch_pdl(clip_squares_kernel<CAP>, g, kClipThreads, 0, s, t, a.ws + partials);
     if (e != cudaSuccess) return e;
     partials += g;
   }
-  cudaError_t e = launch_pdl(clip_norm_kernel, 1, kClipThreads, 0, s, (const double*)a.ws, partials, a.norm);
-  if (e != cudaSuccess || a.outs == nullptr) return e;
+  cudaError_t e = cudaSuccess;
+  if (a.outs == nullptr || partials == 0)
+    return launch_pdl(clip_norm_kernel, 1, kClipThreads, 0, s, (const double*)a.ws, partials, a.norm);
   for (int64_t k = 0; k < a.count;) {
     k = fill(k, t);
     if (t.count == 0) continue;
     const int64_t g = std::min<int64_t>(grid, t.first[t.count]);
-    e = launch_pdl(clip_scale_kernel, g, kClipThreads, 0, s, t, (const float*)a.norm, a.max_norm, a.eps);
+    e = launch_pdl(clip_scale_kernel<CAP>, g, kClipThreads, 0, s, t, (const double*)a.ws, partials, a.norm, a.max_norm, a.eps);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t run_clip_grads(const ClipArgs& a, int sm_count, cudaStream_t s) {
+  return a.count <= kClipFewTensors ? clip_with_tables<kClipFewTensors>(a, sm_count, s)
+                                    : clip_with_tables<kClipTensors>(a, sm_count, s);
 }
 
 cudaError_t status_clip(unsigned int* word, bool clear) { return unit_status(word, clear); }

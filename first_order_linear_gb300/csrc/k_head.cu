@@ -26,8 +26,8 @@ namespace {
 // weight that the copies cannot read in place -- float32, or rows that do not
 // start on 16-byte boundaries -- is packed too, a piece at a time.
 // ---------------------------------------------------------------------------
-constexpr int64_t kPieceBytes = int64_t(256) << 20;  // dz of one piece of the vocabulary
-constexpr int64_t kPackBytes = int64_t(128) << 20;   // packed weight of one piece
+constexpr int64_t kPieceBytes = int64_t(1) << 30;    // dz of one piece of the vocabulary
+constexpr int64_t kPackBytes = int64_t(256) << 20;   // packed weight of one piece
 constexpr int64_t kSplitBytes = int64_t(64) << 20;   // d_hidden's partial sums beyond the first
 constexpr int64_t kWholeStages = 24;                  // k stages (times terms) of a d_hidden sum that is not split
 constexpr int64_t kSplitStages = 8;                   // ... and at least this many a split

@@ -18,6 +18,7 @@ arithmetic, outputs rounded once).
 from __future__ import annotations
 
 import ctypes as C
+import operator
 from array import array
 
 import torch
@@ -622,8 +623,9 @@ def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, nor
     """Global norm of the gradient tensors ``grads`` (each float32 or
     bfloat16, any shape) and the tensors times min(1, max_norm / (norm +
     eps)) -- unscaled when the norm is not finite: ``(clipped, norm)``, norm
-    a float32 scalar tensor.  ``out`` takes the results: a list of matching
-    tensors, or ``grads`` itself to scale in place.  ``norm_only`` leaves the
+    a float32 scalar tensor.  ``out`` takes the results: a list of tensors of
+    the same types and element counts, or ``grads`` itself to scale in
+    place.  ``norm_only`` leaves the
     tensors alone and returns ``(None, norm)``."""
     lib = _lib.load()
     grads = list(grads)
@@ -634,6 +636,12 @@ def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, nor
         if not isinstance(g, torch.Tensor):
             raise TypeError(f"grads[{k}] must be a torch.Tensor")
     dev = grads[0].device if grads else norm.device
+    # the checks over whole lists; one that fails is looked for tensor by tensor
+    flags = [_GRAD_FLAGS.get(g.dtype) for g in grads]
+    if None in flags or not (all([g.device == dev for g in grads]) and all(map(torch.Tensor.is_contiguous, grads))):
+        for k, g in enumerate(grads):
+            _check(g, f"grads[{k}]", (_fdt(g, f"grads[{k}]"),), g.shape, dev)
+    sizes = array("q", map(torch.Tensor.numel, grads))
     if norm_only:
         out = None
     elif out is None:
@@ -642,24 +650,18 @@ def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, nor
         out = list(out)
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors, expected {n}")
-    flags = []
-    for k, g in enumerate(grads):
-        dt = g.dtype
-        f = _GRAD_FLAGS.get(dt)
-        if f is None or g.device != dev or not g.is_contiguous():
-            _check(g, f"grads[{k}]", (_fdt(g, f"grads[{k}]"),), g.shape, dev)  # names the fault
-        flags.append(f)
-        if out is not None:
-            o = out[k]
-            if o is not g and not (isinstance(o, torch.Tensor) and o.dtype is dt and o.shape == g.shape
-                                   and o.device == dev and o.is_contiguous()):
-                _check(o, f"out[{k}]", (dt,), g.shape, dev)
+        if not all(map(operator.is_, out, grads)):
+            if not (all([isinstance(o, torch.Tensor) for o in out]) and [_GRAD_FLAGS.get(o.dtype) for o in out] == flags
+                    and array("q", map(torch.Tensor.numel, out)) == sizes and all([o.device == dev for o in out])
+                    and all(map(torch.Tensor.is_contiguous, out))):
+                for k, (g, o) in enumerate(zip(grads, out)):
+                    _check(o, f"out[{k}]", (g.dtype,), g.shape, dev)
+                raise ValueError("out does not match grads")
     norm = _out(norm, "norm", torch.float32, (), dev)
     _require_cuda(dev)
     # host arrays that the call reads before it returns
-    gp = array("Q", [g.data_ptr() for g in grads])
-    op = None if out is None else array("Q", [o.data_ptr() for o in out])
-    sizes = array("q", [g.numel() for g in grads])
+    gp = array("Q", map(torch.Tensor.data_ptr, grads))
+    op = None if out is None else array("Q", map(torch.Tensor.data_ptr, out))
     dtypes = array("I", flags)
     with _on(dev):
         ws, wsb = _workspace(_lib.RLCA_EST_CLIP_GRADS, n, 1, 0, 0, dev, workspace)

@@ -169,6 +169,11 @@ def test_head_several_pieces_of_the_vocabulary(dtype):
     check_head(3000, 40, 70001, DT[dtype], seed=3, mask=0.2)
 
 
+def test_head_pieces_beyond_a_gigabyte():
+    """dz of the whole vocabulary is 1.15 GB at two bytes an element."""
+    check_head(8192, 24, 70001, torch.bfloat16, seed=4, mask=0.1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_head_many_rows(dtype):
     """More rows than the first kernel's CTAs take in one round."""
