@@ -323,9 +323,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
 // stage is filled again after the barrier that follows its reads (the one the
 // row's sums need anyway).  A wait that gives up is recorded in the status
 // word; the rows are then walked without further copies or waits.
-constexpr int kRingRows = 4;
-
-template <class ST, int VE, int VPT, int TPR>
+template <class ST, int VE, int VPT, int TPR, int kRingRows>
 __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_ring_kernel(NormGradArgs a) {
   using P = Pack<ST, VE>;
   extern __shared__ __align__(128) unsigned char ring_rows[];  // [kRingRows][x, dy][D]
@@ -555,6 +553,7 @@ cudaError_t norm_typed(const NormArgs& a, int sm, cudaStream_t s) {
     if (a.D <= 1024) return launch_norm<ST, 1, 8, 128>(a, sm, s);
     if (a.D <= 2048) return launch_norm<ST, 1, 8, 256>(a, sm, s);
     if (a.D <= 4096) return launch_norm<ST, 1, 8, 512>(a, sm, s);
+    if (a.D <= 8192) return launch_norm<ST, 1, 16, 512>(a, sm, s);
   }
   return launch_pdl(norm_long_kernel<ST>, a.N, kLongThreads, 0, s, a);
 }
@@ -581,10 +580,10 @@ cudaError_t launch_grad(const NormGradArgs& a, int sm, cudaStream_t s) {
   return e == cudaSuccess ? join(a, grid, s) : e;
 }
 
-template <class ST, int VE, int VPT, int TPR>
+template <class ST, int VE, int VPT, int TPR, int kRingRows = 4>
 cudaError_t launch_grad_ring(const NormGradArgs& a, int sm, cudaStream_t s) {
   const size_t smem = (size_t)kRingRows * 2 * a.D * Stor<ST>::kBytes;
-  const auto kernel = norm_grad_ring_kernel<ST, VE, VPT, TPR>;
+  const auto kernel = norm_grad_ring_kernel<ST, VE, VPT, TPR, kRingRows>;
   static std::atomic<uint64_t> allowed;
   cudaError_t e = allow_smem(kernel, (size_t)kRingRows * 2 * TPR * VPT * 16, allowed);
   if (e != cudaSuccess) return e;
@@ -611,12 +610,15 @@ cudaError_t grad_typed(const NormGradArgs& a, int sm, cudaStream_t s) {
     if (nv <= 256) return launch_grad_ring<ST, VE, 2, 128>(a, sm, s);
     if (nv <= 512) return launch_grad_ring<ST, VE, 2, 256>(a, sm, s);
     if (nv <= 1024) return launch_grad_ring<ST, VE, 2, 512>(a, sm, s);
+    if constexpr (VE == 4)  // (three rows of 32 KB, twice, fill the shared memory)
+      if (nv <= 2048) return launch_grad_ring<ST, VE, 4, 512, 3>(a, sm, s);
   } else {
     if (a.D <= 32) return launch_grad<ST, 1, 1, 32>(a, sm, s);
     if (a.D <= 256) return launch_grad<ST, 1, 8, 32>(a, sm, s);
     if (a.D <= 1024) return launch_grad<ST, 1, 8, 128>(a, sm, s);
     if (a.D <= 2048) return launch_grad<ST, 1, 8, 256>(a, sm, s);
     if (a.D <= 4096) return launch_grad<ST, 1, 8, 512>(a, sm, s);
+    if (a.D <= 8192) return launch_grad<ST, 1, 16, 512>(a, sm, s);
   }
   if (a.dx != nullptr) {
     const cudaError_t e = launch_pdl(norm_grad_long_kernel<ST>, a.N, kLongThreads, 0, s, a);

@@ -289,7 +289,7 @@ def check_norm(N, D, dtype, seed=0, bias=True, strided=False, shift=False, eps=1
 
 
 NORM_SIZES = [(1, 1), (1, 2), (2, 3), (8, 1024), (7, 31), (33, 32), (5, 33), (64, 257), (100, 1001), (1000, 64),
-              (300, 4096), (40, 4097), (17, 8192), (9, 8200), (3, 20000), (4099, 129), (2, 65536)]
+              (300, 4096), (40, 4097), (17, 8192), (9, 8200), (3, 20000), (4099, 129), (2, 65536), (700, 5001), (31, 8191), (600, 8192), (33, 16384)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
