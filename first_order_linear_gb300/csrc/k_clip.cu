@@ -1,4 +1,12 @@
 // Global gradient norm over many tensors, and the tensors scaled by it.
+//
+// Bound by HBM: the norm reads everything before the first element can be
+// scaled, so what does not fit in L2 is read twice and written once.  1.34 G
+// elements (2.7 GB) in 50 tensors: 1200 us for 8.05 GB, 6.7 TB/s, the measured
+// copy rate; one load a thread in flight took 2998 us.  Chunks of 32768
+// elements of all tensors are dealt to 8 CTAs an SM, so neither one large
+// tensor nor thousands of small ones leave SMs idle, and the whole list is two
+// launches.  18 small tensors: 20 us on the device, launch latency.
 #include <algorithm>
 
 #include "policy.h"

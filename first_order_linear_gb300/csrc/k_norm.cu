@@ -92,7 +92,11 @@ __device__ __forceinline__ float row_sum(float v, float (*scratch)[32], int slot
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  (The row loop's trip count is the same for all threads of a CTA
+// Forward: bound by HBM.  65536 x 4096 bfloat16: 166 us, 6.46 TB/s, 0.97 of
+// the measured copy rate; 32768 x 4096: 128 threads x 4 vectors a row 91 us,
+// 256 x 2 97 us, 512 x 1 138 us (more threads wait for the same two sums).
+// Single elements (8000 x 7001 bfloat16): 3.2 TB/s, bound by the loads' issue.
+// (The row loop's trip count is the same for all threads of a CTA
 // where a row takes the whole CTA, so the barriers match.)
 // ---------------------------------------------------------------------------
 template <class ST, int VE, int VPT, int TPR>
@@ -193,7 +197,10 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Each CTA leaves the sums of dw and db over its rows in
+// Backward: bound by HBM.  Rows next to each other in a warp or a CTA, the
+// next one loaded into registers ahead: for rows up to 64 vectors (262144 x
+// 256 bfloat16: 93 us, 4.4 TB/s) and for rows of single elements.  Longer rows
+// of vectors take the ring below.  Each CTA leaves the sums of dw and db over its rows in
 // ws[CTA][2][D]; a second kernel joins them in order.
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int grad_resident(int threads, int values) {
@@ -317,7 +324,9 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
   }
 }
 
-// The same for rows of a CTA of their own, fed by bulk copies: thread 0 keeps
+// The same for rows of a CTA of their own, fed by bulk copies (32768 x 4096
+// bfloat16: 143 us with the join, 5.6 TB/s, against 156 us with the next row
+// in registers; two such CTAs an SM are all that 120 registers allow): thread 0 keeps
 // kRingRows - 1 rows of x and dy on their way into shared memory, so what is
 // in flight does not depend on the registers that the columns' sums leave.  A
 // stage is filled again after the barrier that follows its reads (the one the
@@ -479,6 +488,7 @@ __global__ void __launch_bounds__(kSliceThreads)
   a.ws[(2 * slice + 1) * a.D + c] = db;
 }
 
+// (10 MB of partial sums at 32768 x 4096, from L2: about 5 us.)
 // The partial sums of 32 columns, joined by 32 x 32 threads: warp k adds the
 // partials k, k + 32, ... of its columns, then the warps' sums are added in
 // order.  blockIdx.x < col_blocks: dw, else db.
