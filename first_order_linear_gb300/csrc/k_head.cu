@@ -102,8 +102,8 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
     // (one piece, not split: the product writes d_hidden itself)
     if (p.splits > 1 || piece_tiles < tiles) p.dh = take((size_t)(p.two_dz ? 2 : 1) * p.splits * out_bytes);
   } else {
-    // (head_few_kernel: one piece a CTA, of at most 8 rows)
-    p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 8) * sizeof(float4));
+    // (head_few_kernel: one piece a CTA, of at most 16 rows)
+    p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 16) * sizeof(float4));
     p.taken = take((size_t)p.Np * 4);
   }
   p.bytes = at;
@@ -744,14 +744,13 @@ __global__ void __launch_bounds__(kJoinThreads)
 // leaves each lane with one logit, whose running statistics it keeps.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
-constexpr int kFewTokens = 4;  // R
 constexpr size_t kFewSmem = 96 * 1024;
 
-template <class ST, int VE, int NT>
+template <class ST, int VE, int NT, int R>
 __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     head_few_kernel(HeadArgs a, HeadView w, int64_t Ds, float c2) {
   extern __shared__ __align__(16) float few_hidden[];  // [NT][Ds], zeros past D
-  constexpr int R = kFewTokens, C = R * NT, W = kFewThreads / 32;
+  constexpr int C = R * NT, W = kFewThreads / 32;
   constexpr int kLog = C == 4 ? 2 : C == 8 ? 3 : C == 16 ? 4 : 5;  // log2 C
   __shared__ Stats acc[W][C];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -769,14 +768,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
   const int64_t nv = a.D / VE;
   for (int64_t v0 = ((int64_t)blockIdx.x * W + warp) * R; v0 < a.V; v0 += (int64_t)gridDim.x * W * R) {
     float z[C];
+    // vectors: sums of the even and of the odd columns, two to an instruction
+    uint64_t zz[VE >= 4 ? C : 1];
 #pragma unroll
     for (int i = 0; i < C; ++i) z[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < (VE >= 4 ? C : 1); ++i) zz[i] = 0;
     const float* base[R];
 #pragma unroll
     for (int r = 0; r < R; ++r)
       base[r] = reinterpret_cast<const float*>(reinterpret_cast<const unsigned char*>(a.weight) +
                                                min(v0 + r, a.V - 1) * a.weight_stride * Stor<ST>::kBytes);
-#pragma unroll (NT <= 2 ? 4 : 2)
+#pragma unroll (NT <= 2 ? 16 / R : 2)
     for (int64_t j = lane; j < nv; j += 32) {
       float x[R][VE];
 #pragma unroll
@@ -787,20 +790,29 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float h[VE];
         if constexpr (VE >= 4) {
 #pragma unroll
           for (int e = 0; e < VE; e += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(few_hidden + n * Ds + j * VE + e);
-            h[e] = q.x, h[e + 1] = q.y, h[e + 2] = q.z, h[e + 3] = q.w;
+            const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(few_hidden + n * Ds + j * VE + e);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              zz[r * NT + n] = pair_fma(pair_of(x[r][e], x[r][e + 1]), h.x, zz[r * NT + n]);
+              zz[r * NT + n] = pair_fma(pair_of(x[r][e + 2], x[r][e + 3]), h.y, zz[r * NT + n]);
+            }
           }
         } else {
-          h[0] = few_hidden[n * Ds + j];
+          const float h = few_hidden[n * Ds + j];
+#pragma unroll
+          for (int r = 0; r < R; ++r) z[r * NT + n] = fmaf(x[r][0], h, z[r * NT + n]);
         }
+      }
+    }
+    if constexpr (VE >= 4) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) z[r * NT + n] = fmaf(x[r][e], h[e], z[r * NT + n]);
+      for (int i = 0; i < C; ++i) {
+        float even, odd;
+        pair_open(zz[i], even, odd);
+        z[i] = even + odd;
       }
     }
     int n = C;
@@ -884,16 +896,15 @@ TcTerms terms_of(int planes) {
   return t;
 }
 
-// Rows that head_few_kernel takes: up to 8, if their float32 copies fit two
-// CTAs' shared memory an SM.
-bool few(int64_t N, int64_t D) {
-  const int64_t nt = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;
-  return N <= 8 && (size_t)(nt * round_up(D, 4) * 4) <= kFewSmem;
+// Rows that head_few_kernel takes, if their float32 copies fit two CTAs' shared
+// memory an SM: bfloat16 up to 4 (32768 x 1024: 1 row 25 against 36 us on the
+// tensor cores, 4 rows 35 against 33, 8 rows 54 against 32), float32, which
+// the tensor cores take as planes that have to be packed first, up to 16 (87
+// against 137 us).
+bool few(int64_t N, int64_t D, bool bf16_io) {
+  const int64_t nt = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : N <= 8 ? 8 : 16;
+  return N <= (bf16_io ? 4 : 16) && (size_t)(nt * round_up(D, 4) * 4) <= kFewSmem;
 }
-int64_t few_grid(int64_t V, int sm_count) {
-  return std::min<int64_t>(div_up(V, kFewTokens * (kFewThreads / 32)), few_pieces(sm_count));
-}
-
 int64_t tiles_of(const TcShape& s) { return div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits; }
 
 template <class Job1, class Job2>
@@ -1025,21 +1036,31 @@ struct HeadRun {
     return launch_pdl(head_join_kernel, div_up(a.N, 32), 32 * kJoinWarps, 0, s, a, w, pieces, pitch, c2);
   }
 
+  // 16 loads of a lane in flight: 4 tokens at a time, or 8 of up to 64 vectors
+  // (512 x 131072 bfloat16); 16 rows hold 32 sums at 2 tokens
   template <int VE, int NT>
   cudaError_t few_rows() {
-    const auto kernel = head_few_kernel<ST, VE, NT>;
+    if (VE > 1 && NT <= 2 && a.D / VE <= 64) return few_launch<VE, NT, (NT <= 2 ? 8 : 4)>();
+    return few_launch<VE, NT, (NT > 8 ? 2 : 4)>();
+  }
+  template <int VE, int NT, int R>
+  cudaError_t few_launch() {
+    const auto kernel = head_few_kernel<ST, VE, NT, R>;
     const int64_t Ds = round_up(a.D, 4);
     const size_t smem = (size_t)NT * Ds * 4;
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_smem(kernel, kFewSmem, allowed);
     if (e != cudaSuccess) return e;
-    const int64_t grid = few_grid(a.V, sm);
+    const int64_t grid = std::min(div_up(a.V, R * (kFewThreads / 32)), few_pieces(sm));
     e = launch_pdl(kernel, grid, kFewThreads, smem, s, a, w, Ds, a.inv_temperature * kLog2e);
     return e == cudaSuccess ? join(grid, NT, true) : e;
   }
   template <int VE>
   cudaError_t few_rows() {
-    return a.N <= 1 ? few_rows<VE, 1>() : a.N <= 2 ? few_rows<VE, 2>() : a.N <= 4 ? few_rows<VE, 4>() : few_rows<VE, 8>();
+    if (a.N <= 1) return few_rows<VE, 1>();
+    if (a.N <= 2) return few_rows<VE, 2>();
+    if constexpr (Stor<ST>::kBytes == 2) return few_rows<VE, 4>();
+    else return a.N <= 4 ? few_rows<VE, 4>() : a.N <= 8 ? few_rows<VE, 8>() : few_rows<VE, 16>();
   }
   cudaError_t forward_few() {
     constexpr int VE = 16 / Stor<ST>::kBytes;
@@ -1126,7 +1147,7 @@ size_t head_workspace(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backwa
 
 cudaError_t run_token_logprob(const HeadArgs& a, int sm_count, cudaStream_t s) {
   const HeadPlan p = plan_head(a.N, a.D, a.V, a.bf16_io, false, !in_place(a), sm_count);
-  if (few(a.N, a.D)) return a.bf16_io ? HeadRun<bf16>(a, p, sm_count, s).forward_few() : HeadRun<float>(a, p, sm_count, s).forward_few();
+  if (few(a.N, a.D, a.bf16_io)) return a.bf16_io ? HeadRun<bf16>(a, p, sm_count, s).forward_few() : HeadRun<float>(a, p, sm_count, s).forward_few();
   return a.bf16_io ? HeadRun<bf16>(a, p, sm_count, s).forward() : HeadRun<float>(a, p, sm_count, s).forward();
 }
 
