@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const double* p
 // Each CTA forms the norm by itself (at most 8 doubles an SM, from L2) rather
 // than wait for a kernel that does; the first writes it.
 template <int CAP>
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, 5)
     clip_scale_kernel(const __grid_constant__ ClipTable<CAP> t, const double* partials, int64_t parts, float* norm,
                       float max_norm, float eps) {
   pdl_trigger();

@@ -391,7 +391,7 @@ struct StatsEpi {
     st.top = -INFINITY;
     st.s = st.t = 0.f;
   }
-  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
+  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     const int n = v_end - v0 - col;  // columns that exist
     if (n <= 0) return;
     if (n < 32) {
@@ -477,7 +477,7 @@ struct DzEpi {
       st.lse2 = -f.z * kLog2e;
     }
   }
-  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
+  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     if (st.skip) return;
     const float c2 = inv_t * kLog2e;
     const int k = st.at - col;
@@ -525,11 +525,32 @@ struct DzEpi {
   __device__ __forceinline__ void end(State&) const {}
 };
 
-// 32 values from column `col` on to the row that starts at element `at` of a
-// matrix of `width` columns, rounded once; align: what the rows' starts are
-// multiples of, in bytes (32, 16, or less)
+// 32 values a lane from column `col` on, each lane's to its row that starts
+// at element `at` of a matrix of `width` columns (rows that are not `live`
+// excepted), rounded once.  align: what the rows' starts are multiples of, in
+// bytes.  On 16-byte boundaries each lane writes its own row; elsewhere that
+// would be 32 rows an instruction, one element each (20 x 1001 x 30000: 291 us
+// for 60 MB), so the block goes through shared memory and the warp writes row
+// by row.
 template <class ST>
-__device__ __forceinline__ void store_row32(float* out, int64_t at, int64_t col, int64_t width, int align, const float* v) {
+__device__ __forceinline__ void store_rows32(float* out, bool live, int64_t at, int64_t col, int64_t width, int align,
+                                             const float* v, float* block) {
+  if (align < 16) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) block[lane * 33 + i] = v[i];
+    __syncwarp();
+    const unsigned rows = __ballot_sync(0xffffffffu, live);
+    const bool on = col + lane < width;
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r) {
+      const int64_t to = __shfl_sync(0xffffffffu, at, r) + col + lane;
+      if (on && (rows >> r & 1u)) Stor<ST>::st(out, to, block[r * 33 + lane]);
+    }
+    __syncwarp();
+    return;
+  }
+  if (!live) return;
   if (align >= 32 && col + 32 <= width) {
     unsigned char* p = reinterpret_cast<unsigned char*>(out) + (at + col) * Stor<ST>::kBytes;
     if constexpr (Stor<ST>::kBytes == 2) {
@@ -545,16 +566,13 @@ __device__ __forceinline__ void store_row32(float* out, int64_t at, int64_t col,
       }
     }
   } else {
+    // (a width of whole 16-byte vectors: none is cut)
     constexpr int E = 16 / Stor<ST>::kBytes;
 #pragma unroll
     for (int i = 0; i < 32; i += E) {
-      if (align >= 16 && col + i + E <= width) {
+      if (col + i < width) {
         if constexpr (E == 8) Stor<ST>::st8(out, at + col + i, v + i);
         else Stor<ST>::st4(out, at + col + i, v + i);
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (col + i + j < width) Stor<ST>::st(out, at + col + i + j, v[i + j]);
       }
     }
   }
@@ -589,10 +607,9 @@ struct DhEpi {
     st.sum = sums + (halves ? 2 * t.split + row / kTcRows : t.split) * plane + (int64_t)part * pitch;
     st.at = last && st.live ? rows[part] * width : 0;
   }
-  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
-    if (!st.live || col >= pitch) return;
-    if (!(first && last) && !span_in_range(st.sum - sums + col, 32, size)) return;
-    if (!first) {
+  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
+    if (col >= pitch) return;
+    if (!first && st.live && span_in_range(st.sum - sums + col, 32, size)) {
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
         const float4 o = *reinterpret_cast<const float4*>(st.sum + col + i);
@@ -600,8 +617,8 @@ struct DhEpi {
       }
     }
     if (last) {
-      if (in_range(st.at, N * width)) store_row32<ST>(out, st.at, col, width, align, v);
-    } else {
+      store_rows32<ST>(out, st.live && in_range(st.at, N * width), st.at, col, width, align, v, block);
+    } else if (st.live && span_in_range(st.sum - sums + col, 32, size)) {
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         uint32_t r[8];
@@ -629,8 +646,8 @@ struct OutEpi {
     st.live = row < w.m;
     st.at = (row0 + row) * width;
   }
-  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32]) const {
-    if (st.live && in_range(st.at, V * width)) store_row32<ST>(out, st.at, col, width, align, v);
+  __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
+    store_rows32<ST>(out, st.live && in_range(st.at, V * width), st.at, col, width, align, v, block);
   }
   __device__ __forceinline__ void end(State&) const {}
 };
@@ -908,10 +925,10 @@ bool few(int64_t N, int64_t D, bool bf16_io) {
 int64_t tiles_of(const TcShape& s) { return div_up(s.m, kTcM) * div_up(s.n, kTcN) * s.splits; }
 
 template <class Job1, class Job2>
-cudaError_t launch_product(const Job1& j1, const Job2& j2, int64_t tiles, int sm_count, cudaStream_t st) {
+cudaError_t launch_product(const Job1& j1, const Job2& j2, int64_t tiles, int sm_count, cudaStream_t st, bool blocks) {
   void (*const kernel)(const Job1, const Job2) = tc_product_kernel<Job1, Job2>;
   static std::atomic<uint64_t> allowed;
-  cudaError_t e = allow_smem(kernel, kTcSmem, allowed);
+  cudaError_t e = allow_smem(kernel, kTcSmemBlocks, allowed);
   if (e != cudaSuccess) return e;
   if (Job1::GROUP > 0) {
     // the warpgroups' register shares are taken from the launch's registers:
@@ -923,11 +940,12 @@ cudaError_t launch_product(const Job1& j1, const Job2& j2, int64_t tiles, int sm
     }();
     if (!enough) return cudaErrorInvalidConfiguration;
   }
-  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, kTcSmem, st, j1, j2);
+  return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, blocks ? kTcSmemBlocks : kTcSmem, st, j1,
+                    j2);
 }
 template <class Job>
-cudaError_t launch_product(const Job& j, int sm_count, cudaStream_t st) {
-  return launch_product(j, TcNoJob{}, tiles_of(j.s), sm_count, st);
+cudaError_t launch_product(const Job& j, int sm_count, cudaStream_t st, bool blocks = false) {
+  return launch_product(j, TcNoJob{}, tiles_of(j.s), sm_count, st, blocks);
 }
 
 // Whether two products run faster dealt out together than one after the
@@ -1121,10 +1139,10 @@ struct HeadRun {
       if (a.d_hidden && a.d_weight &&
           together(tiles_of(sh), div_up(div_up(len, kTcK), p.splits) * sh.terms.n, tiles_of(sw), div_up(a.N, kTcK) * sw.terms.n,
                    sm / 2)) {
-        e = launch_product(jh, jw, tiles_of(sh) + tiles_of(sw), sm, s);
+        e = launch_product(jh, jw, tiles_of(sh) + tiles_of(sw), sm, s, jh.epi.align < 16 || jw.epi.align < 16);
       } else {
-        if (a.d_hidden) e = launch_product(jh, sm, s);
-        if (e == cudaSuccess && a.d_weight) e = launch_product(jw, sm, s);
+        if (a.d_hidden) e = launch_product(jh, sm, s, jh.epi.align < 16);
+        if (e == cudaSuccess && a.d_weight) e = launch_product(jw, sm, s, jw.epi.align < 16);
       }
     }
     if (e == cudaSuccess && a.d_hidden && p.splits > 1) {

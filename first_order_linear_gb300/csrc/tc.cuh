@@ -58,6 +58,11 @@ constexpr int kTcABytes = kTcRows * kTcK * 2;
 constexpr int kTcBBytes = kTcN / 2 * kTcK * 2;
 constexpr int kTcStageBytes = kTcABytes + kTcBBytes;
 constexpr size_t kTcSmem = (size_t)kTcStages * kTcStageBytes + 1024;  // + alignment of the ring
+// ... and, where an epilogue asks for them, a 32 x 32 block of each of its
+// warps, rows padded against bank conflicts (otherwise L1 keeps the 33 KB)
+constexpr int kTcBlockFloats = 32 * 33;
+constexpr size_t kTcSmemBlocks = kTcSmem + kTcEpiWarps * kTcBlockFloats * 4;
+static_assert(kTcSmemBlocks + 512 <= 227 * 1024, "with the barriers, within a CTA's shared memory");
 
 // the plane pairs of one product, four bits each for A's and B's plane
 struct TcTerms {
@@ -273,8 +278,10 @@ __device__ __forceinline__ int tc_group_end(int at, int stages, int terms) {
 
 // One product.  Epi: struct State; begin(State&, walk, tile, row, col0) with
 // row = the thread's row of C and col0 the first column of its half tile;
-// chunk(State&, col, v[32]) for the 32 columns from col on; end(State&).
-// Rows from walk.m on do not exist.
+// chunk(State&, col, v[32], block) for the 32 columns from col on, by whole
+// warps, with a shared-memory block of the warp's own (if the launch has
+// kTcSmemBlocks); end(State&).  Rows from
+// walk.m on do not exist.
 template <bool A_MN_, bool B_MN_, int GROUP_, class Epi_>
 struct TcJob {
   using Epi = Epi_;
@@ -387,7 +394,7 @@ __device__ __forceinline__ bool tc_mma_tile(const Job& job, const TcWalk& walk, 
 // given up (one verdict for the warp: the TMEM loads need all its lanes).
 template <class Job>
 __device__ __forceinline__ bool tc_finish_tile(const Job& job, const TcWalk& walk, int64_t t, int rank, uint32_t tmem,
-                                               TcShared& sh, TcAcc& acc) {
+                                               TcShared& sh, float* block, TcAcc& acc) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
   const uint32_t src0 = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kTcN / 2);
   const auto ready = [&] {
@@ -422,7 +429,7 @@ __device__ __forceinline__ bool tc_finish_tile(const Job& job, const TcWalk& wal
       done();
     }
 #pragma unroll
-    for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c]);
+    for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c], block);
   } else {
     float v[32], w[32];  // one is worked on while the other is loaded
     if (steps > 0) {
@@ -433,18 +440,18 @@ __device__ __forceinline__ bool tc_finish_tile(const Job& job, const TcWalk& wal
       for (int c = 0; c < kTcN / 2; c += 64) {
         tc_load_wait(v);
         tc_load32(src + c + 32, w);
-        job.epi.chunk(st, col0 + c, v);
+        job.epi.chunk(st, col0 + c, v, block);
         tc_load_wait(w);
         if (c + 64 < kTcN / 2) tc_load32(src + c + 64, v);
         else done();
-        job.epi.chunk(st, col0 + c + 32, w);
+        job.epi.chunk(st, col0 + c + 32, w, block);
       }
     } else {
 #pragma unroll 1
       for (int c = 0; c < kTcN / 2; c += 32) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        job.epi.chunk(st, col0 + c, v);
+        job.epi.chunk(st, col0 + c, v, block);
       }
     }
   }
@@ -546,7 +553,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     // ---- epilogue ----
     if constexpr (GROUP > 0) regs_take<kTcEpiRegs>();
     TcAcc acc;
-    each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_finish_tile(job, w, t, rank, tmem, sh, acc); });
+    float* block = reinterpret_cast<float*>(ring + kTcStages * kTcStageBytes) + warp * kTcBlockFloats;
+    each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_finish_tile(job, w, t, rank, tmem, sh, block, acc); });
   }
   __syncwarp();
   tc_fence_before();
