@@ -17,4 +17,4 @@ from .rlca import (  # noqa: F401
     rlca_token_logprob_backward, rlca_value_targets, rlca_vtrace, rlca_workspace_size,
 )
 
-__version__ = "0.1.0"
+__version__ = "0.2.0"

@@ -434,7 +434,7 @@ const char* rlca_status_string(int status) {
   }
 }
 
-int rlca_version(void) { return 200; }
+int rlca_version(void) { return 300; }
 
 int rlca_index_checks(void) { return kIndexCheck ? 1 : 0; }
 

@@ -157,9 +157,10 @@ int rlca_version(void);
  * memory (0: nothing to report), and zeroes them when `clear` is nonzero.
  * No counterpart in the paper: it reports conditions that a kernel records
  * instead of trapping.  The only one in the product build is
- * RLCA_STATUS_WAIT_TIMEOUT: a kernel that waits for its own tensor copies
- * (the time-major bulk driver) gives up after 0.2 s instead of hanging and
- * leaves that call's outputs incomplete.  The copies are synchronous: the
+ * RLCA_STATUS_WAIT_TIMEOUT: a kernel that waits for its own copies (the
+ * time-major bulk driver, the layer norm's gradient) or matrix instructions
+ * (the policy head) gives up after 0.2 s instead of hanging and leaves that
+ * call's outputs incomplete.  The copies are synchronous: the
  * call waits for the device's earlier work.  Errors: RLCA_ERR_INVALID_ARG
  * for a NULL `status`, RLCA_ERR_CUDA when a copy fails.
  */
