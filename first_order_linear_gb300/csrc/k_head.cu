@@ -75,6 +75,8 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
   if (backward) piece_tiles = std::min(piece_tiles, std::max<int64_t>(1, kPieceBytes / (2 * p.planes * p.Np * kTcN)));
   p.pitch = piece_tiles * kTcN;
   p.piece = std::min(p.pitch, V);
+  // (offsets count from the workspace's first 256-byte boundary: the kernels
+  // write 32 bytes at a time)
   size_t at = 0;
   const auto take = [&](size_t n) {
     const size_t here = at;
@@ -106,7 +108,7 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
     p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 16) * sizeof(float4));
     p.taken = take((size_t)p.Np * 4);
   }
-  p.bytes = at;
+  p.bytes = at + 255;
   return p;
 }
 
@@ -121,7 +123,7 @@ struct HeadView {  // the workspace's arrays on the device
   uint16_t* dz;
   float* dh;
   HeadView(const HeadPlan& p, void* ws) {
-    unsigned char* b = static_cast<unsigned char*>(ws);
+    unsigned char* b = reinterpret_cast<unsigned char*>(((uintptr_t)ws + 255) & ~(uintptr_t)255);
     count = reinterpret_cast<int*>(b + p.count);
     rows = reinterpret_cast<int*>(b + p.rows);
     tok = reinterpret_cast<int*>(b + p.tok);

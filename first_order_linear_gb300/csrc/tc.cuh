@@ -547,8 +547,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_mma_tile(job, w, t, tmem, sh, ring, r, acc); });
       // whatever was issued completes before TMEM is freed
       tc_commit(&sh.drained);
-      mbar_wait_bounded(&sh.drained, 0);
     }
+    // (in both CTAs: no arrival is still on its way when the cluster ends)
+    if (lane == 0) mbar_wait_bounded(&sh.drained, 0);
   } else {
     // ---- epilogue ----
     if constexpr (GROUP > 0) regs_take<kTcEpiRegs>();

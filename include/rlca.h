@@ -177,8 +177,8 @@ int rlca_index_checks(void);
 /*
  * Bytes of device workspace that the call of `estimator` (RLCA_EST_*) with
  * these sizes and flags needs on the CURRENT device (0 for the one-pass
- * path).  num_actions is read for RLCA_EST_RETRACE only.  Writes the size to
- * *bytes.  Errors: RLCA_ERR_INVALID_ARG for a NULL `bytes`, an unknown
+ * path).  num_actions is read for RLCA_EST_RETRACE (actions) and the
+ * RLCA_EST_TOKEN_LOGPROB ids (vocabulary) only.  Writes the size to *bytes.  Errors: RLCA_ERR_INVALID_ARG for a NULL `bytes`, an unknown
  * estimator, bad sizes or flags; RLCA_ERR_CUDA if the device cannot be
  * queried.
  */

@@ -191,6 +191,27 @@ def test_head_repeats_bit_for_bit(dtype):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_head_given_workspace(dtype):
+    """A workspace of exactly the size asked for, on a 16-byte boundary that is no more than that."""
+    N, D, V = 200, 104, 700
+    h, w, tok, g, e = head_inputs(N, D, V, DT[dtype], 12, mask=0.3)
+    flags = _lib.RLCA_BF16 if dtype == "bf16" else 0
+
+    def space(est):
+        n = rlca.rlca_workspace_size(est, N, D, V, flags)
+        return torch.full((n + 32,), 255, dtype=torch.uint8, device="cuda")[16:16 + n]
+    want = rlca.rlca_token_logprob(h, w, tok)
+    got = rlca.rlca_token_logprob(h, w, tok, workspace=space(_lib.RLCA_EST_TOKEN_LOGPROB))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    kw = dict(entropy=want[2], d_entropy=e)
+    ref_grads = rlca.rlca_token_logprob_backward(h, w, tok, want[1], g, **kw)
+    got = rlca.rlca_token_logprob_backward(h, w, tok, want[1], g, workspace=space(_lib.RLCA_EST_TOKEN_LOGPROB_BACKWARD), **kw)
+    assert all(torch.equal(a, b) for a, b in zip(ref_grads, got))
+    with pytest.raises(ValueError):
+        rlca.rlca_token_logprob(h, w, tok, workspace=space(_lib.RLCA_EST_TOKEN_LOGPROB)[:-16])
+
+
 def test_head_one_output_only():
     h, w, tok, g, e = head_inputs(90, 64, 300, torch.bfloat16, 2)
     logp, lse, ent = rlca.rlca_token_logprob(h, w, tok)
