@@ -459,7 +459,7 @@ struct DzEpi {
   bool two;
 
   struct State {
-    float lse2, a0, a1, g;
+    float lse, a0, a1, g;  // lse before the temperature
     int at;
     bool live, skip;
     uint16_t* row;
@@ -469,27 +469,29 @@ struct DzEpi {
     st.skip = two && row >= kTcRows;  // the second values' rows
     st.row = dz + (int64_t)row * pitch;
     st.at = -1;
-    st.lse2 = st.a0 = st.a1 = st.g = 0.f;
+    st.lse = st.a0 = st.a1 = st.g = 0.f;
     if (st.live) {
       const float4 f = info[row];
       st.at = tok[row] - v0;
       st.g = f.x * inv_t;
       st.a0 = -(f.x + f.y * (f.w - f.z)) * inv_t;
       st.a1 = -f.y * inv_t * inv_t;
-      st.lse2 = -f.z * kLog2e;
+      st.lse = f.z / inv_t;
     }
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     if (st.skip) return;
     const float c2 = inv_t * kLog2e;
     const int k = st.at - col;
-    const uint64_t c22 = pair_of(c2, c2), l2 = pair_of(st.lse2, st.lse2);
+    // (the difference first: z c2 and lse c2 rounded apart would put an error
+    // of their size, not of the difference's, into the exponent)
+    const uint64_t c22 = pair_of(c2, c2), l2 = pair_of(-st.lse, -st.lse);
     const uint64_t a02 = pair_of(st.a0, st.a0), a12 = pair_of(st.a1, st.a1);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const uint64_t z = pair_of(v[i], v[i + 1]);
       float x0, x1;
-      pair_open(pair_fma(z, c22, l2), x0, x1);
+      pair_open(pair_mul(pair_add(z, l2), c22), x0, x1);
       const uint64_t p = pair_of(exp2_approx(x0), exp2_approx(x1));
       pair_open(pair_mul(p, pair_fma(a12, z, a02)), v[i], v[i + 1]);
     }
@@ -977,12 +979,16 @@ bool in_place(const HeadArgs& a) {
 
 // Stages summed by the tensor cores alone (tc.cuh): 512 values of k for
 // results that leave in float32; the bfloat16 gradients' own rounding is
-// larger than the whole sum's error.
-constexpr int kLogitsGroup = 8;
+// larger than the whole sum's error.  The logits of float32 operands, whose
+// error is dz's relative error, take 128 (of the leading product only: 2 to 4%
+// of the time; gradients at 2 x 4000 x 20000 4.1e-7 off instead of 1.9e-6).
+constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2;
 
 template <class ST>
 struct HeadRun {
-  static constexpr int kGradGroup = Stor<ST>::kBytes == 4 ? kLogitsGroup : 0;
+  static constexpr bool kF32 = Stor<ST>::kBytes == 4;
+  static constexpr int kGradGroup = kF32 ? kLogitsGroup : 0, kDzGroup = kF32 ? kLogitsGroupF32 : 0,
+                       kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
   const HeadArgs& a;
   const HeadPlan p;
   const HeadView w;
@@ -1043,7 +1049,7 @@ struct HeadRun {
       CUtensorMap wk;
       if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, div_up(a.V, kTcN) * 2, (int)v0, (int)(v0 + len), c2};
-      e = launch_product(TcJob<false, false, kLogitsGroup, StatsEpi>{hidden_k, wk, in_place_k, logits_shape(v0, len), epi},
+      e = launch_product(TcJob<false, false, kStatsGroup, StatsEpi>{hidden_k, wk, in_place_k, logits_shape(v0, len), epi},
                          sm, s);
     }
     return e == cudaSuccess ? join(div_up(a.V, kTcN) * 2, p.Np, false) : e;
@@ -1116,7 +1122,7 @@ struct HeadRun {
         return cudaErrorNotSupported;
       using Dz = DzEpi<Stor<ST>::kBytes == 2 ? 1 : 3>;
       const Dz dz{w.dz, p.pitch, dz_plane, dz_planes * dz_plane, w.info, w.tok, (int)v0, a.inv_temperature, p.two_dz};
-      e = launch_product(TcJob<false, false, kGradGroup, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
+      e = launch_product(TcJob<false, false, kDzGroup, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
       if (e != cudaSuccess) break;
       // d_hidden's sum over this piece's tokens, and its tokens' d_weight
       TcShape sh = {}, sw = {};
