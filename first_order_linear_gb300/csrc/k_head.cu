@@ -8,8 +8,8 @@
 // vocabulary at a time.
 //
 // Measured (device time of a whole call): 8192 x 4096 x 131072 bfloat16
-// log-probabilities 5.29 ms, 1664 TFLOP/s under the power cap (0.97 of the
-// library product's sustained rate); 8192 x 4096 x 32768 alone 1.21 ms, 1820
+// log-probabilities 5.15 ms, 1709 TFLOP/s under the power cap (0.99 of the
+// library product's sustained rate); 8192 x 4096 x 32768 alone 1.15 ms, 1918
 // TFLOP/s; the gradient at 4096 x 4096 x 32768 1.82 ms, 1815 TFLOP/s.
 #include <algorithm>
 
@@ -368,8 +368,8 @@ __device__ __forceinline__ void store16(uint16_t* p, const float* v) {
 
 // part[half tile][part] = (max of acc, sum e, sum e acc) with
 // e = 2^(c2 (acc - max)), c2 = log2(e) / temperature.  The product runs at 80%
-// of the tensor pipe (2048 x 4096 x 32768: 312 us, 1761 TFLOP/s); without the
-// partial sums' TMEM reads 7% less time.  At k = 256 the epilogue's 32768
+// of the tensor pipe with partial sums every 512 k (2048 x 4096 x 32768: 312 us,
+// 1761 TFLOP/s); without their TMEM reads 7% less time.  At k = 256 the epilogue's 32768
 // exponentials a tile are the limit: 16 an SM and cycle, as long as the
 // product's 2048 cycles.
 struct StatsEpi {

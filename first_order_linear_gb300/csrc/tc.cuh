@@ -29,7 +29,8 @@
 // round (measured: the error of a sum grows with its number of k steps,
 // 1.7e-6 of a log-probability at k = 4096 against 3e-7 in plain float32).
 // GROUP > 0 therefore starts a new accumulator every GROUP stages and adds
-// the partial sums in float32 registers (about 4% of the product's time).
+// the partial sums in float32 registers; the TMEM reads cost 7% of the time at
+// 8 stages, 2 to 3% at 16.
 //
 // Every wait is bounded: a wait that gives up records the timeout in the
 // status word and raises a shared flag that ends the CTA's roles (the other
