@@ -150,43 +150,71 @@ __device__ __forceinline__ void split3(float v, float& hi, float& mid, float& lo
   lo = r - mid;
 }
 
-// eight elements from column c of a row that starts at element `at`, zeros
-// from `width` on
+// Eight elements from column c of a row that starts at element `at`, as they
+// lie in memory, zeros from `width` on.  `size`: elements from src to the end
+// of the matrix.  A row that starts off a 16-byte boundary is read as the
+// aligned vectors around the eight elements, shifted into place, where those
+// vectors lie inside the matrix; otherwise element by element.
 template <class ST>
-__device__ __forceinline__ void load8(const float* src, int64_t at, int64_t c, int64_t width, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= width) {
-    if constexpr (Stor<ST>::kBytes == 2) {
-      Stor<ST>::ld8(src, at + c, true, v);
+struct Eight {
+  static constexpr int ES = Stor<ST>::kBytes, NV = 8 * ES / 16;  // vectors that eight elements fill
+  uint32_t w[4 * NV + 4];
+
+  __device__ __forceinline__ void load(const float* src, int64_t size, int64_t at, int64_t c, int64_t width) {
+    const uintptr_t p = (uintptr_t)src + (uintptr_t)(at + c) * ES;
+    const uint32_t off = (uint32_t)(p & 15);
+    const uintptr_t lo = p - off, hi = lo + 16 * (NV + (off ? 1 : 0));
+    if (lo >= (uintptr_t)src && hi <= (uintptr_t)src + (uintptr_t)size * ES) {
+      const uint4* q = reinterpret_cast<const uint4*>(lo);
+#pragma unroll
+      for (int i = 0; i <= NV; ++i) {
+        const uint4 x = i < NV || off ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+      if (off) {
+#pragma unroll
+        for (int i = 0; i + 2 < 4 * NV + 4; ++i) w[i] = off & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i + 3 < 4 * NV + 4; ++i) w[i] = off & 4 ? w[i + 1] : w[i];
+        if (ES == 2 && (off & 2)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+      }
+      if (c + 8 > width) {
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) {
+          if (ES == 4) w[i] = c + i < width ? w[i] : 0u;
+          else w[i] = c + 2 * i + 1 < width ? w[i] : c + 2 * i < width ? w[i] & 0xffffu : 0u;
+        }
+      }
     } else {
-      Stor<ST>::ld4(src, at + c, true, v);
-      Stor<ST>::ld4(src, at + c + 4, true, v + 4);
+#pragma unroll
+      for (int i = 0; i < 4 * NV; ++i) {
+        if constexpr (ES == 4) {
+          w[i] = c + i < width ? __float_as_uint(Stor<ST>::ld(src, at + c + i)) : 0u;
+        } else {
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(src) + at + c + 2 * i;
+          w[i] = (c + 2 * i < width ? (uint32_t)__ldg(e) : 0u) | (c + 2 * i + 1 < width ? (uint32_t)__ldg(e + 1) << 16 : 0u);
+        }
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < width ? Stor<ST>::ld(src, at + c + i) : 0.f;
   }
-}
-
-// ... to element `to` of the packed planes, `plane` elements apart
-template <class ST>
-__device__ __forceinline__ void pack8(void* planes, int64_t to, int64_t plane, const float (&v)[8]) {
-  float* dst = static_cast<float*>(planes);  // Stor<bf16> counts in elements of two bytes
-  if constexpr (Stor<ST>::kBytes == 2) {
-    Stor<bf16>::st8(dst, to, v);
-  } else {
-    float h[8], m[8], l[8];
+  // ... to element `to` of the packed planes, `plane` elements apart
+  __device__ __forceinline__ void pack(void* planes, int64_t to, int64_t plane) const {
+    if constexpr (ES == 2) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(planes) + to) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float* dst = static_cast<float*>(planes);  // Stor<bf16> counts in elements of two bytes
+      float h[8], m[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split3(v[i], h[i], m[i], l[i]);
-    Stor<bf16>::st8(dst, to, h);
-    Stor<bf16>::st8(dst, to + plane, m);
-    Stor<bf16>::st8(dst, to + 2 * plane, l);
+      for (int i = 0; i < 8; ++i) split3(__uint_as_float(w[i]), h[i], m[i], l[i]);
+      Stor<bf16>::st8(dst, to, h);
+      Stor<bf16>::st8(dst, to + plane, m);
+      Stor<bf16>::st8(dst, to + 2 * plane, l);
+    }
   }
-}
-
-template <class ST>
-__device__ __forceinline__ bool rows_of_vectors(const float* p, int64_t stride) {
-  return ((uintptr_t)p & 15) == 0 && (stride * Stor<ST>::kBytes) % 16 == 0;
-}
+};
 
 constexpr int kPackThreads = 256;
 
@@ -223,7 +251,7 @@ __global__ void __launch_bounds__(kPackThreads)
   const bool pack = !(in_place && all == a.N);
   const int groups = (int)(Dp / 8);
   const int64_t plane = Np * Dp;
-  const bool vec = rows_of_vectors<ST>(a.hidden, a.hidden_stride);
+  const int64_t size = (a.N - 1) * a.hidden_stride + a.D;
   for (int64_t i0 = r0; i0 < r1; i0 += kPackThreads) {
     const int64_t i = i0 + threadIdx.x;
     const int tok = i < r1 ? a.tokens[i] : -1;
@@ -262,18 +290,18 @@ __global__ void __launch_bounds__(kPackThreads)
     }
     constexpr int B = 4;  // groups a thread has in flight
     for (int t0 = threadIdx.x; pack && t0 < n * groups; t0 += B * kPackThreads) {
-      float v[B][8];
+      Eight<ST> v[B];
       int64_t to[B];
 #pragma unroll
       for (int u = 0; u < B; ++u) {
         const int t = min(t0 + u * kPackThreads, n * groups - 1);
         const int r = t / groups, c = (t - r * groups) * 8;
-        load8<ST>(a.hidden, list[r] * a.hidden_stride, c, a.D, vec, v[u]);
+        v[u].load(a.hidden, size, list[r] * a.hidden_stride, c, a.D);
         to[u] = (int64_t)(before + r) * Dp + c;
       }
 #pragma unroll
       for (int u = 0; u < B; ++u)
-        if (t0 + u * kPackThreads < n * groups) pack8<ST>(w.hidden, to[u], plane, v[u]);
+        if (t0 + u * kPackThreads < n * groups) v[u].pack(w.hidden, to[u], plane);
     }
     before += n;
     __syncthreads();
@@ -282,15 +310,17 @@ __global__ void __launch_bounds__(kPackThreads)
   const int64_t end = min(Np, ((int64_t)all + kTcK - 1) / kTcK * kTcK);
   for (int64_t r = all + blockIdx.x; r < end; r += gridDim.x)
     for (int c = threadIdx.x; c < groups; c += kPackThreads) {
-      const float v[8] = {};
-      pack8<ST>(w.hidden, r * Dp + c * 8, plane, v);
+      Eight<ST> zero = {};
+      zero.pack(w.hidden, r * Dp + c * 8, plane);
     }
 }
 
 // the weight's rows [r0, r0 + rows) packed, zeros past the width (float32:
-// 89 MB to 134 MB in 33 us, bound by HBM)
+// 89 MB to 134 MB in 33 us; bfloat16 rows of 2999: 268 MB to 268 MB in 108 us,
+// 5 TB/s -- element by element 149 us; bound by HBM)
 struct PackArgs {
   const float* src;
+  int64_t size;  // elements from src to the end of the matrix
   int64_t r0, rows, width, stride;
   void* dst;  // planes x [dst_rows, pitch]
   int64_t pitch, dst_rows;
@@ -299,23 +329,25 @@ template <class ST>
 __global__ void __launch_bounds__(kPackThreads) head_pack_kernel(PackArgs a) {
   pdl_trigger();
   pdl_wait();
-  const uint32_t groups = (uint32_t)(a.pitch / 8);
-  const bool vec = rows_of_vectors<ST>(a.src, a.stride);
+  // a warp's lanes side by side on a row, or on several narrow ones
+  const int groups = (int)(a.pitch / 8);
+  int lanes = 32;
+  while (lanes > 1 && lanes / 2 >= groups) lanes /= 2;
+  const int lane = threadIdx.x & 31, sub = lane & (lanes - 1), rows = 32 / lanes;
+  const int64_t warp = (int64_t)blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * (kPackThreads / 32) * rows;
   constexpr int B = 4;
-  const int64_t total = a.rows * groups, step = (int64_t)gridDim.x * kPackThreads;
-  for (int64_t t0 = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; t0 < total; t0 += B * step) {
-    float v[B][8];
-    int64_t to[B];
+  for (int64_t r = warp * rows + lane / lanes; r < a.rows; r += step) {
+    const int64_t at = (a.r0 + r) * a.stride, to = r * a.pitch;
+    for (int g0 = sub; g0 < groups; g0 += B * lanes) {
+      Eight<ST> v[B];
 #pragma unroll
-    for (int u = 0; u < B; ++u) {
-      const int64_t t = min(t0 + u * step, total - 1);
-      const int64_t r = t / groups, c = (t - r * groups) * 8;
-      load8<ST>(a.src, (a.r0 + r) * a.stride, c, a.width, vec, v[u]);
-      to[u] = r * a.pitch + c;
+      for (int u = 0; u < B; ++u)
+        if (g0 + u * lanes < groups) v[u].load(a.src, a.size, at, (g0 + u * lanes) * 8, a.width);
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+        if (g0 + u * lanes < groups) v[u].pack(a.dst, to + (g0 + u * lanes) * 8, a.dst_rows * a.pitch);
     }
-#pragma unroll
-    for (int u = 0; u < B; ++u)
-      if (t0 + u * step < total) pack8<ST>(a.dst, to[u], a.dst_rows * a.pitch, v[u]);
   }
 }
 
@@ -772,6 +804,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     head_few_kernel(HeadArgs a, HeadView w, int64_t Ds, float c2) {
   extern __shared__ __align__(16) float few_hidden[];  // [NT][Ds], zeros past D
   constexpr int C = R * NT, W = kFewThreads / 32;
+  constexpr int kUnroll = VE == 1 ? (Stor<ST>::kBytes == 2 ? 6 : 8) : NT <= 2 ? 16 / R : 2;
   constexpr int kLog = C == 4 ? 2 : C == 8 ? 3 : C == 16 ? 4 : 5;  // log2 C
   __shared__ Stats acc[W][C];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -800,7 +833,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     for (int r = 0; r < R; ++r)
       base[r] = reinterpret_cast<const float*>(reinterpret_cast<const unsigned char*>(a.weight) +
                                                min(v0 + r, a.V - 1) * a.weight_stride * Stor<ST>::kBytes);
-#pragma unroll (NT <= 2 ? 16 / R : 2)
+#pragma unroll kUnroll
     for (int64_t j = lane; j < nv; j += 32) {
       float x[R][VE];
 #pragma unroll
@@ -1027,7 +1060,7 @@ struct HeadRun {
   cudaError_t weight_piece(int64_t v0, int64_t len) {
     if (!p.packed) return cudaSuccess;
     PackArgs k = {};
-    k.src = a.weight; k.r0 = v0; k.rows = len; k.width = a.D; k.stride = a.weight_stride;
+    k.src = a.weight; k.size = (a.V - 1) * a.weight_stride + a.D; k.r0 = v0; k.rows = len; k.width = a.D; k.stride = a.weight_stride;
     k.dst = w.weight; k.pitch = p.Dp; k.dst_rows = p.pitch;
     return launch_pdl(head_pack_kernel<ST>, std::min<int64_t>(div_up(len * (p.Dp / 8), 4 * kPackThreads), 8 * (int64_t)sm), kPackThreads, 0, s, k);
   }
