@@ -34,8 +34,11 @@
 //
 // Every wait is bounded: a wait that gives up records the timeout in the
 // status word and raises a shared flag that ends the CTA's roles (the other
-// CTA's waits then run out too); copies and matrix instructions in flight are
-// waited for (bounded) before TMEM is freed and the cluster ends together.
+// CTA's waits then run out too).  Each wait covers a few stages or one
+// accumulator, never the product, so its limit holds for products of any
+// length.  Once the roles of both CTAs have ended, copies and matrix
+// instructions in flight are waited for (bounded) before TMEM is freed and the
+// cluster ends together.
 #pragma once
 
 #include <type_traits>
@@ -520,6 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   };
 
+  TcRing copied;  // where the copies' thread has stopped
   // (without partial sums the launch's 168 registers are enough)
   if (warp >= kTcEpiWarps + 2) {
     // ---- idle ----
@@ -530,14 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (lane == 0) {
       // operands written by earlier kernels' ordinary stores, read by copies
       asm volatile("fence.proxy.async;" ::: "memory");
-      TcRing r;
-      each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_copy_tile(job, w, t, rank, sh, ring, r); });
-      // Every copy that was issued lands before the cluster ends (when all
-      // went well the matrix instructions have waited for it too).  Stage i
-      // was last filled in r.phase if i < r.stage, else in the phase before,
-      // or never: that wait returns at once.
-      if (rank == 0)
-        for (int i = 0; i < kTcStages; ++i) mbar_wait_bounded(&sh.full[i], i < r.stage ? r.phase : r.phase ^ 1);
+      each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_copy_tile(job, w, t, rank, sh, ring, copied); });
     }
   } else if (warp == kTcEpiWarps + 1) {
     // ---- matrix instructions ----
@@ -546,11 +543,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       TcRing r;
       TcAcc acc;
       each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_mma_tile(job, w, t, tmem, sh, ring, r, acc); });
-      // whatever was issued completes before TMEM is freed
       tc_commit(&sh.drained);
     }
-    // (in both CTAs: no arrival is still on its way when the cluster ends)
-    if (lane == 0) mbar_wait_bounded(&sh.drained, 0);
   } else {
     // ---- epilogue ----
     if constexpr (GROUP > 0) regs_take<kTcEpiRegs>();
@@ -558,9 +552,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     float* block = reinterpret_cast<float*>(ring + kTcStages * kTcStageBytes) + warp * kTcBlockFloats;
     each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_finish_tile(job, w, t, rank, tmem, sh, block, acc); });
   }
+  // The roles of both CTAs have ended: nothing more is issued, and what is
+  // still in flight is over shortly (a wait that began with the role would
+  // have to last as long as the other CTA's, the whole product).
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
+  // Every copy lands before the cluster ends (when all went well the matrix
+  // instructions have waited for it too).  Stage i was last filled in
+  // copied.phase if i < copied.stage, else in the phase before, or never:
+  // that wait returns at once.
+  if (threadIdx.x == 32 * kTcEpiWarps && rank == 0)
+    for (int i = 0; i < kTcStages; ++i)
+      mbar_wait_bounded(&sh.full[i], i < copied.stage ? copied.phase : copied.phase ^ 1);
+  // whatever was issued completes before TMEM is freed (in both CTAs: no
+  // arrival is still on its way when the cluster ends)
+  if (threadIdx.x == 32 * (kTcEpiWarps + 1)) mbar_wait_bounded(&sh.drained, 0);
+  __syncwarp();
   cluster_sync();
   tc_fence_after();
   if (warp == kTcEpiWarps + 1) tc_free(tmem, 2 * kTcN);
