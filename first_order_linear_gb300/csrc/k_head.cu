@@ -1011,8 +1011,10 @@ bool in_place(const HeadArgs& a) {
 }
 
 // Stages summed by the tensor cores alone (tc.cuh): 512 values of k for
-// results that leave in float32; the bfloat16 gradients' own rounding is
-// larger than the whole sum's error.  The logits of float32 operands, whose
+// results that leave in float32; 4096 for the bfloat16 gradients, whose sums
+// over rows or tokens may have millions of terms (a sum of one sign then stays
+// within 3e-5, a hundredth of its rounding; unbounded, d_weight of 3 million
+// such rows came out 1.8% too small).  The logits of float32 operands, whose
 // error is dz's relative error, take 128 (of the leading product only: 2 to 4%
 // of the time; gradients at 2 x 4000 x 20000 4.1e-7 off instead of 1.9e-6).
 // From k = 4096 on the groups are of 1024: with four or more of them each
@@ -1020,13 +1022,13 @@ bool in_place(const HeadArgs& a) {
 // x 32768: 5% less time, entropy 4.2e-7 off instead of 2.0e-7, up to 1.4e-6 at
 // temperature 0.7 over few tokens; at k = 2048 groups of 1024 would leave
 // 1.1e-6 at large vocabularies too).
-constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kLogitsGroupLong = 16;
+constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kLogitsGroupLong = 16, kGradGroupBf16 = 64;
 constexpr int64_t kLogitsLong = 4096;
 
 template <class ST>
 struct HeadRun {
   static constexpr bool kF32 = Stor<ST>::kBytes == 4;
-  static constexpr int kGradGroup = kF32 ? kLogitsGroup : 0, kDzGroup = kF32 ? kLogitsGroupF32 : 0,
+  static constexpr int kGradGroup = kF32 ? kLogitsGroup : kGradGroupBf16, kDzGroup = kF32 ? kLogitsGroupF32 : 0,
                        kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
   const HeadArgs& a;
   const HeadPlan p;

@@ -27,7 +27,8 @@
 //
 // The accumulator of a tensor core drops bits where IEEE addition would
 // round (measured: the error of a sum grows with its number of k steps,
-// 1.7e-6 of a log-probability at k = 4096 against 3e-7 in plain float32).
+// 1.7e-6 of a log-probability at k = 4096 against 3e-7 in plain float32; a sum
+// of one sign loses about 2e-7 of itself at each step of 16 k).
 // GROUP > 0 therefore starts a new accumulator every GROUP stages and adds
 // the partial sums in float32 registers; the TMEM reads cost 7% of the time at
 // 8 stages, 2 to 3% at 16.
