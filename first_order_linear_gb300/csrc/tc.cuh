@@ -272,13 +272,17 @@ struct TcWalk {
 };
 
 // End of the accumulation that starts at step `at` of terms x stages steps.
-// All terms but the last are at most 2^-8 of it: they share one accumulator,
-// whose dropped bits are that much smaller.
+// All terms but the last are at most 2^-8 of it: they share accumulators of
+// kTcLead steps, whose dropped bits are that much smaller.  (An accumulator
+// bounds the epilogue's wait, too: the lead terms of 16 million rows in one
+// would be 0.35 s, longer than a wait may last.)
+constexpr int kTcLead = 128;  // about 35 us
 template <int GROUP>
-__device__ __forceinline__ int tc_group_end(int at, int stages, int terms) {
-  if (GROUP == 0) return stages * terms;
-  const int lead = stages * (terms - 1);
-  return at < lead ? lead : min(at + GROUP, stages * terms);
+__host__ __device__ constexpr int tc_group_end(int at, int stages, int terms) {
+  const int all = stages * terms, lead = stages * (terms - 1);
+  if (GROUP == 0) return all;
+  const int end = at < lead ? at + kTcLead : at + GROUP, last = at < lead ? lead : all;
+  return end < last ? end : last;
 }
 
 // One product.  Epi: struct State; begin(State&, walk, tile, row, col0) with

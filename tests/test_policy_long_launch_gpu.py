@@ -55,3 +55,20 @@ def test_scoring_in_one_launch_of_over_a_fifth_of_a_second(cuda_lib):
     assert ((lse[rows] - lse0).abs() <= tol).all()
     assert ((logp[rows] - logp0).abs() <= tol).all()
     assert ((entropy[rows] - ent0).abs() <= tol * (1 + lse0.abs() + ent0.abs())).all()
+
+
+def test_float32_gradient_of_sixteen_million_rows(cuda_lib):
+    """One tile of d_weight is six products over all rows: 1.5 million steps
+    of one CTA pair, of which each wait covers 128 at most."""
+    from tests.test_policy_sums_gpu import exact, one_signed
+    N, D, V = 16_000_001, 8, 20
+    h, w, tok, g = one_signed(N, D, V, torch.float32, 2)
+    lse, dw0 = exact(h, w, g)
+    assert status(cuda_lib, clear=1) == 0
+    _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
+    torch.cuda.synchronize()
+    assert status(cuda_lib) == 0
+    # 32 steps of the tensor cores' sums at 2e-7 of one sign each, on average
+    # over them 3.2e-6; 31,251 partial sums added with errors of either sign,
+    # of 2^-25 / sqrt(3) each: 3e-6, of which four are allowed; 2e-6 for dz
+    assert ((dw[1:].double() - dw0) / dw0).abs().max().item() <= 3.2e-6 + 1.2e-5 + 2e-6
