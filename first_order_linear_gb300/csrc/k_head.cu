@@ -967,16 +967,14 @@ cudaError_t launch_product(const Job1& j1, const Job2& j2, int64_t tiles, int sm
   static std::atomic<uint64_t> allowed;
   cudaError_t e = allow_smem(kernel, kTcSmemBlocks, allowed);
   if (e != cudaSuccess) return e;
-  if (Job1::GROUP > 0) {
-    // the warpgroups' register shares are taken from the launch's registers:
-    // a kernel built with fewer would wait for the rest for ever
-    static const bool enough = [&] {
-      cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
-             f.numRegs * kTcThreads >= 32 * (kTcEpiWarps * kTcEpiRegs + 4 * kTcIssueRegs);
-    }();
-    if (!enough) return cudaErrorInvalidConfiguration;
-  }
+  // the warpgroups' register shares are taken from the launch's registers: a
+  // kernel built with fewer would wait for the rest for ever
+  static const bool enough = [&] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
+           f.numRegs * kTcThreads >= 32 * (kTcEpiWarps * kTcEpiRegs + 4 * kTcIssueRegs);
+  }();
+  if (!enough) return cudaErrorInvalidConfiguration;
   return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, blocks ? kTcSmemBlocks : kTcSmem, st, j1,
                     j2);
 }
@@ -1014,7 +1012,9 @@ bool in_place(const HeadArgs& a) {
 // results that leave in float32; 4096 for the bfloat16 gradients, whose sums
 // over rows or tokens may have millions of terms (a sum of one sign then stays
 // within 3e-5, a hundredth of its rounding; unbounded, d_weight of 3 million
-// such rows came out 1.8% too small).  The logits of float32 operands, whose
+// such rows came out 1.8% too small), and 1024 for the logits of their dz, where
+// 6e-6 of a logit, an error in the exponent of p, has to stay below dz's
+// rounding too (one sum over 65536 columns put 0.5% into every p).  The logits of float32 operands, whose
 // error is dz's relative error, take 128 (of the leading product only: 2 to 4%
 // of the time; gradients at 2 x 4000 x 20000 4.1e-7 off instead of 1.9e-6).
 // From k = 4096 on the groups are of 1024: with four or more of them each
@@ -1022,13 +1022,14 @@ bool in_place(const HeadArgs& a) {
 // x 32768: 5% less time, entropy 4.2e-7 off instead of 2.0e-7, up to 1.4e-6 at
 // temperature 0.7 over few tokens; at k = 2048 groups of 1024 would leave
 // 1.1e-6 at large vocabularies too).
-constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kLogitsGroupLong = 16, kGradGroupBf16 = 64;
+constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kLogitsGroupLong = 16, kGradGroupBf16 = 64,
+              kDzGroupBf16 = 16;
 constexpr int64_t kLogitsLong = 4096;
 
 template <class ST>
 struct HeadRun {
   static constexpr bool kF32 = Stor<ST>::kBytes == 4;
-  static constexpr int kGradGroup = kF32 ? kLogitsGroup : kGradGroupBf16, kDzGroup = kF32 ? kLogitsGroupF32 : 0,
+  static constexpr int kGradGroup = kF32 ? kLogitsGroup : kGradGroupBf16, kDzGroup = kF32 ? kLogitsGroupF32 : kDzGroupBf16,
                        kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
   const HeadArgs& a;
   const HeadPlan p;

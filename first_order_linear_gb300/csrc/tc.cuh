@@ -29,9 +29,9 @@
 // round (measured: the error of a sum grows with its number of k steps,
 // 1.7e-6 of a log-probability at k = 4096 against 3e-7 in plain float32; a sum
 // of one sign loses about 2e-7 of itself at each step of 16 k).
-// GROUP > 0 therefore starts a new accumulator every GROUP stages and adds
-// the partial sums in float32 registers; the TMEM reads cost 7% of the time at
-// 8 stages, 2 to 3% at 16.
+// A new accumulator therefore starts every GROUP stages, and the partial sums
+// are added in float32 registers; the TMEM reads cost 7% of the time at 8
+// stages, 2 to 3% at 16.
 //
 // Every wait is bounded: a wait that gives up records the timeout in the
 // status word and raises a shared flag that ends the CTA's roles (the other
@@ -119,29 +119,7 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// Starts the load of 32 columns of this warp's 32 TMEM lanes (one row a
-// thread); the values are there after tc_load_wait.
-__device__ __forceinline__ void tc_load32(uint32_t addr, float (&v)[32]) {
-  __syncwarp();
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(addr)
-      : "memory");
-}
-// waits for this thread's loads so far; v passes through so that its uses stay behind the wait
-__device__ __forceinline__ void tc_load_wait(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
-}
-
-// ... 16 columns, added to v
+// 16 columns of this warp's 32 TMEM lanes (one row a thread), added to v
 __device__ __forceinline__ void tc_add16(uint32_t addr, float* v) {
   uint32_t r[16];
   __syncwarp();
@@ -280,7 +258,7 @@ constexpr int kTcLead = 128;  // about 35 us
 template <int GROUP>
 __host__ __device__ constexpr int tc_group_end(int at, int stages, int terms) {
   const int all = stages * terms, lead = stages * (terms - 1);
-  if (GROUP == 0) return all;
+  static_assert(GROUP > 0 && GROUP <= kTcLead);
   const int end = at < lead ? at + kTcLead : at + GROUP, last = at < lead ? lead : all;
   return end < last ? end : last;
 }
@@ -422,48 +400,22 @@ __device__ __forceinline__ bool tc_finish_tile(const Job& job, const TcWalk& wal
   const int col0 = tile.n0 + half * (kTcN / 2);
   typename Job::Epi::State st;
   job.epi.begin(st, walk, tile, tile.m0 + rank * kTcRows + quarter * 32 + lane, col0);
-  if constexpr (Job::GROUP > 0) {
-    float sum[kTcN / 64][32];
+  float sum[kTcN / 64][32];
 #pragma unroll
-    for (int c = 0; c < kTcN / 64; ++c)
+  for (int c = 0; c < kTcN / 64; ++c)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-    for (int at = 0; at < steps; at = tc_group_end<Job::GROUP>(at, stages, job.s.terms.n)) {
-      if (!ready()) return false;
+    for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+  for (int at = 0; at < steps; at = tc_group_end<Job::GROUP>(at, stages, job.s.terms.n)) {
+    if (!ready()) return false;
 #pragma unroll
-      for (int c = 0; c < kTcN / 64; ++c) {
-        tc_add16(src0 + acc.buf * kTcN + 32 * c, sum[c]);
-        tc_add16(src0 + acc.buf * kTcN + 32 * c + 16, sum[c] + 16);
-      }
-      done();
+    for (int c = 0; c < kTcN / 64; ++c) {
+      tc_add16(src0 + acc.buf * kTcN + 32 * c, sum[c]);
+      tc_add16(src0 + acc.buf * kTcN + 32 * c + 16, sum[c] + 16);
     }
-#pragma unroll
-    for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c], block);
-  } else {
-    float v[32], w[32];  // one is worked on while the other is loaded
-    if (steps > 0) {
-      if (!ready()) return false;
-      const uint32_t src = src0 + acc.buf * kTcN;
-      tc_load32(src, v);
-#pragma unroll 1
-      for (int c = 0; c < kTcN / 2; c += 64) {
-        tc_load_wait(v);
-        tc_load32(src + c + 32, w);
-        job.epi.chunk(st, col0 + c, v, block);
-        tc_load_wait(w);
-        if (c + 64 < kTcN / 2) tc_load32(src + c + 64, v);
-        else done();
-        job.epi.chunk(st, col0 + c + 32, w, block);
-      }
-    } else {
-#pragma unroll 1
-      for (int c = 0; c < kTcN / 2; c += 32) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        job.epi.chunk(st, col0 + c, v, block);
-      }
-    }
+    done();
   }
+#pragma unroll
+  for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c], block);
   job.epi.end(st);
   return true;
 }
@@ -474,7 +426,6 @@ template <class Job1, class Job2>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_product_kernel(const __grid_constant__ Job1 j1, const __grid_constant__ Job2 j2) {
   constexpr bool two = !std::is_same_v<Job2, TcNoJob>;
-  constexpr int GROUP = Job1::GROUP;
   extern __shared__ unsigned char tc_smem_raw[];
   __shared__ __align__(8) TcShared sh;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)tc_smem_raw + 1023) & ~(uintptr_t)1023);
@@ -529,13 +480,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   };
 
   TcRing copied;  // where the copies' thread has stopped
-  // (without partial sums the launch's 168 registers are enough)
   if (warp >= kTcEpiWarps + 2) {
     // ---- idle ----
-    if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
+    regs_give<kTcIssueRegs>();
   } else if (warp == kTcEpiWarps) {
     // ---- copies ----
-    if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
+    regs_give<kTcIssueRegs>();
     if (lane == 0) {
       // operands written by earlier kernels' ordinary stores, read by copies
       asm volatile("fence.proxy.async;" ::: "memory");
@@ -543,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == kTcEpiWarps + 1) {
     // ---- matrix instructions ----
-    if constexpr (GROUP > 0) regs_give<kTcIssueRegs>();
+    regs_give<kTcIssueRegs>();
     if (lane == 0 && rank == 0) {
       TcRing r;
       TcAcc acc;
@@ -552,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ---- epilogue ----
-    if constexpr (GROUP > 0) regs_take<kTcEpiRegs>();
+    regs_take<kTcEpiRegs>();
     TcAcc acc;
     float* block = reinterpret_cast<float*>(ring + kTcStages * kTcStageBytes) + warp * kTcBlockFloats;
     each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_finish_tile(job, w, t, rank, tmem, sh, block, acc); });

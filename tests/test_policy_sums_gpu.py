@@ -49,3 +49,19 @@ def test_weight_gradient_of_millions_of_bfloat16_rows():
     _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
     bias = ((dw[1:].double() - dw0.bfloat16().double()) / dw0).mean().item()
     assert abs(bias) <= 2.6e-5 + 4e-5, bias
+
+
+def test_probabilities_of_wide_bfloat16_rows():
+    """Logits of 16 that add up from 65536 terms of one sign: an accumulator
+    restarted every 64 steps loses 6.4e-6 of them on average, 1e-4 in the
+    exponent of p and so of every dz; as much again is allowed.  One
+    accumulator for all 4096 steps would make it 6.6e-3."""
+    N, D, V = 64, 65536, 300
+    h, _, tok, g = one_signed(N, D, V, torch.bfloat16, 3)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    w = ((0.75 + 0.5 * torch.rand((V, D), generator=gen, device="cuda")) * (16.0 / h.float().sum(1).mean())).bfloat16()
+    lse, dw0 = exact(h, w, g)
+    _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
+    bias = ((dw[1:].double() - dw0.bfloat16().double()) / dw0).mean().item()
+    assert abs(bias) <= 2e-4, bias
