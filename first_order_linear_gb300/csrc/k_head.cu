@@ -398,8 +398,11 @@ __device__ __forceinline__ void store16(uint16_t* p, const float* v) {
   store32(p, w);
 }
 
-// part[half tile][part] = (max of acc, sum e, sum e acc) with
-// e = 2^(c2 (acc - max)), c2 = log2(e) / temperature.  The product runs at 80%
+// part[half tile][part] = (max of acc, sum e, sum e (acc - max)) with
+// e = 2^(c2 (acc - max)), c2 = log2(e) / temperature.  Logits enter as their
+// differences to the max, both in the exponent and in the second sum: with
+// max c2 rounded apart, or the products e acc, the errors would have the size
+// of the logits instead of their spread.  The product runs at 80%
 // of the tensor pipe with partial sums every 512 k (2048 x 4096 x 32768: 312 us,
 // 1761 TFLOP/s); without their TMEM reads 7% less time.  At k = 256 the epilogue's 32768
 // exponentials a tile are the limit: 16 an SM and cycle, as long as the
@@ -428,26 +431,34 @@ struct StatsEpi {
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     const int n = v_end - v0 - col;  // columns that exist
     if (n <= 0) return;
-    if (n < 32) {
+    const int k = st.at - col;
+    if (k >= 0 && k < 32) {
+      float z = v[0];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = i < n ? v[i] : -3.402823466e38f;
+      for (int i = 1; i < 32; ++i) z = i == k ? v[i] : z;
+      if (in_range(st.m, Np)) taken[st.m] = z;
+    }
+    if (n < 32) {  // the others take the first one's place here and are left out of the sums below
+#pragma unroll
+      for (int i = 1; i < 32; ++i) v[i] = i < n ? v[i] : v[0];
     }
     float top = st.top;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(v[i]), "f"(v[i + 1]));
-    // the first chunk: 0 drops the empty sums (kept off inf - inf)
-    const float f = st.top == -INFINITY ? 0.f : exp2_approx((st.top - top) * c2);
-    const float off = -top * c2;
-    const uint64_t c22 = pair_of(c2, c2), off2 = pair_of(off, off);
-    uint64_t s2 = pair_of(st.s * f, 0.f), t2 = pair_of(st.t * f, 0.f);
+    // (the first chunk: there are no sums to carry over)
+    const float down = st.top == -INFINITY ? 0.f : st.top - top, f = exp2_approx(down * c2);
+    const uint64_t c22 = pair_of(c2, c2), off2 = pair_of(-top, -top);
+    uint64_t s2 = pair_of(st.s * f, 0.f), t2 = pair_of(fmaf(st.s, down, st.t) * f, 0.f);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const uint64_t z = pair_of(v[i], v[i + 1]);
+      const uint64_t d = pair_add(pair_of(v[i], v[i + 1]), off2);
       float x0, x1;
-      pair_open(pair_fma(z, c22, off2), x0, x1);
-      const uint64_t e = pair_of(exp2_approx(x0), exp2_approx(x1));
+      pair_open(pair_mul(d, c22), x0, x1);
+      x0 = exp2_approx(x0), x1 = exp2_approx(x1);
+      if (n < 32) x0 = i < n ? x0 : 0.f, x1 = i + 1 < n ? x1 : 0.f;
+      const uint64_t e = pair_of(x0, x1);
       s2 = pair_add(s2, e);
-      t2 = pair_fma(e, z, t2);
+      t2 = pair_fma(e, d, t2);
     }
     float s, t, hi;
     pair_open(s2, s, hi);
@@ -457,13 +468,6 @@ struct StatsEpi {
     st.top = top;
     st.s = s;
     st.t = t;
-    const int k = st.at - col;
-    if (k >= 0 && k < 32) {
-      float z = v[0];
-#pragma unroll
-      for (int i = 1; i < 32; ++i) z = i == k ? v[i] : z;
-      if (in_range(st.m, Np)) taken[st.m] = z;
-    }
   }
   __device__ __forceinline__ void end(State& st) const {
     const int64_t at = (int64_t)((v0 + st.col0) / (kTcN / 2)) * Np + st.m;
@@ -692,15 +696,16 @@ struct OutEpi {
 constexpr int kJoinThreads = 256;
 
 // partial statistics over some of a part's tokens: the largest value z (before
-// the temperature), the sum of e = 2^(c2 (z - top)), the sum of e z
+// the temperature), the sum of e = 2^(c2 (z - top)), the sum of e (z - top)
 struct Stats {
   float top, s, t;
   __device__ __forceinline__ void add(float top2, float s2, float t2, float c2) {
     if (s2 == 0.f) return;  // none
     const float m = fmaxf(top, top2);
-    const float f = s == 0.f ? 0.f : exp2_approx((top - m) * c2), f2 = exp2_approx((top2 - m) * c2);
+    const float down = s == 0.f ? 0.f : top - m, down2 = top2 - m;
+    const float f = exp2_approx(down * c2), f2 = exp2_approx(down2 * c2);
+    t = fmaf(fmaf(s, down, t), f, fmaf(s2, down2, t2) * f2);
     s = fmaf(s, f, s2 * f2);
-    t = fmaf(t, f, t2 * f2);
     top = m;
   }
 };
@@ -710,7 +715,7 @@ __device__ __forceinline__ void finish(const HeadArgs& a, const HeadView& w, int
   const float inv_t = a.inv_temperature, log_s = logf(st.s);
   a.lse[row] = fmaf(st.top, inv_t, log_s);
   a.logp[row] = fmaf(w.taken[m] - st.top, inv_t, -log_s);
-  if (a.entropy) a.entropy[row] = fmaf(st.top - st.t / st.s, inv_t, log_s);
+  if (a.entropy) a.entropy[row] = fmaf(-st.t / st.s, inv_t, log_s);
 }
 
 // (33 MB of statistics at 8192 parts x 256 half tiles: 17 us cold, 1.4% of
@@ -886,7 +891,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
       }
     }
     if (v0 + my_tok < a.V) {
-      st.add(z[0], 1.f, z[0], c2);
+      st.add(z[0], 1.f, 0.f, c2);
       if (v0 + my_tok == taken_tok && (lane & ((32 >> kLog) - 1)) == 0) w.taken[my_row] = z[0];
     }
   }
