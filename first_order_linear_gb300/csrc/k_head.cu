@@ -476,8 +476,10 @@ struct StatsEpi {
 };
 
 // (2048 x 4096 x 16384: 148 us, 88% of the tensor pipe.)
-// dz = p (a0 + a1 acc), plus g / temperature for the token taken: as three
-// planes where the operands are float32; for bfloat16 operands as one
+// dz = p (a0 + a1 log p), plus g / temperature for the token taken, with
+// log p = acc / temperature - lse rounded once, for the exponent and the factor
+// alike: terms of the size of the logits or of lse would leave their rounding
+// in either.  As three planes where the operands are float32; for bfloat16 operands as one
 // bfloat16, rounded once because the two products that read it run on
 // bfloat16 -- its error of 2^-9 a term is as large as the rounding of the
 // gradients themselves, and adds to it.  Up to 128 rows a second bfloat16
@@ -495,7 +497,7 @@ struct DzEpi {
   bool two;
 
   struct State {
-    float lse, a0, a1, g;  // lse before the temperature
+    float lse, a0, a1, g;
     int at;
     bool live, skip;
     uint16_t* row;
@@ -510,26 +512,23 @@ struct DzEpi {
       const float4 f = info[row];
       st.at = tok[row] - v0;
       st.g = f.x * inv_t;
-      st.a0 = -(f.x + f.y * (f.w - f.z)) * inv_t;
-      st.a1 = -f.y * inv_t * inv_t;
-      st.lse = f.z / inv_t;
+      st.a0 = -fmaf(f.y, f.w, f.x) * inv_t;
+      st.a1 = -f.y * inv_t;
+      st.lse = f.z;
     }
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     if (st.skip) return;
-    const float c2 = inv_t * kLog2e;
     const int k = st.at - col;
-    // (the difference first: z c2 and lse c2 rounded apart would put an error
-    // of their size, not of the difference's, into the exponent)
-    const uint64_t c22 = pair_of(c2, c2), l2 = pair_of(-st.lse, -st.lse);
+    const uint64_t t2 = pair_of(inv_t, inv_t), l2 = pair_of(-st.lse, -st.lse), e2 = pair_of(kLog2e, kLog2e);
     const uint64_t a02 = pair_of(st.a0, st.a0), a12 = pair_of(st.a1, st.a1);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const uint64_t z = pair_of(v[i], v[i + 1]);
+      const uint64_t logp = pair_fma(pair_of(v[i], v[i + 1]), t2, l2);
       float x0, x1;
-      pair_open(pair_mul(pair_add(z, l2), c22), x0, x1);
+      pair_open(pair_mul(logp, e2), x0, x1);
       const uint64_t p = pair_of(exp2_approx(x0), exp2_approx(x1));
-      pair_open(pair_mul(p, pair_fma(a12, z, a02)), v[i], v[i + 1]);
+      pair_open(pair_mul(p, pair_fma(a12, logp, a02)), v[i], v[i + 1]);
     }
     if (k >= 0 && k < 32) {
 #pragma unroll

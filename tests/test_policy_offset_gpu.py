@@ -69,3 +69,35 @@ def test_statistics_do_not_feel_a_common_offset(cuda_lib, N, V, offset, temperat
     assert ((logp - logp0).abs() <= rel + 4 * U * logp0.abs()).all(), (logp - logp0).abs().max().item()
     assert ((ent - ent0).abs() <= rel * (1 + below)).all(), (ent - ent0).abs().max().item()
     assert ((lse - lse0).abs() <= rel + U * lse0.abs()).all(), (lse - lse0).abs().max().item()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 2.0])
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("N,V", SIZES)
+def test_gradients_do_not_feel_a_common_offset(cuda_lib, N, V, offset, temperature, dtype):
+    # the factor that is multiplied with the logits is 1 / temperature in
+    # float32: the reference takes its exact inverse
+    exact_t = 1.0 / float(torch.tensor(1.0 / temperature, dtype=torch.float32).double())
+    h, w, tok, z = offset_inputs(N, V, offset, DT[dtype], N + V)
+    x = z / exact_t
+    lse = torch.logsumexp(x, 1).float()
+    logq = x - torch.logsumexp(x, 1)[:, None]
+    ent = -(logq.exp() * logq).sum(1).float()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    g, e = (torch.randn(N, generator=gen, device="cuda") / N for _ in range(2))
+    dh, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse, g, entropy=ent, d_entropy=e, temperature=exact_t)
+    dh0, dw0, *_ = ref.token_logprob_backward(h, w, tok, lse, g, ent, e, exact_t)
+    # dz's terms, each with its own relative error
+    logq32 = x - lse.double()[:, None]
+    p, gd, ed = logq32.exp(), g.double().abs()[:, None], e.double().abs()[:, None]
+    taken = torch.zeros_like(p).scatter_(1, tok.long()[:, None], 1.0)
+    err = (8 + 2 * logq32.abs()) * U * p * (gd + ed * (logq32.abs() + ent.double()[:, None])) + 4 * U * gd * taken
+    mag = p * (gd + ed * (logq32 + ent.double()[:, None]).abs()) + gd * taken
+    rd, out = ((R if N > 128 else R * R), R) if dtype == "bf16" else (0.0, U)
+    for got, want, left, right, K, name in ((dh, dh0, (err, mag), w.double().abs(), V, "d_hidden"),
+                                            (dw, dw0, (err.t(), mag.t()), h.double().abs(), N, "d_weight")):
+        tol = (left[0] + (rd + (4 * math.sqrt(K) + 32) * U) * left[1]) @ right / exact_t + out * want.abs()
+        over = (got.double() - want).abs() - tol
+        assert over.max().item() <= 0, (name, over.max().item(), tol.reshape(-1)[over.argmax()].item())
