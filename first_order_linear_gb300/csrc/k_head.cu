@@ -1021,14 +1021,11 @@ bool in_place(const HeadArgs& a) {
 // rounding too (one sum over 65536 columns put 0.5% into every p).  The logits of float32 operands, whose
 // error is dz's relative error, take 128 (of the leading product only: 2 to 4%
 // of the time; gradients at 2 x 4000 x 20000 4.1e-7 off instead of 1.9e-6).
-// From k = 4096 on the groups are of 1024: with four or more of them each
-// partial sum is that much smaller, and so are the bits it drops (8192 x 4096
-// x 32768: 5% less time, entropy 4.2e-7 off instead of 2.0e-7, up to 1.4e-6 at
-// temperature 0.7 over few tokens; at k = 2048 groups of 1024 would leave
-// 1.1e-6 at large vocabularies too).
-constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kLogitsGroupLong = 16, kGradGroupBf16 = 64,
-              kDzGroupBf16 = 16;
-constexpr int64_t kLogitsLong = 4096;
+// The error grows with the group and not with the width: 512 x 1024 to 8192 x
+// 4001, bfloat16, log-probabilities 1.8e-7 to 2.1e-7 off in groups of 512 (a plain
+// float32 form 1.6e-7 to 6.1e-7), 3.9e-7 to 4.3e-7 in groups of 1024, which take
+// 3 to 5% less time.
+constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kGradGroupBf16 = 64, kDzGroupBf16 = 16;
 
 template <class ST>
 struct HeadRun {
@@ -1096,10 +1093,7 @@ struct HeadRun {
       if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, div_up(a.V, kTcN) * 2, (int)v0, (int)(v0 + len), c2};
       const TcShape t = logits_shape(v0, len);
-      if (!kF32 && a.D >= kLogitsLong)
-        e = launch_product(TcJob<false, false, kLogitsGroupLong, StatsEpi>{hidden_k, wk, in_place_k, t, epi}, sm, s);
-      else
-        e = launch_product(TcJob<false, false, kStatsGroup, StatsEpi>{hidden_k, wk, in_place_k, t, epi}, sm, s);
+      e = launch_product(TcJob<false, false, kStatsGroup, StatsEpi>{hidden_k, wk, in_place_k, t, epi}, sm, s);
     }
     return e == cudaSuccess ? join(div_up(a.V, kTcN) * 2, p.Np, false) : e;
   }
