@@ -374,15 +374,13 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
   }
   float mean = 0.f, rstd = 0.f;
   if (row < a.N) mean = a.mean[row], rstd = a.rstd[row];
-  int stage = 0, slot = 0;
-  uint32_t phase = 0;
-  bool ok = true;
+  int slot = 0;
+  FillRing<kRingRows> ring;
   for (; row < a.N; row += step) {
     // the stage before this one was read in the last round
-    if (lane == 0 && ok && row + (kRingRows - 1) * step < a.N)
-      fill(stage == 0 ? kRingRows - 1 : stage - 1, row + (kRingRows - 1) * step);
-    if (ok) ok = mbar_wait_bounded(&full[stage], phase);
-    const unsigned char* at = ring_rows + (size_t)stage * 2 * row_bytes;
+    if (lane == 0 && ring.ok && row + (kRingRows - 1) * step < a.N) fill(ring.fill_stage(), row + (kRingRows - 1) * step);
+    if (ring.ok) ring.ok = mbar_wait_bounded(&full[ring.stage], ring.phase);
+    const unsigned char* at = ring_rows + (size_t)ring.stage * 2 * row_bytes;
     float xh[VPT][VE], g[VPT][VE];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -417,7 +415,7 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
     s1 = warp_sum(l < TPR / 32 ? scratch[slot][0][l] : 0.f) * inv_d;
     s2 = warp_sum(l < TPR / 32 ? scratch[slot][1][l] : 0.f) * inv_d;
     slot ^= 1;
-    if (++stage == kRingRows) stage = 0, phase ^= 1;
+    ring.next();
     if (a.dx == nullptr) continue;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -428,8 +426,8 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
     }
   }
   // (copies still on their way after a wait gave up land before the CTA ends)
-  if (!ok && lane == 0)
-    for (int i = 0; i < kRingRows; ++i) mbar_wait_bounded(&full[i], i < stage ? phase ^ 1 : phase);
+  if (!ring.ok && lane == 0)
+    for (int i = 0; i < kRingRows; ++i) mbar_wait_bounded(&full[i], ring.last_fill(i));
   if (a.dweight == nullptr && a.dbias == nullptr) return;
   float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D;
 #pragma unroll

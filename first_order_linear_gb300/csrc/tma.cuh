@@ -81,6 +81,23 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// Bookkeeping of a ring of shared-memory stages that one thread fills, one
+// stage behind the one being read.  Once a wait has given up nothing is filled
+// any more and the position stays: it says which fill of each stage may still
+// be on its way.
+template <int STAGES>
+struct FillRing {
+  int stage = 0;  // being read
+  uint32_t phase = 0;
+  bool ok = true;
+  __host__ __device__ int fill_stage() const { return stage == 0 ? STAGES - 1 : stage - 1; }
+  __host__ __device__ void next() {
+    if (ok && ++stage == STAGES) stage = 0, phase ^= 1;
+  }
+  // parity of the last fill of stage i: behind the position it was the next turn's
+  __host__ __device__ uint32_t last_fill(int i) const { return i < stage ? phase ^ 1 : phase; }
+};
+
 // one [rows, EW] tile at (x = first environment, y = first step) of a 2-D map
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
