@@ -60,6 +60,8 @@ __device__ __forceinline__ ClipItem clip_item(const ClipTable<CAP>& t, uint32_t 
   it.at = (int64_t)(chunk - t.first[lo]) * kClipChunk;
   it.n = min(kClipChunk, size - it.at);
   it.bf16_io = t.size[lo] < 0;
+  // (an empty chunk, so nothing is touched, where this one is not the tensor's)
+  if (!in_range(lo, t.count) || !in_range(it.at, size) || !span_in_range(it.at, it.n, size)) it.at = it.n = 0;
   return it;
 }
 
@@ -146,6 +148,9 @@ __device__ __forceinline__ ClipSpan clip_span(const ClipItem& it) {
   s.lead = min((int64_t)(((16 - (at & 15)) & 15) / es), it.n);
   s.vecs = (it.n - s.lead) / (16 / es);
   s.tail = s.lead + s.vecs * (16 / es);
+  // (only single elements, each checked, where the vectors are not the chunk's or not on their boundary)
+  if (s.vecs > 0 && (!span_in_range(s.lead, s.vecs * (16 / es), it.n) || !in_range((int64_t)((at + s.lead * es) & 15), 1)))
+    s.lead = s.vecs = s.tail = 0;
   return s;
 }
 
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(kClipThreads)
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(it.grad) + (it.at + sp.lead) * es);
     // float32 over at most kClipChunk / kClipThreads squares, float64 beyond
     float s = it.bf16_io ? chunk_squares<true>(p, (int)sp.vecs) : chunk_squares<false>(p, (int)sp.vecs);
-    if (threadIdx.x < sp.lead) {
+    if (threadIdx.x < sp.lead && in_range(threadIdx.x, it.n)) {
       const float g = load_any(it.grad, it.at + threadIdx.x, it.bf16_io);
       s = fmaf(g, g, s);
     }
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kClipThreads, 5)
     uint4* o = reinterpret_cast<uint4*>(static_cast<unsigned char*>(it.out) + (it.at + sp.lead) * es);
     if (it.bf16_io) chunk_scale<true>(p, o, (int)sp.vecs, scale);
     else chunk_scale<false>(p, o, (int)sp.vecs, scale);
-    if (threadIdx.x < sp.lead)
+    if (threadIdx.x < sp.lead && in_range(threadIdx.x, it.n))
       store_any(it.out, it.at + threadIdx.x, it.bf16_io, load_any(it.grad, it.at + threadIdx.x, it.bf16_io) * scale);
     for (int64_t e = sp.tail + threadIdx.x; e < it.n; e += kClipThreads)
       store_any(it.out, it.at + e, it.bf16_io, load_any(it.grad, it.at + e, it.bf16_io) * scale);

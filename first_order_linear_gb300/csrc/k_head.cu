@@ -56,6 +56,7 @@ struct HeadPlan {
   int row_tiles, d_tiles, splits;
   bool two_dz;      // dz as two bfloat16 values (their sum), the second's rows after the first's
   size_t count, rows, tok, info, hidden, weight, part, taken, dz, dh;  // byte offsets
+  int64_t part_size, dh_size;  // elements
   size_t bytes;
 };
 
@@ -102,10 +103,14 @@ HeadPlan plan_head(int64_t N, int64_t D, int64_t V, bool bf16_io, bool backward,
       p.splits = (int)std::max<int64_t>(
           1, std::min({(int64_t)sm_count / 2 / out_tiles, 1 + kSplitBytes / out_bytes, div_up(stages, kSplitStages)}));
     // (one piece, not split: the product writes d_hidden itself)
-    if (p.splits > 1 || piece_tiles < tiles) p.dh = take((size_t)(p.two_dz ? 2 : 1) * p.splits * out_bytes);
+    if (p.splits > 1 || piece_tiles < tiles) {
+      p.dh_size = (p.two_dz ? 2 : 1) * p.splits * p.Np * p.Dh;
+      p.dh = take((size_t)p.dh_size * sizeof(float));
+    }
   } else {
     // (head_few_kernel: one piece a CTA, of at most 16 rows)
-    p.part = take(std::max((size_t)tiles * 2 * p.Np, (size_t)few_pieces(sm_count) * 16) * sizeof(float4));
+    p.part_size = std::max(tiles * 2 * p.Np, few_pieces(sm_count) * 16);
+    p.part = take((size_t)p.part_size * sizeof(float4));
     p.taken = take((size_t)p.Np * 4);
   }
   p.bytes = at + 255;
@@ -122,6 +127,8 @@ struct HeadView {  // the workspace's arrays on the device
   float* taken;
   uint16_t* dz;
   float* dh;
+  // elements of part, hidden, weight (planes and all) and dh
+  int64_t part_size, hidden_size, weight_size, dh_size;
   HeadView(const HeadPlan& p, void* ws) {
     unsigned char* b = reinterpret_cast<unsigned char*>(((uintptr_t)ws + 255) & ~(uintptr_t)255);
     count = reinterpret_cast<int*>(b + p.count);
@@ -134,6 +141,9 @@ struct HeadView {  // the workspace's arrays on the device
     taken = reinterpret_cast<float*>(b + p.taken);
     dz = reinterpret_cast<uint16_t*>(b + p.dz);
     dh = reinterpret_cast<float*>(b + p.dh);
+    part_size = p.part_size, dh_size = p.dh_size;
+    hidden_size = p.planes * p.Np * p.Dp;
+    weight_size = p.packed ? p.planes * p.pitch * p.Dp : 0;
   }
 };
 
@@ -192,16 +202,19 @@ struct Eight {
 #pragma unroll
       for (int i = 0; i < 4 * NV; ++i) {
         if constexpr (ES == 4) {
-          w[i] = c + i < width ? __float_as_uint(Stor<ST>::ld(src, at + c + i)) : 0u;
+          w[i] = c + i < width && in_range(at + c + i, size) ? __float_as_uint(Stor<ST>::ld(src, at + c + i)) : 0u;
         } else {
-          const uint16_t* e = reinterpret_cast<const uint16_t*>(src) + at + c + 2 * i;
-          w[i] = (c + 2 * i < width ? (uint32_t)__ldg(e) : 0u) | (c + 2 * i + 1 < width ? (uint32_t)__ldg(e + 1) << 16 : 0u);
+          const int64_t k = c + 2 * i;
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(src) + at + k;
+          w[i] = (k < width && in_range(at + k, size) ? (uint32_t)__ldg(e) : 0u) |
+                 (k + 1 < width && in_range(at + k + 1, size) ? (uint32_t)__ldg(e + 1) << 16 : 0u);
         }
       }
     }
   }
-  // ... to element `to` of the packed planes, `plane` elements apart
-  __device__ __forceinline__ void pack(void* planes, int64_t to, int64_t plane) const {
+  // ... to element `to` of the packed planes, `plane` elements apart, `size` in all
+  __device__ __forceinline__ void pack(void* planes, int64_t to, int64_t plane, int64_t size) const {
+    if (!span_in_range(to, 8 + (ES == 2 ? 0 : 2 * plane), size)) return;
     if constexpr (ES == 2) {
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(planes) + to) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
@@ -265,14 +278,14 @@ __global__ void __launch_bounds__(kPackThreads)
       at += k < warp ? scratch[k] : 0;
       n += scratch[k];
     }
-    if (on && in_range(before + at, a.N)) {
+    if (on && in_range(before + at, a.N) && in_range(at, kPackThreads)) {
       list[at] = (int)i;
       w.rows[before + at] = (int)i;
       w.tok[before + at] = tok;
       if (a.d_logp != nullptr)
         w.info[before + at] = make_float4(a.d_logp[i], a.d_entropy ? a.d_entropy[i] : 0.f, a.in_lse[i],
                                           a.d_entropy ? a.in_entropy[i] : 0.f);
-    } else if (!on && i < r1) {
+    } else if (!on && i < r1 && in_range((i - i0) - at, kPackThreads)) {
       list[kPackThreads - 1 - ((int)(i - i0) - at)] = (int)i;  // from the end: those that do not
       if (a.logp != nullptr) {
         a.logp[i] = 0.f;
@@ -285,7 +298,8 @@ __global__ void __launch_bounds__(kPackThreads)
       const int off = (int)min((int64_t)kPackThreads, r1 - i0) - n;
       for (int r = 0; r < off; ++r) {
         const int64_t to = list[kPackThreads - 1 - r] * a.D;
-        for (int64_t c = threadIdx.x; c < a.D; c += kPackThreads) Stor<ST>::st(a.d_hidden, to + c, 0.f);
+        for (int64_t c = threadIdx.x; c < a.D; c += kPackThreads)
+          if (in_range(to + c, a.N * a.D)) Stor<ST>::st(a.d_hidden, to + c, 0.f);
       }
     }
     constexpr int B = 4;  // groups a thread has in flight
@@ -301,7 +315,7 @@ __global__ void __launch_bounds__(kPackThreads)
       }
 #pragma unroll
       for (int u = 0; u < B; ++u)
-        if (t0 + u * kPackThreads < n * groups) v[u].pack(w.hidden, to[u], plane);
+        if (t0 + u * kPackThreads < n * groups) v[u].pack(w.hidden, to[u], plane, w.hidden_size);
     }
     before += n;
     __syncthreads();
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(kPackThreads)
   for (int64_t r = all + blockIdx.x; r < end; r += gridDim.x)
     for (int c = threadIdx.x; c < groups; c += kPackThreads) {
       Eight<ST> zero = {};
-      zero.pack(w.hidden, r * Dp + c * 8, plane);
+      zero.pack(w.hidden, r * Dp + c * 8, plane, w.hidden_size);
     }
 }
 
@@ -323,7 +337,7 @@ struct PackArgs {
   int64_t size;  // elements from src to the end of the matrix
   int64_t r0, rows, width, stride;
   void* dst;  // planes x [dst_rows, pitch]
-  int64_t pitch, dst_rows;
+  int64_t pitch, dst_rows, dst_size;
 };
 template <class ST>
 __global__ void __launch_bounds__(kPackThreads) head_pack_kernel(PackArgs a) {
@@ -346,7 +360,7 @@ __global__ void __launch_bounds__(kPackThreads) head_pack_kernel(PackArgs a) {
         if (g0 + u * lanes < groups) v[u].load(a.src, a.size, at, (g0 + u * lanes) * 8, a.width);
 #pragma unroll
       for (int u = 0; u < B; ++u)
-        if (g0 + u * lanes < groups) v[u].pack(a.dst, to + (g0 + u * lanes) * 8, a.dst_rows * a.pitch);
+        if (g0 + u * lanes < groups) v[u].pack(a.dst, to + (g0 + u * lanes) * 8, a.dst_rows * a.pitch, a.dst_size);
     }
   }
 }
@@ -709,8 +723,13 @@ struct Stats {
   }
 };
 
+__device__ __forceinline__ float4 part_at(const HeadView& w, int64_t i) {
+  return in_range(i, w.part_size) ? __ldg(w.part + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 // the results of part m, from all its statistics
 __device__ __forceinline__ void finish(const HeadArgs& a, const HeadView& w, int64_t m, int64_t row, const Stats& st) {
+  if (!in_range(row, a.N) || !in_range(m, a.N)) return;
   const float inv_t = a.inv_temperature, log_s = logf(st.s);
   a.lse[row] = fmaf(st.top, inv_t, log_s);
   a.logp[row] = fmaf(w.taken[m] - st.top, inv_t, -log_s);
@@ -738,7 +757,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       float4 p[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        p[u] = k + u * kJoinWarps < pieces ? __ldg(w.part + (k + u * kJoinWarps) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+        p[u] = k + u * kJoinWarps < pieces ? part_at(w, (k + u * kJoinWarps) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < 4; ++u) st.add(p[u].x, p[u].y, p[u].z, c2);
     }
@@ -766,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     float4 p[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      p[u] = k + u * kJoinThreads < pieces ? __ldg(w.part + (k + u * kJoinThreads) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+      p[u] = k + u * kJoinThreads < pieces ? part_at(w, (k + u * kJoinThreads) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < 4; ++u) st.add(p[u].x, p[u].y, p[u].z, c2);
   }
@@ -782,6 +801,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
   for (int k = 1; k < W; ++k) st.add(acc[k].top, acc[k].s, acc[k].t, c2);
   const int64_t row = identity ? m : w.rows[m];
+  if (!in_range(row, a.N)) return;
   const bool on = (unsigned)a.tokens[row] < (unsigned)a.V;
   if (on) {
     finish(a, w, m, row, st);
@@ -816,14 +836,16 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
   pdl_wait();
   for (int64_t t = threadIdx.x; t < NT * Ds; t += kFewThreads) {
     const int64_t r = t / Ds, c = t - r * Ds;
-    few_hidden[t] = r < a.N && c < a.D ? Stor<ST>::ld(a.hidden, r * a.hidden_stride + c) : 0.f;
+    few_hidden[t] = r < a.N && c < a.D && in_range(r * a.hidden_stride + c, (a.N - 1) * a.hidden_stride + a.D)
+                        ? Stor<ST>::ld(a.hidden, r * a.hidden_stride + c)
+                        : 0.f;
   }
   __syncthreads();
   const int mine = lane >> (5 - kLog);           // the logit this lane ends up with:
   const int my_tok = mine / NT, my_row = mine % NT;  // token my_tok of the R, row my_row
   const int64_t taken_tok = my_row < a.N ? a.tokens[my_row] : -1;
   Stats st = {-INFINITY, 0.f, 0.f};
-  const int64_t nv = a.D / VE;
+  const int64_t nv = a.D / VE, w_size = (a.V - 1) * a.weight_stride + a.D;
   for (int64_t v0 = ((int64_t)blockIdx.x * W + warp) * R; v0 < a.V; v0 += (int64_t)gridDim.x * W * R) {
     float z[C];
     // vectors: sums of the even and of the odd columns, two to an instruction
@@ -842,9 +864,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
       float x[R][VE];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if constexpr (VE == 8) Stor<ST>::ld8(base[r], j * VE, true, x[r]);
-        else if constexpr (VE == 4) Stor<ST>::ld4(base[r], j * VE, true, x[r]);
-        else x[r][0] = Stor<ST>::ld(base[r], j);
+        const bool in = span_in_range(min(v0 + r, a.V - 1) * a.weight_stride + j * VE, VE, w_size) && span_in_range(j * VE, VE, Ds);
+        if constexpr (VE == 8) Stor<ST>::ld8(base[r], j * VE, in, x[r]);
+        else if constexpr (VE == 4) Stor<ST>::ld4(base[r], j * VE, in, x[r]);
+        else x[r][0] = in ? Stor<ST>::ld(base[r], j) : 0.f;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -891,7 +914,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     }
     if (v0 + my_tok < a.V) {
       st.add(z[0], 1.f, 0.f, c2);
-      if (v0 + my_tok == taken_tok && (lane & ((32 >> kLog) - 1)) == 0) w.taken[my_row] = z[0];
+      if (v0 + my_tok == taken_tok && (lane & ((32 >> kLog) - 1)) == 0 && in_range(my_row, a.N)) w.taken[my_row] = z[0];
     }
   }
   if ((lane & ((32 >> kLog) - 1)) == 0) acc[warp][mine] = st;
@@ -903,7 +926,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
         const Stats& q = acc[k][r * NT + threadIdx.x];
         all.add(q.top, q.s, q.t, c2);
       }
-    w.part[(int64_t)blockIdx.x * NT + threadIdx.x] = make_float4(all.top, all.s, all.t, 0.f);
+    const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (in_range(at, w.part_size)) w.part[at] = make_float4(all.top, all.s, all.t, 0.f);
   }
 }
 
@@ -919,6 +943,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int64_t t = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kJoinThreads) {
     const int64_t b = t / groups, c = (t - b * groups) * 4;
     const float* src = w.dh + b * Dh + c;
+    const int64_t to = w.rows[b] * a.D + c;
+    if (!span_in_range(b * Dh + c, (splits - 1) * plane + 4, w.dh_size) ||
+        !span_in_range(to, min((int64_t)4, a.D - c), a.N * a.D))
+      continue;
     float4 v = *reinterpret_cast<const float4*>(src);
     for (int k0 = 1; k0 < splits; k0 += 8) {
       float4 q[8];
@@ -929,7 +957,6 @@ __global__ void __launch_bounds__(kJoinThreads)
       for (int u = 0; u < 8; ++u) v.x += q[u].x, v.y += q[u].y, v.z += q[u].z, v.w += q[u].w;
     }
     const float f[4] = {v.x, v.y, v.z, v.w};
-    const int64_t to = w.rows[b] * a.D + c;
     if (vec) {
       Stor<ST>::st4(a.d_hidden, to, f);
     } else {
@@ -1065,7 +1092,7 @@ struct HeadRun {
     if (!p.packed) return cudaSuccess;
     PackArgs k = {};
     k.src = a.weight; k.size = (a.V - 1) * a.weight_stride + a.D; k.r0 = v0; k.rows = len; k.width = a.D; k.stride = a.weight_stride;
-    k.dst = w.weight; k.pitch = p.Dp; k.dst_rows = p.pitch;
+    k.dst = w.weight; k.pitch = p.Dp; k.dst_rows = p.pitch; k.dst_size = w.weight_size;
     return launch_pdl(head_pack_kernel<ST>, std::min<int64_t>(div_up(len * (p.Dp / 8), 4 * kPackThreads), 8 * (int64_t)sm), kPackThreads, 0, s, k);
   }
   bool weight_map(CUtensorMap* m, int64_t len, int box_rows) {

@@ -22,22 +22,28 @@ namespace rlca {
 
 namespace {
 
-// VE consecutive elements of type ST as they lie in memory
+// VE consecutive elements of type ST as they lie in memory, from element i of
+// the n that there are (in the index-check build a miss reads zero, and is not
+// written)
 template <class ST, int VE>
 struct Pack;
 template <>
 struct Pack<float, 4> {
   using Raw = float4;
-  __device__ static Raw load(const float* p, int64_t i) { return __ldg(reinterpret_cast<const float4*>(p + i)); }
+  __device__ static Raw load(const float* p, int64_t i, int64_t n) {
+    return span_in_range(i, 4, n) ? __ldg(reinterpret_cast<const float4*>(p + i)) : zero();
+  }
   __device__ static Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ static void open(const Raw& r, float* v) { v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w; }
-  __device__ static void store(float* p, int64_t i, const float* v) { Stor<float>::st4(p, i, v); }
+  __device__ static void store(float* p, int64_t i, int64_t n, const float* v) {
+    if (span_in_range(i, 4, n)) Stor<float>::st4(p, i, v);
+  }
 };
 template <>
 struct Pack<bf16, 8> {
   using Raw = uint4;
-  __device__ static Raw load(const float* p, int64_t i) {
-    return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i));
+  __device__ static Raw load(const float* p, int64_t i, int64_t n) {
+    return span_in_range(i, 8, n) ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i)) : zero();
   }
   __device__ static Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
   __device__ static void open(const Raw& r, float* v) {
@@ -45,24 +51,48 @@ struct Pack<bf16, 8> {
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
   }
-  __device__ static void store(float* p, int64_t i, const float* v) { Stor<bf16>::st8(p, i, v); }
+  __device__ static void store(float* p, int64_t i, int64_t n, const float* v) {
+    if (span_in_range(i, 8, n)) Stor<bf16>::st8(p, i, v);
+  }
 };
 template <>
 struct Pack<float, 1> {
   using Raw = float;
-  __device__ static Raw load(const float* p, int64_t i) { return __ldg(p + i); }
+  __device__ static Raw load(const float* p, int64_t i, int64_t n) { return in_range(i, n) ? __ldg(p + i) : zero(); }
   __device__ static Raw zero() { return 0.f; }
   __device__ static void open(const Raw& r, float* v) { v[0] = r; }
-  __device__ static void store(float* p, int64_t i, const float* v) { p[i] = v[0]; }
+  __device__ static void store(float* p, int64_t i, int64_t n, const float* v) {
+    if (in_range(i, n)) p[i] = v[0];
+  }
 };
 template <>
 struct Pack<bf16, 1> {
   using Raw = uint16_t;  // widened when used: a conversion at the load would wait for it
-  __device__ static Raw load(const float* p, int64_t i) { return __ldg(reinterpret_cast<const uint16_t*>(p) + i); }
+  __device__ static Raw load(const float* p, int64_t i, int64_t n) {
+    return in_range(i, n) ? __ldg(reinterpret_cast<const uint16_t*>(p) + i) : zero();
+  }
   __device__ static Raw zero() { return 0; }
   __device__ static void open(const Raw& r, float* v) { v[0] = Stor<bf16>::from_bits(r); }
-  __device__ static void store(float* p, int64_t i, const float* v) { Stor<bf16>::st(p, i, v[0]); }
+  __device__ static void store(float* p, int64_t i, int64_t n, const float* v) {
+    if (in_range(i, n)) Stor<bf16>::st(p, i, v[0]);
+  }
 };
+
+// ... single elements, and the elements from the first to the last of a
+// matrix's rows
+template <class ST>
+__device__ __forceinline__ float load1(const float* p, int64_t i, int64_t n) {
+  return in_range(i, n) ? Stor<ST>::ld(p, i) : 0.f;
+}
+template <class ST>
+__device__ __forceinline__ void store1(float* p, int64_t i, int64_t n, float v) {
+  if (in_range(i, n)) Stor<ST>::st(p, i, v);
+}
+// a column's partial sums of dw and db, `apart` elements apart
+__device__ __forceinline__ void store2(float* ws, int64_t i, int64_t apart, int64_t n, float dw, float db) {
+  if (in_range(i, n) && in_range(i + apart, n)) ws[i] = dw, ws[i + apart] = db;
+}
+__device__ __forceinline__ int64_t extent(int64_t rows, int64_t width, int64_t stride) { return (rows - 1) * stride + width; }
 
 // Threads of a CTA: whole warps of rows, or one row over the CTA.
 __host__ __device__ constexpr int cta_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
@@ -108,7 +138,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), norm_resident(cta_threads(TP
   const int lane = threadIdx.x % TPR;
   const int nv = (int)(a.D / VE);
   const float inv_d = 1.f / (float)a.D;
-  const int64_t step = (int64_t)gridDim.x * ROWS;
+  const int64_t step = (int64_t)gridDim.x * ROWS, x_size = extent(a.N, a.D, a.x_stride);
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   pdl_trigger();
   pdl_wait();
@@ -118,9 +148,9 @@ __global__ void __launch_bounds__(cta_threads(TPR), norm_resident(cta_threads(TP
   for (int j = 0; j < VPT; ++j) {
     const int v = lane + j * TPR;
     const bool on = v < nv;
-    w[j] = on ? P::load(a.weight, (int64_t)v * VE) : P::zero();
-    b[j] = on && a.bias ? P::load(a.bias, (int64_t)v * VE) : P::zero();
-    x[j] = on && row < a.N ? P::load(a.x, row * a.x_stride + (int64_t)v * VE) : P::zero();
+    w[j] = on ? P::load(a.weight, (int64_t)v * VE, a.D) : P::zero();
+    b[j] = on && a.bias ? P::load(a.bias, (int64_t)v * VE, a.D) : P::zero();
+    x[j] = on && row < a.N ? P::load(a.x, row * a.x_stride + (int64_t)v * VE, x_size) : P::zero();
   }
   for (; row < a.N; row += step) {
     float f[VPT][VE];
@@ -135,7 +165,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), norm_resident(cta_threads(TP
     if (next < a.N) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (lane + j * TPR < nv) x[j] = P::load(a.x, next * a.x_stride + (int64_t)(lane + j * TPR) * VE);
+        if (lane + j * TPR < nv) x[j] = P::load(a.x, next * a.x_stride + (int64_t)(lane + j * TPR) * VE, x_size);
     }
     const float mean = row_sum<TPR>(s, scratch, 0) * inv_d;
     float q = 0.f;
@@ -157,9 +187,9 @@ __global__ void __launch_bounds__(cta_threads(TPR), norm_resident(cta_threads(TP
       P::open(b[j], fb);
 #pragma unroll
       for (int e = 0; e < VE; ++e) f[j][e] = fmaf(f[j][e] * rstd, fw[e], fb[e]);
-      if (v < nv) P::store(a.y, row * a.D + (int64_t)v * VE, f[j]);
+      if (v < nv) P::store(a.y, row * a.D + (int64_t)v * VE, a.N * a.D, f[j]);
     }
-    if (lane == 0) {
+    if (lane == 0 && in_range(row, a.N)) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
@@ -173,24 +203,24 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(NormArgs a) {
   pdl_trigger();
   pdl_wait();
   __shared__ float scratch[32];
-  const int64_t i = blockIdx.x;
+  const int64_t i = blockIdx.x, x_size = extent(a.N, a.D, a.x_stride);
   const float inv_d = 1.f / (float)a.D;
   const int64_t at = i * a.x_stride;
   float s = 0.f;
-  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) s += Stor<ST>::ld(a.x, at + c);
+  for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) s += load1<ST>(a.x, at + c, x_size);
   const float mean = cta_sum(s, scratch) * inv_d;
   float q = 0.f;
   for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
-    const float d = Stor<ST>::ld(a.x, at + c) - mean;
+    const float d = load1<ST>(a.x, at + c, x_size) - mean;
     q += d * d;
   }
   const float rstd = rsqrtf(cta_sum(q, scratch) * inv_d + a.eps);
   for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
-    const float xh = (Stor<ST>::ld(a.x, at + c) - mean) * rstd;
-    const float b = a.bias ? Stor<ST>::ld(a.bias, c) : 0.f;
-    Stor<ST>::st(a.y, i * a.D + c, xh * Stor<ST>::ld(a.weight, c) + b);
+    const float xh = (load1<ST>(a.x, at + c, x_size) - mean) * rstd;
+    const float b = a.bias ? load1<ST>(a.bias, c, a.D) : 0.f;
+    store1<ST>(a.y, i * a.D + c, a.N * a.D, xh * load1<ST>(a.weight, c, a.D) + b);
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && in_range(i, a.N)) {
     if (a.mean) a.mean[i] = mean;
     if (a.rstd) a.rstd[i] = rstd;
   }
@@ -218,6 +248,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
   const float inv_d = 1.f / (float)a.D;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const int64_t x_size = extent(a.N, a.D, a.x_stride), dy_size = extent(a.N, a.D, a.dy_stride);
   const bool sums = a.dweight != nullptr || a.dbias != nullptr;
   pdl_trigger();
   pdl_wait();
@@ -230,9 +261,9 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
   for (int j = 0; j < VPT; ++j) {
     const int v = lane + j * TPR;
     const bool on = v < nv;
-    w[j] = on ? P::load(a.weight, (int64_t)v * VE) : P::zero();
-    x[j] = on && row < a.N ? P::load(a.x, row * a.x_stride + (int64_t)v * VE) : P::zero();
-    dy[j] = on && row < a.N ? P::load(a.dy, row * a.dy_stride + (int64_t)v * VE) : P::zero();
+    w[j] = on ? P::load(a.weight, (int64_t)v * VE, a.D) : P::zero();
+    x[j] = on && row < a.N ? P::load(a.x, row * a.x_stride + (int64_t)v * VE, x_size) : P::zero();
+    dy[j] = on && row < a.N ? P::load(a.dy, row * a.dy_stride + (int64_t)v * VE, dy_size) : P::zero();
 #pragma unroll
     for (int e = 0; e < VE; ++e) dw[j][e] = db[j][e] = 0.f;
   }
@@ -265,8 +296,8 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
       for (int j = 0; j < VPT; ++j) {
         const int v = lane + j * TPR;
         if (v < nv) {
-          x[j] = P::load(a.x, next * a.x_stride + (int64_t)v * VE);
-          dy[j] = P::load(a.dy, next * a.dy_stride + (int64_t)v * VE);
+          x[j] = P::load(a.x, next * a.x_stride + (int64_t)v * VE, x_size);
+          dy[j] = P::load(a.dy, next * a.dy_stride + (int64_t)v * VE, dy_size);
         }
       }
     }
@@ -290,18 +321,18 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
       const int v = lane + j * TPR;
 #pragma unroll
       for (int e = 0; e < VE; ++e) g[j][e] = r * (g[j][e] - s1 - xh[j][e] * s2);
-      if (v < nv) P::store(a.dx, row * a.D + (int64_t)v * VE, g[j]);
+      if (v < nv) P::store(a.dx, row * a.D + (int64_t)v * VE, a.N * a.D, g[j]);
     }
   }
   if (!sums) return;
-  float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D;
+  const int64_t at = (int64_t)blockIdx.x * 2 * a.D, ws_size = 2 * a.D * (int64_t)gridDim.x;
   if constexpr (ROWS == 1) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = lane + j * TPR;
       if (v < nv) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) out[v * VE + e] = dw[j][e], out[a.D + v * VE + e] = db[j][e];
+        for (int e = 0; e < VE; ++e) store2(a.ws, at + v * VE + e, a.D, ws_size, dw[j][e], db[j][e]);
       }
     }
   } else {
@@ -314,13 +345,14 @@ __global__ void __launch_bounds__(cta_threads(TPR), grad_resident(cta_threads(TP
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
             const int c = (lane + j * TPR) * VE + e;
+            if (!in_range(c, VPT * TPR * VE)) continue;
             acc[0][c] = dw[j][e] + (k > 0 ? acc[0][c] : 0.f);
             acc[1][c] = db[j][e] + (k > 0 ? acc[1][c] : 0.f);
           }
       }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.D; c += cta_threads(TPR)) out[c] = acc[0][c], out[a.D + c] = acc[1][c];
+    for (int c = threadIdx.x; c < a.D; c += cta_threads(TPR)) store2(a.ws, at + c, a.D, ws_size, acc[0][c], acc[1][c]);
   }
 }
 
@@ -352,6 +384,8 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
   pdl_wait();
 
   const auto fill = [&](int stage, int64_t row) {
+    // (an index that is off is recorded, and the row is waited for in vain)
+    if (!in_range(stage, kRingRows) || !in_range(row, a.N)) return;
     unsigned char* to = ring_rows + (size_t)stage * 2 * row_bytes;
     mbar_arrive_expect_tx(&full[stage], 2 * row_bytes);
     bulk_load(to, reinterpret_cast<const unsigned char*>(a.x) + row * a.x_stride * Stor<ST>::kBytes, row_bytes, &full[stage]);
@@ -368,7 +402,7 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = lane + j * TPR;
-    w[j] = v < nv ? P::load(a.weight, (int64_t)v * VE) : P::zero();
+    w[j] = v < nv ? P::load(a.weight, (int64_t)v * VE, a.D) : P::zero();
 #pragma unroll
     for (int e = 0; e < VE; ++e) dw[j][e] = db[j][e] = 0.f;
   }
@@ -388,7 +422,7 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
       const int v = lane + j * TPR;
       const bool on = v < nv;
       typename P::Raw x = P::zero(), dy = P::zero();
-      if (on) {
+      if (on && span_in_range((int64_t)ring.stage * 2 * row_bytes + v * 16, row_bytes + 16, (int64_t)kRingRows * 2 * row_bytes)) {
         x = *reinterpret_cast<const typename P::Raw*>(at + v * 16);
         dy = *reinterpret_cast<const typename P::Raw*>(at + row_bytes + v * 16);
       }
@@ -422,20 +456,20 @@ __global__ void __launch_bounds__(TPR, grad_resident(TPR, VPT * VE)) norm_grad_r
       const int v = lane + j * TPR;
 #pragma unroll
       for (int e = 0; e < VE; ++e) g[j][e] = r * (g[j][e] - s1 - xh[j][e] * s2);
-      if (v < nv) P::store(a.dx, row * a.D + (int64_t)v * VE, g[j]);
+      if (v < nv) P::store(a.dx, row * a.D + (int64_t)v * VE, a.N * a.D, g[j]);
     }
   }
   // (copies still on their way after a wait gave up land before the CTA ends)
   if (!ring.ok && lane == 0)
     for (int i = 0; i < kRingRows; ++i) mbar_wait_bounded(&full[i], ring.last_fill(i));
   if (a.dweight == nullptr && a.dbias == nullptr) return;
-  float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D;
+  const int64_t to = (int64_t)blockIdx.x * 2 * a.D, ws_size = 2 * a.D * (int64_t)gridDim.x;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = lane + j * TPR;
     if (v < nv) {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) out[v * VE + e] = dw[j][e], out[a.D + v * VE + e] = db[j][e];
+      for (int e = 0; e < VE; ++e) store2(a.ws, to + v * VE + e, a.D, ws_size, dw[j][e], db[j][e]);
     }
   }
 }
@@ -446,22 +480,22 @@ __global__ void __launch_bounds__(kLongThreads) norm_grad_long_kernel(NormGradAr
   pdl_trigger();
   pdl_wait();
   __shared__ float scratch[32];
-  const int64_t i = blockIdx.x;
+  const int64_t i = blockIdx.x, x_size = extent(a.N, a.D, a.x_stride), dy_size = extent(a.N, a.D, a.dy_stride);
   const float inv_d = 1.f / (float)a.D;
   const float mean = a.mean[i], rstd = a.rstd[i];
   float s1 = 0.f, s2 = 0.f;
   for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
-    const float g = Stor<ST>::ld(a.dy, i * a.dy_stride + c) * Stor<ST>::ld(a.weight, c);
-    const float xh = (Stor<ST>::ld(a.x, i * a.x_stride + c) - mean) * rstd;
+    const float g = load1<ST>(a.dy, i * a.dy_stride + c, dy_size) * load1<ST>(a.weight, c, a.D);
+    const float xh = (load1<ST>(a.x, i * a.x_stride + c, x_size) - mean) * rstd;
     s1 += g;
     s2 += g * xh;
   }
   s1 = cta_sum(s1, scratch) * inv_d;
   s2 = cta_sum(s2, scratch) * inv_d;
   for (int64_t c = threadIdx.x; c < a.D; c += kLongThreads) {
-    const float g = Stor<ST>::ld(a.dy, i * a.dy_stride + c) * Stor<ST>::ld(a.weight, c);
-    const float xh = (Stor<ST>::ld(a.x, i * a.x_stride + c) - mean) * rstd;
-    Stor<ST>::st(a.dx, i * a.D + c, rstd * (g - s1 - xh * s2));
+    const float g = load1<ST>(a.dy, i * a.dy_stride + c, dy_size) * load1<ST>(a.weight, c, a.D);
+    const float xh = (load1<ST>(a.x, i * a.x_stride + c, x_size) - mean) * rstd;
+    store1<ST>(a.dx, i * a.D + c, a.N * a.D, rstd * (g - s1 - xh * s2));
   }
 }
 
@@ -476,14 +510,14 @@ __global__ void __launch_bounds__(kSliceThreads)
   const int64_t c = (blockIdx.x % col_blocks) * kSliceThreads + threadIdx.x;
   if (c >= a.D) return;
   const int64_t i1 = min(a.N, (slice + 1) * slice_rows);
+  const int64_t x_size = extent(a.N, a.D, a.x_stride), dy_size = extent(a.N, a.D, a.dy_stride);
   float dw = 0.f, db = 0.f;
   for (int64_t i = slice * slice_rows; i < i1; ++i) {
-    const float dy = Stor<ST>::ld(a.dy, i * a.dy_stride + c);
-    dw += dy * ((Stor<ST>::ld(a.x, i * a.x_stride + c) - a.mean[i]) * a.rstd[i]);
+    const float dy = load1<ST>(a.dy, i * a.dy_stride + c, dy_size);
+    dw += dy * ((load1<ST>(a.x, i * a.x_stride + c, x_size) - a.mean[i]) * a.rstd[i]);
     db += dy;
   }
-  a.ws[(2 * slice) * a.D + c] = dw;
-  a.ws[(2 * slice + 1) * a.D + c] = db;
+  store2(a.ws, 2 * slice * a.D + c, a.D, 2 * a.D * (gridDim.x / col_blocks), dw, db);
 }
 
 // (10 MB of partial sums at 32768 x 4096, from L2: about 5 us.)
@@ -507,7 +541,7 @@ __global__ void __launch_bounds__(1024)
     for (int64_t k0 = warp; k0 < parts; k0 += 32 * B) {
       float v[B];
 #pragma unroll
-      for (int u = 0; u < B; ++u) v[u] = k0 + 32 * u < parts ? __ldg(ws + (2 * (k0 + 32 * u) + which) * D + c) : 0.f;
+      for (int u = 0; u < B; ++u) v[u] = k0 + 32 * u < parts ? load1<float>(ws, (2 * (k0 + 32 * u) + which) * D + c, 2 * parts * D) : 0.f;
 #pragma unroll
       for (int u = 0; u < B; ++u) s += v[u];
     }
@@ -518,8 +552,8 @@ __global__ void __launch_bounds__(1024)
   s = 0.f;
 #pragma unroll
   for (int k = 0; k < 32; ++k) s += acc[k][lane];
-  if (bf16_io) Stor<bf16>::st(out, c, s);
-  else Stor<float>::st(out, c, s);
+  if (bf16_io) store1<bf16>(out, c, D, s);
+  else store1<float>(out, c, D, s);
 }
 
 // ---------------------------------------------------------------------------
