@@ -412,11 +412,31 @@ __device__ __forceinline__ void store16(uint16_t* p, const float* v) {
   store32(p, w);
 }
 
-// part[half tile][part] = (max of acc, sum e, sum e (acc - max)) with
-// e = 2^(c2 (acc - max)), c2 = log2(e) / temperature.  Logits enter as their
-// differences to the max, both in the exponent and in the second sum: with
-// max c2 rounded apart, or the products e acc, the errors would have the size
-// of the logits instead of their spread.  The product runs at 80%
+// Partial statistics over some of a part's tokens: top, the largest logit
+// (before the temperature); s, the sum of e = 2^(c2 d); t, the sum of e d, with
+// d = z - top and c2 = log2(e) / temperature.  The difference comes first: a z c2
+// and a top c2 rounded apart, or a sum of e z, would put errors of the size of
+// the logits, not of their spread, into the sums.
+struct Stats {
+  float top, s, t;
+  // moves the sums to another top: down is the old one minus the new one
+  __device__ __forceinline__ void rebase(float down, float c2) {
+    const float f = exp2_approx(down * c2);
+    s *= f;  // (first: where f is 0, down may be of any size)
+    t = fmaf(s, down, t * f);
+  }
+  __device__ __forceinline__ void add(Stats o, float c2) {
+    if (o.s == 0.f) return;  // none
+    const float m = fmaxf(top, o.top);
+    if (s != 0.f) rebase(top - m, c2);
+    o.rebase(o.top - m, c2);
+    top = m;
+    s += o.s;
+    t += o.t;
+  }
+};
+
+// part[half tile][part] = its statistics.  The product runs at 80%
 // of the tensor pipe with partial sums every 512 k (2048 x 4096 x 32768: 312 us,
 // 1761 TFLOP/s); without their TMEM reads 7% less time.  At k = 256 the epilogue's 32768
 // exponentials a tile are the limit: 16 an SM and cycle, as long as the
@@ -430,7 +450,7 @@ struct StatsEpi {
   float c2;
 
   struct State {
-    float top, s, t;
+    Stats sums;
     int m, at, col0;
     bool live;
   };
@@ -439,8 +459,7 @@ struct StatsEpi {
     st.live = row < w.m;
     st.at = st.live ? tok[row] - v0 : -1;
     st.col0 = col0;
-    st.top = -INFINITY;
-    st.s = st.t = 0.f;
+    st.sums = {-INFINITY, 0.f, 0.f};
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     const int n = v_end - v0 - col;  // columns that exist
@@ -452,40 +471,41 @@ struct StatsEpi {
       for (int i = 1; i < 32; ++i) z = i == k ? v[i] : z;
       if (in_range(st.m, Np)) taken[st.m] = z;
     }
-    if (n < 32) {  // the others take the first one's place here and are left out of the sums below
+    if (n < 32) {  // the others take the first one's place for now
 #pragma unroll
       for (int i = 1; i < 32; ++i) v[i] = i < n ? v[i] : v[0];
     }
-    float top = st.top;
+    Stats q = st.sums;
+    float top = q.top;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(v[i]), "f"(v[i + 1]));
-    // (the first chunk: there are no sums to carry over)
-    const float down = st.top == -INFINITY ? 0.f : st.top - top, f = exp2_approx(down * c2);
+    if (n < 32) {  // ... and one that is far below the largest, whatever its size: d finite, e = 0
+      const float low = top - fmaxf(fabsf(top), 2000.f / c2);
+#pragma unroll
+      for (int i = 1; i < 32; ++i) v[i] = i < n ? v[i] : low;
+    }
+    if (q.s != 0.f) q.rebase(q.top - top, c2);
     const uint64_t c22 = pair_of(c2, c2), off2 = pair_of(-top, -top);
-    uint64_t s2 = pair_of(st.s * f, 0.f), t2 = pair_of(fmaf(st.s, down, st.t) * f, 0.f);
+    uint64_t s2 = pair_of(q.s, 0.f), t2 = pair_of(q.t, 0.f);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const uint64_t d = pair_add(pair_of(v[i], v[i + 1]), off2);
+      const uint64_t d2 = pair_add(pair_of(v[i], v[i + 1]), off2);
       float x0, x1;
-      pair_open(pair_mul(d, c22), x0, x1);
-      x0 = exp2_approx(x0), x1 = exp2_approx(x1);
-      if (n < 32) x0 = i < n ? x0 : 0.f, x1 = i + 1 < n ? x1 : 0.f;
-      const uint64_t e = pair_of(x0, x1);
-      s2 = pair_add(s2, e);
-      t2 = pair_fma(e, d, t2);
+      pair_open(pair_mul(d2, c22), x0, x1);
+      const uint64_t e2 = pair_of(exp2_approx(x0), exp2_approx(x1));
+      s2 = pair_add(s2, e2);
+      t2 = pair_fma(e2, d2, t2);
     }
     float s, t, hi;
     pair_open(s2, s, hi);
     s += hi;
     pair_open(t2, t, hi);
     t += hi;
-    st.top = top;
-    st.s = s;
-    st.t = t;
+    st.sums = {top, s, t};
   }
   __device__ __forceinline__ void end(State& st) const {
     const int64_t at = (int64_t)((v0 + st.col0) / (kTcN / 2)) * Np + st.m;
-    if (st.live && in_range(at, halves * Np)) part[at] = make_float4(st.top, st.s, st.t, 0.f);
+    if (st.live && in_range(at, halves * Np)) part[at] = make_float4(st.sums.top, st.sums.s, st.sums.t, 0.f);
   }
 };
 
@@ -708,23 +728,10 @@ struct OutEpi {
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-// partial statistics over some of a part's tokens: the largest value z (before
-// the temperature), the sum of e = 2^(c2 (z - top)), the sum of e (z - top)
-struct Stats {
-  float top, s, t;
-  __device__ __forceinline__ void add(float top2, float s2, float t2, float c2) {
-    if (s2 == 0.f) return;  // none
-    const float m = fmaxf(top, top2);
-    const float down = s == 0.f ? 0.f : top - m, down2 = top2 - m;
-    const float f = exp2_approx(down * c2), f2 = exp2_approx(down2 * c2);
-    t = fmaf(fmaf(s, down, t), f, fmaf(s2, down2, t2) * f2);
-    s = fmaf(s, f, s2 * f2);
-    top = m;
-  }
-};
-
-__device__ __forceinline__ float4 part_at(const HeadView& w, int64_t i) {
-  return in_range(i, w.part_size) ? __ldg(w.part + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+__device__ __forceinline__ Stats part_at(const HeadView& w, int64_t i, bool on) {
+  if (!on || !in_range(i, w.part_size)) return {0.f, 0.f, 0.f};
+  const float4 p = __ldg(w.part + i);
+  return {p.x, p.y, p.z};
 }
 
 // the results of part m, from all its statistics
@@ -754,18 +761,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   Stats st = {-INFINITY, 0.f, 0.f};
   if (on) {
     for (int64_t k = warp; k < pieces; k += 4 * kJoinWarps) {
-      float4 p[4];
+      Stats p[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        p[u] = k + u * kJoinWarps < pieces ? part_at(w, (k + u * kJoinWarps) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < 4; ++u) p[u] = part_at(w, (k + u * kJoinWarps) * pitch + m, k + u * kJoinWarps < pieces);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) st.add(p[u].x, p[u].y, p[u].z, c2);
+      for (int u = 0; u < 4; ++u) st.add(p[u], c2);
     }
   }
   acc[warp][lane] = st;
   __syncthreads();
   if (warp != 0 || !on) return;
-  for (int k = 1; k < kJoinWarps; ++k) st.add(acc[k][lane].top, acc[k][lane].s, acc[k][lane].t, c2);
+  for (int k = 1; k < kJoinWarps; ++k) st.add(acc[k][lane], c2);
   finish(a, w, m, w.rows[m], st);
 }
 
@@ -782,24 +788,23 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (!identity && m >= w.count[0]) return;
   Stats st = {-INFINITY, 0.f, 0.f};
   for (int64_t k = threadIdx.x; k < pieces; k += 4 * kJoinThreads) {
-    float4 p[4];
+    Stats p[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      p[u] = k + u * kJoinThreads < pieces ? part_at(w, (k + u * kJoinThreads) * pitch + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < 4; ++u) p[u] = part_at(w, (k + u * kJoinThreads) * pitch + m, k + u * kJoinThreads < pieces);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) st.add(p[u].x, p[u].y, p[u].z, c2);
+    for (int u = 0; u < 4; ++u) st.add(p[u], c2);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float top = __shfl_xor_sync(0xffffffffu, st.top, o), s = __shfl_xor_sync(0xffffffffu, st.s, o),
-                t = __shfl_xor_sync(0xffffffffu, st.t, o);
-    st.add(top, s, t, c2);
+    const Stats other = {__shfl_xor_sync(0xffffffffu, st.top, o), __shfl_xor_sync(0xffffffffu, st.s, o),
+                         __shfl_xor_sync(0xffffffffu, st.t, o)};
+    st.add(other, c2);
   }
   if (lane == 0) acc[warp] = st;
   __syncthreads();
   if (threadIdx.x != 0) return;
 #pragma unroll
-  for (int k = 1; k < W; ++k) st.add(acc[k].top, acc[k].s, acc[k].t, c2);
+  for (int k = 1; k < W; ++k) st.add(acc[k], c2);
   const int64_t row = identity ? m : w.rows[m];
   if (!in_range(row, a.N)) return;
   const bool on = (unsigned)a.tokens[row] < (unsigned)a.V;
@@ -913,7 +918,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
       }
     }
     if (v0 + my_tok < a.V) {
-      st.add(z[0], 1.f, 0.f, c2);
+      st.add({z[0], 1.f, 0.f}, c2);
       if (v0 + my_tok == taken_tok && (lane & ((32 >> kLog) - 1)) == 0 && in_range(my_row, a.N)) w.taken[my_row] = z[0];
     }
   }
@@ -923,8 +928,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     Stats all = {-INFINITY, 0.f, 0.f};
     for (int k = 0; k < W; ++k)
       for (int r = 0; r < R; ++r) {
-        const Stats& q = acc[k][r * NT + threadIdx.x];
-        all.add(q.top, q.s, q.t, c2);
+        all.add(acc[k][r * NT + threadIdx.x], c2);
       }
     const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
     if (in_range(at, w.part_size)) w.part[at] = make_float4(all.top, all.s, all.t, 0.f);
