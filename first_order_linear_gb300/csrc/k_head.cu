@@ -12,6 +12,7 @@
 // library product's sustained rate); 8192 x 4096 x 32768 alone 1.15 ms, 1918
 // TFLOP/s; the gradient at 4096 x 4096 x 32768 1.82 ms, 1815 TFLOP/s.
 #include <algorithm>
+#include <type_traits>
 
 #include "policy.h"
 #include "reduce.cuh"
@@ -1002,14 +1003,16 @@ cudaError_t launch_product(const Job1& j1, const Job2& j2, int64_t tiles, int sm
   static std::atomic<uint64_t> allowed;
   cudaError_t e = allow_smem(kernel, kTcSmemBlocks, allowed);
   if (e != cudaSuccess) return e;
-  // the warpgroups' register shares are taken from the launch's registers: a
-  // kernel built with fewer would wait for the rest for ever
-  static const bool enough = [&] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
-           f.numRegs * kTcThreads >= 32 * (kTcEpiWarps * kTcEpiRegs + 4 * kTcIssueRegs);
-  }();
-  if (!enough) return cudaErrorInvalidConfiguration;
+  if (kTcShares<Job1, Job2>) {
+    // the warpgroups' register shares are taken from the launch's registers:
+    // a kernel built with fewer would wait for the rest for ever
+    static const bool enough = [&] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
+             f.numRegs * kTcThreads >= 32 * (kTcEpiWarps * kTcEpiRegs + 4 * kTcIssueRegs);
+    }();
+    if (!enough) return cudaErrorInvalidConfiguration;
+  }
   return launch_pdl(kernel, 2 * std::min<int64_t>(tiles, sm_count / 2), kTcThreads, blocks ? kTcSmemBlocks : kTcSmem, st, j1,
                     j2);
 }
@@ -1057,6 +1060,19 @@ bool in_place(const HeadArgs& a) {
 // float32 form 1.6e-7 to 6.1e-7), 3.9e-7 to 4.3e-7 in groups of 1024, which take
 // 3 to 5% less time.
 constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kGradGroupBf16 = 64, kDzGroupBf16 = 16;
+
+// f(the group), or f(0) where no sum is of more than ONE steps: the whole sum
+// in one accumulator, worked on straight from TMEM (tc.cuh).  The bfloat16
+// gradients take up to 128 steps that way, 8192 terms, at most 5e-5 off
+// (128 x 4096 x 32768: 201 us; in groups of 64 219).  float32 products are of six
+// terms, of which the leading one has sums of its own.
+template <class ST, int GROUP, int ONE, class F>
+cudaError_t with_group(int64_t steps, F&& f) {
+  if constexpr (Stor<ST>::kBytes == 2) {
+    if (steps <= ONE) return f(std::integral_constant<int, 0>{});
+  }
+  return f(std::integral_constant<int, GROUP>{});
+}
 
 template <class ST>
 struct HeadRun {
@@ -1124,7 +1140,9 @@ struct HeadRun {
       if (!weight_map(&wk, len, kTcN / 2)) return cudaErrorNotSupported;
       const StatsEpi epi{w.part, w.taken, w.tok, p.Np, div_up(a.V, kTcN) * 2, (int)v0, (int)(v0 + len), c2};
       const TcShape t = logits_shape(v0, len);
-      e = launch_product(TcJob<false, false, kStatsGroup, StatsEpi>{hidden_k, wk, in_place_k, t, epi}, sm, s);
+      e = with_group<ST, kStatsGroup, kStatsGroup>(div_up(a.D, kTcK), [&](auto g) {
+        return launch_product(TcJob<false, false, g.value, StatsEpi>{hidden_k, wk, in_place_k, t, epi}, sm, s);
+      });
     }
     return e == cudaSuccess ? join(div_up(a.V, kTcN) * 2, p.Np, false) : e;
   }
@@ -1196,7 +1214,9 @@ struct HeadRun {
         return cudaErrorNotSupported;
       using Dz = DzEpi<Stor<ST>::kBytes == 2 ? 1 : 3>;
       const Dz dz{w.dz, p.pitch, dz_plane, dz_planes * dz_plane, w.info, w.tok, (int)v0, a.inv_temperature, p.two_dz};
-      e = launch_product(TcJob<false, false, kDzGroup, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
+      e = with_group<ST, kDzGroup, kDzGroup>(div_up(a.D, kTcK), [&](auto g) {
+        return launch_product(TcJob<false, false, g.value, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
+      });
       if (e != cudaSuccess) break;
       // d_hidden's sum over this piece's tokens, and its tokens' d_weight
       TcShape sh = {}, sw = {};
@@ -1212,19 +1232,24 @@ struct HeadRun {
       sw.m = (int)len; sw.n = (int)a.D; sw.k = (int)a.N;
       sw.splits = 1;
       sw.other = hidden_ok ? 2 : 0; sw.full = (int)a.N;
-      const TcJob<false, true, kGradGroup, DhEpi<ST>> jh{
-          dz_k, wmn, wmn, sh,
-          {w.dh, p.Dh, dh_plane, (halves ? 2 : 1) * p.splits * dh_plane, v0 == 0, p.splits == 1 && v0 + len == a.V, a.d_hidden,
-           w.rows, a.N, a.D, align_of(a.d_hidden), halves}};
-      const TcJob<true, true, kGradGroup, OutEpi<ST>> jw{
-          dz_mn, hidden_mn, in_place_mn, sw, {a.d_weight, v0, a.D, a.V, align_of(a.d_weight)}};
-      if (a.d_hidden && a.d_weight &&
-          together(tiles_of(sh), div_up(div_up(len, kTcK), p.splits) * sh.terms.n, tiles_of(sw), div_up(a.N, kTcK) * sw.terms.n,
-                   sm / 2)) {
-        e = launch_product(jh, jw, tiles_of(sh) + tiles_of(sw), sm, s, jh.epi.align < 16 || jw.epi.align < 16);
+      const DhEpi<ST> eh{w.dh, p.Dh, dh_plane, (halves ? 2 : 1) * p.splits * dh_plane, v0 == 0, p.splits == 1 && v0 + len == a.V,
+                         a.d_hidden, w.rows, a.N, a.D, align_of(a.d_hidden), halves};
+      const OutEpi<ST> ew{a.d_weight, v0, a.D, a.V, align_of(a.d_weight)};
+      const int64_t kh = div_up(div_up(len, kTcK), p.splits) * sh.terms.n, kw = div_up(a.N, kTcK) * sw.terms.n;
+      const bool rows_h = eh.align < 16, rows_w = ew.align < 16;
+      const auto hidden_grad = [&](auto g) { return TcJob<false, true, g.value, DhEpi<ST>>{dz_k, wmn, wmn, sh, eh}; };
+      const auto weight_grad = [&](auto g) { return TcJob<true, true, g.value, OutEpi<ST>>{dz_mn, hidden_mn, in_place_mn, sw, ew}; };
+      if (a.d_hidden && a.d_weight && together(tiles_of(sh), kh, tiles_of(sw), kw, sm / 2)) {
+        e = with_group<ST, kGradGroup, kTcLead>(kh, [&](auto g) {
+          return with_group<ST, kGradGroup, kTcLead>(kw, [&](auto g2) {
+            return launch_product(hidden_grad(g), weight_grad(g2), tiles_of(sh) + tiles_of(sw), sm, s, rows_h || rows_w);
+          });
+        });
       } else {
-        if (a.d_hidden) e = launch_product(jh, sm, s, jh.epi.align < 16);
-        if (e == cudaSuccess && a.d_weight) e = launch_product(jw, sm, s, jw.epi.align < 16);
+        if (a.d_hidden)
+          e = with_group<ST, kGradGroup, kTcLead>(kh, [&](auto g) { return launch_product(hidden_grad(g), sm, s, rows_h); });
+        if (e == cudaSuccess && a.d_weight)
+          e = with_group<ST, kGradGroup, kTcLead>(kw, [&](auto g) { return launch_product(weight_grad(g), sm, s, rows_w); });
       }
     }
     if (e == cudaSuccess && a.d_hidden && p.splits > 1) {

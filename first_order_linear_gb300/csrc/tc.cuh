@@ -31,7 +31,9 @@
 // of one sign loses about 2e-7 of itself at each step of 16 k).
 // A new accumulator therefore starts every GROUP stages, and the partial sums
 // are added in float32 registers; the TMEM reads cost 7% of the time at 8
-// stages, 2 to 3% at 16.
+// stages, 2 to 3% at 16.  GROUP = 0 is for sums that are no longer than a group
+// anyway: their epilogue works on the accumulator straight from TMEM, with
+// fewer registers.
 //
 // Every wait is bounded: a wait that gives up records the timeout in the
 // status word and raises a shared flag that ends the CTA's roles (the other
@@ -119,7 +121,29 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// 16 columns of this warp's 32 TMEM lanes (one row a thread), added to v
+// Starts the load of 32 columns of this warp's 32 TMEM lanes (one row a
+// thread); the values are there after tc_load_wait.
+__device__ __forceinline__ void tc_load32(uint32_t addr, float (&v)[32]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+// waits for this thread's loads so far; v passes through so that its uses stay behind the wait
+__device__ __forceinline__ void tc_load_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// ... 16 columns, added to v
 __device__ __forceinline__ void tc_add16(uint32_t addr, float* v) {
   uint32_t r[16];
   __syncwarp();
@@ -262,7 +286,8 @@ constexpr int kTcLead = 128;  // about 35 us
 template <int GROUP>
 __host__ __device__ constexpr int tc_group_end(int at, int stages, int terms) {
   const int all = stages * terms, lead = stages * (terms - 1);
-  static_assert(GROUP > 0 && GROUP <= kTcLead);
+  static_assert(GROUP <= kTcLead);
+  if (GROUP == 0) return all;
   const int end = at < lead ? at + kTcLead : at + GROUP, last = at < lead ? lead : all;
   return end < last ? end : last;
 }
@@ -282,7 +307,12 @@ struct TcJob {
   TcShape s;
   Epi epi;
 };
-struct TcNoJob {};
+struct TcNoJob {
+  static constexpr int GROUP = 0;
+};
+// whether the epilogue's partial sums take registers from the other warps
+template <class Job1, class Job2>
+constexpr bool kTcShares = Job1::GROUP > 0 || Job2::GROUP > 0;
 
 // what a CTA's roles share
 struct TcShared {
@@ -404,22 +434,48 @@ __device__ __forceinline__ bool tc_finish_tile(const Job& job, const TcWalk& wal
   const int col0 = tile.n0 + half * (kTcN / 2);
   typename Job::Epi::State st;
   job.epi.begin(st, walk, tile, tile.m0 + rank * kTcRows + quarter * 32 + lane, col0);
-  float sum[kTcN / 64][32];
-#pragma unroll
-  for (int c = 0; c < kTcN / 64; ++c)
-#pragma unroll
-    for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-  for (int at = 0; at < steps; at = tc_group_end<Job::GROUP>(at, stages, job.s.terms.n)) {
+  if (Job::GROUP == 0 && steps > 0) {
+    // straight from TMEM, 32 columns worked on while the next are loaded
+    float v[32], w[32];
     if (!ready()) return false;
-#pragma unroll
-    for (int c = 0; c < kTcN / 64; ++c) {
-      tc_add16(src0 + acc.buf * kTcN + 32 * c, sum[c]);
-      tc_add16(src0 + acc.buf * kTcN + 32 * c + 16, sum[c] + 16);
+    const uint32_t src = src0 + acc.buf * kTcN;
+    tc_load32(src, v);
+#pragma unroll 1
+    for (int c = 0; c < kTcN / 2; c += 64) {
+      tc_load_wait(v);
+      tc_load32(src + c + 32, w);
+      job.epi.chunk(st, col0 + c, v, block);
+      tc_load_wait(w);
+      if (c + 64 < kTcN / 2) tc_load32(src + c + 64, v);
+      else done();
+      job.epi.chunk(st, col0 + c + 32, w, block);
     }
-    done();
-  }
+  } else if (Job::GROUP == 0) {
+    float v[32];
+#pragma unroll 1
+    for (int c = 0; c < kTcN / 2; c += 32) {
 #pragma unroll
-  for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c], block);
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      job.epi.chunk(st, col0 + c, v, block);
+    }
+  } else {
+    float sum[kTcN / 64][32];
+#pragma unroll
+    for (int c = 0; c < kTcN / 64; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+    for (int at = 0; at < steps; at = tc_group_end<Job::GROUP>(at, stages, job.s.terms.n)) {
+      if (!ready()) return false;
+#pragma unroll
+      for (int c = 0; c < kTcN / 64; ++c) {
+        tc_add16(src0 + acc.buf * kTcN + 32 * c, sum[c]);
+        tc_add16(src0 + acc.buf * kTcN + 32 * c + 16, sum[c] + 16);
+      }
+      done();
+    }
+#pragma unroll
+    for (int c = 0; c < kTcN / 64; ++c) job.epi.chunk(st, col0 + 32 * c, sum[c], block);
+  }
   job.epi.end(st);
   return true;
 }
@@ -430,6 +486,7 @@ template <class Job1, class Job2>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     tc_product_kernel(const __grid_constant__ Job1 j1, const __grid_constant__ Job2 j2) {
   constexpr bool two = !std::is_same_v<Job2, TcNoJob>;
+  constexpr bool shares = kTcShares<Job1, Job2>;
   extern __shared__ unsigned char tc_smem_raw[];
   __shared__ __align__(8) TcShared sh;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)tc_smem_raw + 1023) & ~(uintptr_t)1023);
@@ -484,12 +541,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   };
 
   TcRing copied;  // where the copies' thread has stopped
+  // (without partial sums the launch's registers are enough)
   if (warp >= kTcEpiWarps + 2) {
     // ---- idle ----
-    regs_give<kTcIssueRegs>();
+    if constexpr (shares) regs_give<kTcIssueRegs>();
   } else if (warp == kTcEpiWarps) {
     // ---- copies ----
-    regs_give<kTcIssueRegs>();
+    if constexpr (shares) regs_give<kTcIssueRegs>();
     if (lane == 0) {
       // operands written by earlier kernels' ordinary stores, read by copies
       asm volatile("fence.proxy.async;" ::: "memory");
@@ -497,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == kTcEpiWarps + 1) {
     // ---- matrix instructions ----
-    regs_give<kTcIssueRegs>();
+    if constexpr (shares) regs_give<kTcIssueRegs>();
     if (lane == 0 && rank == 0) {
       TcRing r;
       TcAcc acc;
@@ -506,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ---- epilogue ----
-    regs_take<kTcEpiRegs>();
+    if constexpr (shares) regs_take<kTcEpiRegs>();
     TcAcc acc;
     float* block = reinterpret_cast<float*>(ring + kTcStages * kTcStageBytes) + warp * kTcBlockFloats;
     each_tile([&](const auto& job, const TcWalk& w, int64_t t) { return tc_finish_tile(job, w, t, rank, tmem, sh, block, acc); });
