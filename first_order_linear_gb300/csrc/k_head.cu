@@ -1046,20 +1046,25 @@ bool in_place(const HeadArgs& a) {
   return a.bf16_io && ((uintptr_t)a.weight & 15) == 0 && a.weight_stride % 8 == 0;
 }
 
-// Stages summed by the tensor cores alone (tc.cuh): 512 values of k for
-// results that leave in float32; 4096 for the bfloat16 gradients, whose sums
-// over rows or tokens may have millions of terms (a sum of one sign then stays
-// within 3e-5, a hundredth of its rounding; unbounded, d_weight of 3 million
-// such rows came out 1.8% too small), and 1024 for the logits of their dz, where
-// 6e-6 of a logit, an error in the exponent of p, has to stay below dz's
-// rounding too (one sum over 65536 columns put 0.5% into every p).  The logits of float32 operands, whose
-// error is dz's relative error, take 128 (of the leading product only: 2 to 4%
-// of the time; gradients at 2 x 4000 x 20000 4.1e-7 off instead of 1.9e-6).
-// The error grows with the group and not with the width: 512 x 1024 to 8192 x
-// 4001, bfloat16, log-probabilities 1.8e-7 to 2.1e-7 off in groups of 512 (a plain
-// float32 form 1.6e-7 to 6.1e-7), 3.9e-7 to 4.3e-7 in groups of 1024, which take
-// 3 to 5% less time.
-constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kGradGroupBf16 = 64, kDzGroupBf16 = 16;
+// Stages summed by the tensor cores alone (tc.cuh).
+//
+// Statistics: 512 values of k.  The error grows with the group and not with the
+// width: 512 x 1024 to 8192 x 4001, bfloat16, log-probabilities 1.8e-7 to 2.1e-7
+// off in groups of 512 (a plain float32 form 1.6e-7 to 6.1e-7), 3.9e-7 to 4.3e-7 in
+// groups of 1024, which take 3 to 5% less time.  float32 operands take 128, and
+// so does their dz, whose relative error is the gradients' (of the leading
+// product only: 2 to 4% of the time; gradients at 2 x 4000 x 20000 4.1e-7 off
+// instead of 1.9e-6).  Their gradients' sums take 512.
+//
+// bfloat16 gradients: 4096 terms, over rows or tokens of which there may be
+// millions.  A sum of one sign stays within 3e-5, a hundredth of the result's
+// rounding (unbounded, d_weight of 3 million such rows came out 1.8% too small).
+// The logits of their dz: an error in the exponent of p has to stay below dz's
+// own rounding, 2^-9.  Up to 4096 columns in one accumulator a logit of 16 of one
+// sign is 4e-4 off, beyond, in groups of 1024, 1e-4 (one sum over 65536 columns
+// put 0.5% into every p; groups of 1024 at 4096 columns cost the whole gradient
+// 2%: 2048 x 4096 x 16384 487 against 478 us).
+constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kGradGroupBf16 = 64, kDzGroupBf16 = 16, kDzOneBf16 = 64;
 
 // f(the group), or f(0) where no sum is of more than ONE steps: the whole sum
 // in one accumulator, worked on straight from TMEM (tc.cuh).  The bfloat16
@@ -1078,7 +1083,7 @@ template <class ST>
 struct HeadRun {
   static constexpr bool kF32 = Stor<ST>::kBytes == 4;
   static constexpr int kGradGroup = kF32 ? kLogitsGroup : kGradGroupBf16, kDzGroup = kF32 ? kLogitsGroupF32 : kDzGroupBf16,
-                       kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
+                       kDzOne = kDzOneBf16, kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
   const HeadArgs& a;
   const HeadPlan p;
   const HeadView w;
@@ -1214,7 +1219,7 @@ struct HeadRun {
         return cudaErrorNotSupported;
       using Dz = DzEpi<Stor<ST>::kBytes == 2 ? 1 : 3>;
       const Dz dz{w.dz, p.pitch, dz_plane, dz_planes * dz_plane, w.info, w.tok, (int)v0, a.inv_temperature, p.two_dz};
-      e = with_group<ST, kDzGroup, kDzGroup>(div_up(a.D, kTcK), [&](auto g) {
+      e = with_group<ST, kDzGroup, kDzOne>(div_up(a.D, kTcK), [&](auto g) {
         return launch_product(TcJob<false, false, g.value, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
       });
       if (e != cudaSuccess) break;

@@ -65,3 +65,20 @@ def test_probabilities_of_wide_bfloat16_rows():
     _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
     bias = ((dw[1:].double() - dw0.bfloat16().double()) / dw0).mean().item()
     assert abs(bias) <= 2e-4, bias
+
+
+@pytest.mark.parametrize("D,steps", [(4096, 256), (5000, 64)])
+def test_probabilities_of_bfloat16_rows_around_the_longest_single_sum(D, steps):
+    """The same for widths up to which one accumulator takes all columns, and
+    beyond: logits of 16 lose 2e-7 a step of 16 columns, on average over the
+    `steps` between restarts half of that times their number; as much again is
+    allowed."""
+    N, V = 64, 300
+    h, _, tok, g = one_signed(N, D, V, torch.bfloat16, 3)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    w = ((0.75 + 0.5 * torch.rand((V, D), generator=gen, device="cuda")) * (16.0 / h.float().sum(1).mean())).bfloat16()
+    lse, dw0 = exact(h, w, g)
+    _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
+    bias = ((dw[1:].double() - dw0.bfloat16().double()) / dw0).mean().item()
+    assert abs(bias) <= 2 * 16 * 2e-7 * steps / 2, bias
