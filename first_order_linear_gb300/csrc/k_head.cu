@@ -8,9 +8,9 @@
 // vocabulary at a time.
 //
 // Measured (device time of a whole call): 8192 x 4096 x 131072 bfloat16
-// log-probabilities 5.15 ms, 1709 TFLOP/s under the power cap (0.99 of the
-// library product's sustained rate); 8192 x 4096 x 32768 alone 1.15 ms, 1918
-// TFLOP/s; the gradient at 4096 x 4096 x 32768 1.82 ms, 1815 TFLOP/s.
+// log-probabilities 5.37 to 5.45 ms, 1614 to 1638 TFLOP/s under the power cap (0.94 to
+// 0.95 of the library product's sustained rate); 8192 x 4096 x 32768 alone 1.22 ms,
+// 1805 TFLOP/s; the gradient at 4096 x 4096 x 32768 1.88 ms, 1754 TFLOP/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -437,11 +437,11 @@ struct Stats {
   }
 };
 
-// part[half tile][part] = its statistics.  The product runs at 80%
-// of the tensor pipe with partial sums every 512 k (2048 x 4096 x 32768: 312 us,
-// 1761 TFLOP/s); without their TMEM reads 7% less time.  At k = 256 the epilogue's 32768
-// exponentials a tile are the limit: 16 an SM and cycle, as long as the
-// product's 2048 cycles.
+// part[half tile][part] = its statistics.  The product runs at 79% of the
+// tensor pipe with partial sums every 512 k (2048 x 4096 x 32768: 320 us, 1717
+// TFLOP/s); without their TMEM reads 7% less time.  At k = 256 the epilogue is the
+// limit (2048 x 256 x 131072: 127 us, the tensor pipe at 48%): 4500 cycles a tile,
+// 2048 of them for its 32768 exponentials, 16 an SM and cycle.
 struct StatsEpi {
   float4* part;
   float* taken;
@@ -510,17 +510,19 @@ struct StatsEpi {
   }
 };
 
-// (2048 x 4096 x 16384: 148 us, 88% of the tensor pipe.)
+// (2048 x 4096 x 16384: 152 us, 87% of the tensor pipe.)
 // dz = p (a0 + a1 log p), plus g / temperature for the token taken, with
 // log p = acc / temperature - lse rounded once, for the exponent and the factor
 // alike: terms of the size of the logits or of lse would leave their rounding
-// in either.  As three planes where the operands are float32; for bfloat16 operands as one
-// bfloat16, rounded once because the two products that read it run on
-// bfloat16 -- its error of 2^-9 a term is as large as the rounding of the
-// gradients themselves, and adds to it.  Up to 128 rows a second bfloat16
-// takes what the first left over, in rows 128 further on: half of each 256-row
-// tile would be empty otherwise, and with few rows the errors of single terms
-// (the tokens taken) do not average out.
+// in either.  As three planes where the operands are float32; for bfloat16
+// operands as one bfloat16, rounded once because the two products that read it
+// run on bfloat16 -- its error of 2^-9 a term is as large as the rounding of the
+// gradients themselves, and adds to it (2.4e-3 off in the 2-norm where results
+// rounded once are 1.7e-3 off).  A second bfloat16 for what the first left over
+// would make two of the three products twice as long.  Up to 128 rows half of
+// each 256-row tile is empty otherwise, and it takes that half, in rows 128
+// further on: 1.7e-3 off, for 84 instead of 73 us (128 x 1024 x 32768; 202
+// instead of 192 at 4096 columns).
 template <int PLANES>
 struct DzEpi {
   uint16_t* dz;
@@ -652,8 +654,8 @@ __device__ __forceinline__ void store_rows32(float* out, bool live, int64_t at, 
   }
 }
 
-// (d_hidden and d_weight in one launch at 2048 x 4096 x 16384: 312 us, 87% of
-// the tensor pipe; float32 at 768 x 1024 x 16384, six products: 190 us, 83%.)
+// (d_hidden and d_weight in one launch at 2048 x 4096 x 16384: 329 us, 84% of
+// the tensor pipe; float32 at 768 x 1024 x 16384, six products: 192 us, 83%.)
 // d_hidden.  The sum over the pieces of the vocabulary is kept in float32
 // (`sums`, one plane a split), set by the first piece and added to by the
 // others; without splits the last piece writes the result itself, to the

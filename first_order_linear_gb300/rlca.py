@@ -585,7 +585,9 @@ def rlca_token_logprob_backward(hidden, weight, tokens, lse, d_logp, *, entropy=
                                 want_d_weight=True, workspace=None, stream=None):
     """Gradient of :func:`rlca_token_logprob` for the factors ``d_logp`` [N]
     and, with the saved ``entropy``, ``d_entropy`` [N] (float32):
-    ``(d_hidden, d_weight)``, None for one not wanted (at least one is)."""
+    ``(d_hidden, d_weight)``, None for one not wanted (at least one is).
+    bfloat16, more than 128 rows: the logits' gradient is rounded to bfloat16
+    before its two products."""
     lib = _lib.load()
     fdt, dev, N, D, V, hs, wst = _check_head(hidden, weight, tokens, temperature)
     rows = (N,)
