@@ -420,22 +420,28 @@ __device__ __forceinline__ void store16(uint16_t* p, const float* v) {
 // the logits, not of their spread, into the sums.
 struct Stats {
   float top, s, t;
-  // moves the sums to another top: down is the old one minus the new one
-  __device__ __forceinline__ void rebase(float down, float c2) {
-    const float f = exp2_approx(down * c2);
+  // moves the sums to a top that is no lower
+  __device__ __forceinline__ void rebase(float to, float c2) {
+    const float down = s == 0.f ? 0.f : top - to, f = exp2_approx(down * c2);  // (no sums: off inf - inf)
     s *= f;  // (first: where f is 0, down may be of any size)
     t = fmaf(s, down, t * f);
+    top = to;
   }
   __device__ __forceinline__ void add(Stats o, float c2) {
-    if (o.s == 0.f) return;  // none
     const float m = fmaxf(top, o.top);
-    if (s != 0.f) rebase(top - m, c2);
-    o.rebase(o.top - m, c2);
-    top = m;
+    rebase(m, c2);
+    o.rebase(m, c2);
     s += o.s;
     t += o.t;
   }
+  // ... those of the warp's other lanes
+  __device__ __forceinline__ void add_lanes(float c2) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      add({__shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, s, o), __shfl_xor_sync(0xffffffffu, t, o)}, c2);
+  }
 };
+constexpr float kNoTop = -INFINITY;  // of no logits
 
 // part[half tile][part] = its statistics.  The product runs at 79% of the
 // tensor pipe with partial sums every 512 k (2048 x 4096 x 32768: 320 us, 1717
@@ -460,7 +466,7 @@ struct StatsEpi {
     st.live = row < w.m;
     st.at = st.live ? tok[row] - v0 : -1;
     st.col0 = col0;
-    st.sums = {-INFINITY, 0.f, 0.f};
+    st.sums = {kNoTop, 0.f, 0.f};
   }
   __device__ __forceinline__ void chunk(State& st, int col, float (&v)[32], float* block) const {
     const int n = v_end - v0 - col;  // columns that exist
@@ -485,7 +491,7 @@ struct StatsEpi {
 #pragma unroll
       for (int i = 1; i < 32; ++i) v[i] = i < n ? v[i] : low;
     }
-    if (q.s != 0.f) q.rebase(q.top - top, c2);
+    q.rebase(top, c2);
     const uint64_t c22 = pair_of(c2, c2), off2 = pair_of(-top, -top);
     uint64_t s2 = pair_of(q.s, 0.f), t2 = pair_of(q.t, 0.f);
 #pragma unroll
@@ -732,7 +738,7 @@ struct OutEpi {
 constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ Stats part_at(const HeadView& w, int64_t i, bool on) {
-  if (!on || !in_range(i, w.part_size)) return {0.f, 0.f, 0.f};
+  if (!on || !in_range(i, w.part_size)) return {kNoTop, 0.f, 0.f};
   const float4 p = __ldg(w.part + i);
   return {p.x, p.y, p.z};
 }
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int64_t m = (int64_t)blockIdx.x * 32 + lane;
   if ((int64_t)blockIdx.x * 32 >= w.count[0]) return;
   const bool on = m < w.count[0];
-  Stats st = {-INFINITY, 0.f, 0.f};
+  Stats st = {kNoTop, 0.f, 0.f};
   if (on) {
     for (int64_t k = warp; k < pieces; k += 4 * kJoinWarps) {
       Stats p[4];
@@ -789,7 +795,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t m = blockIdx.x;
   if (!identity && m >= w.count[0]) return;
-  Stats st = {-INFINITY, 0.f, 0.f};
+  Stats st = {kNoTop, 0.f, 0.f};
   for (int64_t k = threadIdx.x; k < pieces; k += 4 * kJoinThreads) {
     Stats p[4];
 #pragma unroll
@@ -797,12 +803,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int u = 0; u < 4; ++u) st.add(p[u], c2);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stats other = {__shfl_xor_sync(0xffffffffu, st.top, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                         __shfl_xor_sync(0xffffffffu, st.t, o)};
-    st.add(other, c2);
-  }
+  st.add_lanes(c2);
   if (lane == 0) acc[warp] = st;
   __syncthreads();
   if (threadIdx.x != 0) return;
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
   const int mine = lane >> (5 - kLog);           // the logit this lane ends up with:
   const int my_tok = mine / NT, my_row = mine % NT;  // token my_tok of the R, row my_row
   const int64_t taken_tok = my_row < a.N ? a.tokens[my_row] : -1;
-  Stats st = {-INFINITY, 0.f, 0.f};
+  Stats st = {kNoTop, 0.f, 0.f};
   const int64_t nv = a.D / VE, w_size = (a.V - 1) * a.weight_stride + a.D;
   for (int64_t v0 = ((int64_t)blockIdx.x * W + warp) * R; v0 < a.V; v0 += (int64_t)gridDim.x * W * R) {
     float z[C];
@@ -927,14 +928,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
   }
   if ((lane & ((32 >> kLog) - 1)) == 0) acc[warp][mine] = st;
   __syncthreads();
-  if (threadIdx.x < NT) {
-    Stats all = {-INFINITY, 0.f, 0.f};
-    for (int k = 0; k < W; ++k)
-      for (int r = 0; r < R; ++r) {
-        all.add(acc[k][r * NT + threadIdx.x], c2);
-      }
-    const int64_t at = (int64_t)blockIdx.x * NT + threadIdx.x;
-    if (in_range(at, w.part_size)) w.part[at] = make_float4(all.top, all.s, all.t, 0.f);
+  // the CTA's statistics of row n, by a warp
+  for (int n = warp; n < NT; n += W) {
+    Stats all = {kNoTop, 0.f, 0.f};
+    for (int i = lane; i < W * R; i += 32) all.add(acc[i / R][i % R * NT + n], c2);
+    all.add_lanes(c2);
+    const int64_t at = (int64_t)blockIdx.x * NT + n;
+    if (lane == 0 && in_range(at, w.part_size)) w.part[at] = make_float4(all.top, all.s, all.t, 0.f);
   }
 }
 
