@@ -6,6 +6,8 @@ import pytest
 import torch
 
 from first_order_linear_gb300 import rlca
+from oracle import policy_ref as ref
+from tests.test_policy_gpu import DT, check_head, head_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +84,19 @@ def test_probabilities_of_bfloat16_rows_around_the_longest_single_sum(D, steps):
     _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
     bias = ((dw[1:].double() - dw0.bfloat16().double()) / dw0).mean().item()
     assert abs(bias) <= 2 * 16 * 2e-7 * steps / 2, bias
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V", [(300, 300), (9000, 300), (8000, 20000), (9000, 20000)])
+def test_short_and_long_sums_in_every_pairing(N, V, dtype):
+    """d_hidden's sums over V tokens (two halves at 8000 rows and more) and
+    d_weight's over N rows, each within one accumulator of 128 steps (8192
+    terms) or beyond, together in a launch and alone: right, and the same bits
+    either way."""
+    *_, dh, dw = check_head(N, 64, V, DT[dtype], seed=N + V, mask=0.1)
+    h, w, tok, g, e = head_inputs(N, 64, V, DT[dtype], N + V, mask=0.1)
+    _, lse0, ent0, _ = ref.token_logprob(h, w, tok)
+    kw = dict(entropy=ent0.float(), d_entropy=e)
+    only_h = rlca.rlca_token_logprob_backward(h, w, tok, lse0.float(), g, want_d_weight=False, **kw)[0]
+    only_w = rlca.rlca_token_logprob_backward(h, w, tok, lse0.float(), g, want_d_hidden=False, **kw)[1]
+    assert torch.equal(only_h, dh) and torch.equal(only_w, dw)
