@@ -9,8 +9,8 @@
 //
 // Measured (device time of a whole call): 8192 x 4096 x 131072 bfloat16
 // log-probabilities 5.37 to 5.45 ms, 1614 to 1638 TFLOP/s under the power cap (0.94 to
-// 0.95 of the library product's sustained rate); 8192 x 4096 x 32768 alone 1.22 ms,
-// 1805 TFLOP/s; the gradient at 4096 x 4096 x 32768 1.88 ms, 1754 TFLOP/s.
+// 0.95 of the library product's sustained rate); 8192 x 4096 x 32768 alone 1.23 ms,
+// 1788 TFLOP/s; the gradient at 4096 x 4096 x 32768 1.94 ms, 1700 TFLOP/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -516,7 +516,7 @@ struct StatsEpi {
   }
 };
 
-// (2048 x 4096 x 16384: 152 us, 87% of the tensor pipe.)
+// (2048 x 4096 x 16384: 162 us, 82% of the tensor pipe.)
 // dz = p (a0 + a1 log p), plus g / temperature for the token taken, with
 // log p = acc / temperature - lse rounded once, for the exponent and the factor
 // alike: terms of the size of the logits or of lse would leave their rounding
@@ -1061,12 +1061,11 @@ bool in_place(const HeadArgs& a) {
 // bfloat16 gradients: 4096 terms, over rows or tokens of which there may be
 // millions.  A sum of one sign stays within 3e-5, a hundredth of the result's
 // rounding (unbounded, d_weight of 3 million such rows came out 1.8% too small).
-// The logits of their dz: an error in the exponent of p has to stay below dz's
-// own rounding, 2^-9.  Up to 4096 columns in one accumulator a logit of 16 of one
-// sign is 4e-4 off, beyond, in groups of 1024, 1e-4 (one sum over 65536 columns
-// put 0.5% into every p; groups of 1024 at 4096 columns cost the whole gradient
-// 2%: 2048 x 4096 x 16384 487 against 478 us).
-constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kGradGroupBf16 = 64, kDzGroupBf16 = 16, kDzOneBf16 = 64;
+// The logits of their dz: an error in the exponent of p has to stay well below
+// dz's own rounding, 2^-9.  In groups of 1024 a logit of 16 of one sign is 1e-4 off
+// (in one sum 4e-4 at 4096 columns, 0.5% at 65536); the whole gradient takes 2%
+// longer for them (2048 x 4096 x 16384: 487 us, in one sum 478).
+constexpr int kLogitsGroup = 8, kLogitsGroupF32 = 2, kGradGroupBf16 = 64, kDzGroupBf16 = 16;
 
 // f(the group), or f(0) where no sum is of more than ONE steps: the whole sum
 // in one accumulator, worked on straight from TMEM (tc.cuh).  The bfloat16
@@ -1085,7 +1084,7 @@ template <class ST>
 struct HeadRun {
   static constexpr bool kF32 = Stor<ST>::kBytes == 4;
   static constexpr int kGradGroup = kF32 ? kLogitsGroup : kGradGroupBf16, kDzGroup = kF32 ? kLogitsGroupF32 : kDzGroupBf16,
-                       kDzOne = kDzOneBf16, kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
+                       kStatsGroup = kF32 ? kLogitsGroupF32 : kLogitsGroup;
   const HeadArgs& a;
   const HeadPlan p;
   const HeadView w;
@@ -1221,7 +1220,7 @@ struct HeadRun {
         return cudaErrorNotSupported;
       using Dz = DzEpi<Stor<ST>::kBytes == 2 ? 1 : 3>;
       const Dz dz{w.dz, p.pitch, dz_plane, dz_planes * dz_plane, w.info, w.tok, (int)v0, a.inv_temperature, p.two_dz};
-      e = with_group<ST, kDzGroup, kDzOne>(div_up(a.D, kTcK), [&](auto g) {
+      e = with_group<ST, kDzGroup, kDzGroup>(div_up(a.D, kTcK), [&](auto g) {
         return launch_product(TcJob<false, false, g.value, Dz>{hidden_k, wk, in_place_k, logits_shape(v0, len), dz}, sm, s);
       });
       if (e != cudaSuccess) break;

@@ -69,12 +69,10 @@ def test_probabilities_of_wide_bfloat16_rows():
     assert abs(bias) <= 2e-4, bias
 
 
-@pytest.mark.parametrize("D,steps", [(4096, 256), (5000, 64)])
-def test_probabilities_of_bfloat16_rows_around_the_longest_single_sum(D, steps):
-    """The same for widths up to which one accumulator takes all columns, and
-    beyond: logits of 16 lose 2e-7 a step of 16 columns, on average over the
-    `steps` between restarts half of that times their number; as much again is
-    allowed."""
+@pytest.mark.parametrize("D", [1024, 4096, 5000])
+def test_probabilities_of_bfloat16_rows_of_any_width(D):
+    """The same where one accumulator takes all columns, where a few do, and
+    at an odd number of them: the error does not depend on the width."""
     N, V = 64, 300
     h, _, tok, g = one_signed(N, D, V, torch.bfloat16, 3)
     gen = torch.Generator(device="cuda")
@@ -83,7 +81,7 @@ def test_probabilities_of_bfloat16_rows_around_the_longest_single_sum(D, steps):
     lse, dw0 = exact(h, w, g)
     _, dw = rlca.rlca_token_logprob_backward(h, w, tok, lse.float(), g, want_d_hidden=False)
     bias = ((dw[1:].double() - dw0.bfloat16().double()) / dw0).mean().item()
-    assert abs(bias) <= 2 * 16 * 2e-7 * steps / 2, bias
+    assert abs(bias) <= 2e-4, bias
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
