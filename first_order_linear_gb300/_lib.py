@@ -43,12 +43,14 @@ RLCA_EST_TOKEN_LOGPROB = 10
 RLCA_EST_TOKEN_LOGPROB_BACKWARD = 11
 RLCA_EST_LAYER_NORM_BACKWARD = 12
 RLCA_EST_CLIP_GRADS = 13
+RLCA_EST_RMS_NORM_BACKWARD = 14
 
 RLCA_F32 = 0
 RLCA_I32 = 1
 RLCA_MAX_ACTIONS = 64
 RLCA_MAX_HEAD_DIM = 65536
 RLCA_MAX_HEAD_ROWS = 16777216
+RLCA_GROUP = 128
 RLCA_STATIC_SCRATCH_BYTES = 1 << 20
 RLCA_STATUS_WAIT_TIMEOUT = 0x1
 RLCA_STATUS_INDEX = 0x2
@@ -85,6 +87,10 @@ SIGNATURES = {
     "rlca_token_logprob_backward": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _f, _u32,
                                          _p, _sz, _p]),
     "rlca_clip_grads": (_i, [_p, _p, _p, _p, _i64, _f, _f, _p, _p, _sz, _p]),
+    "rlca_rms_norm": (_i, [_p] * 10 + [_i64, _i64, _i64, _i64, _f, _u32, _p]),
+    "rlca_rms_norm_backward": (_i, [_p] * 9 + [_i64] * 5 + [_u32, _p, _sz, _p]),
+    "rlca_gated_scan": (_i, [_p] * 8 + [_i64] * 5 + [_u32, _p]),
+    "rlca_gated_scan_backward": (_i, [_p] * 12 + [_i64] * 9 + [_u32, _p]),
 }
 
 

@@ -434,7 +434,7 @@ const char* rlca_status_string(int status) {
   }
 }
 
-int rlca_version(void) { return 300; }
+int rlca_version(void) { return 400; }
 
 int rlca_index_checks(void) { return kIndexCheck ? 1 : 0; }
 
@@ -444,7 +444,8 @@ int rlca_device_status(unsigned int* status, int clear) {
   const bool c = clear != 0;
   cudaError_t (*const units[])(unsigned int*, bool) = {status_values, status_values_bf16_a, status_values_bf16_b,
                                                        status_offpolicy, status_offpolicy_bf16, status_forward,
-                                                       status_forward_bf16, status_norm, status_head, status_clip};
+                                                       status_forward_bf16, status_norm, status_head, status_clip,
+                                                       status_rms, status_gated};
   for (auto f : units)
     if (f(status, c) != cudaSuccess) return RLCA_ERR_CUDA;
   return RLCA_OK;

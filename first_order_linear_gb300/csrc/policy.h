@@ -95,10 +95,15 @@ struct ClipArgs {
 size_t clip_workspace(int64_t count, int sm_count);
 cudaError_t run_clip_grads(const ClipArgs& a, int sm_count, cudaStream_t s);
 
+// workspace of the RMS norm's gradient (k_rms.cu; its calls are in trunk.h)
+size_t rms_norm_backward_workspace(int64_t N, int64_t D, int sm_count);
+
 // the device status words of these translation units, ORed into *word
 cudaError_t status_norm(unsigned int* word, bool clear);
 cudaError_t status_head(unsigned int* word, bool clear);
 cudaError_t status_clip(unsigned int* word, bool clear);
+cudaError_t status_rms(unsigned int* word, bool clear);
+cudaError_t status_gated(unsigned int* word, bool clear);
 
 int checked_build_status(cudaStream_t s);
 

@@ -46,7 +46,7 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 }  // namespace
 
 bool policy_estimator(int estimator) {
-  return estimator >= RLCA_EST_TOKEN_LOGPROB && estimator <= RLCA_EST_CLIP_GRADS;
+  return estimator >= RLCA_EST_TOKEN_LOGPROB && estimator <= RLCA_EST_RMS_NORM_BACKWARD;
 }
 
 int policy_workspace_size(int estimator, int64_t E, int64_t T, int32_t num_actions, uint32_t flags, size_t* bytes) {
@@ -65,6 +65,8 @@ int policy_workspace_size(int estimator, int64_t E, int64_t T, int32_t num_actio
     *bytes = head_workspace(E, T, num_actions, (flags & RLCA_BF16) != 0, estimator == RLCA_EST_TOKEN_LOGPROB_BACKWARD, sm);
   else if (estimator == RLCA_EST_LAYER_NORM_BACKWARD)
     *bytes = layer_norm_backward_workspace(E, T, sm);
+  else if (estimator == RLCA_EST_RMS_NORM_BACKWARD)
+    *bytes = rms_norm_backward_workspace(E, T, sm);
   else
     *bytes = clip_workspace(E, sm);
   return RLCA_OK;

@@ -31,6 +31,7 @@ __all__ = [
     "rlca_elig_trace", "rlca_episodic_prefix_sum", "rlca_affine_scan", "rlca_workspace_size",
     "rlca_layer_norm", "rlca_layer_norm_backward", "rlca_token_logprob", "rlca_token_logprob_backward",
     "rlca_clip_grads",
+    "rlca_rms_norm", "rlca_rms_norm_backward", "rlca_gated_scan", "rlca_gated_scan_backward",
 ]
 
 
@@ -672,3 +673,197 @@ def rlca_clip_grads(grads, max_norm, *, eps=1e-6, out=None, norm_only=False, nor
             norm.data_ptr(), _ptr(ws), wsb, _raw_stream(dev, stream)))
         _hold(dev, stream, ws, norm, *(out or ()))
     return out, norm
+
+
+# ---- a recurrent policy's trunk ---------------------------------------------
+# Rows in 8 bits are pairs (q, scale): q [N, D] float8_e4m3fn, scale
+# [N, ceil(D / 128)] float32, one for each group of 128 columns; a value is
+# q * scale.
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _scale_width(D):
+    return -(-D // _lib.RLCA_GROUP)
+
+
+def _check_pair(pair, name, N, D, device):
+    if not (isinstance(pair, (tuple, list)) and len(pair) == 2):
+        raise TypeError(f"{name} must be a pair (values, scales)")
+    _check(pair[0], f"{name}[0]", (_E4M3,), (N, D), device)
+    _check(pair[1], f"{name}[1]", _F, (N, _scale_width(D)), device)
+    return pair
+
+
+def _out_pair(pair, name, N, D, device, want):
+    """An output in 8 bits: the pair given (checked), a new one, or (None, None)."""
+    if pair is not None:
+        return _check_pair(pair, name, N, D, device)
+    if not want:
+        return None, None
+    return (torch.empty((N, D), dtype=_E4M3, device=device),
+            torch.empty((N, _scale_width(D)), dtype=torch.float32, device=device))
+
+
+def rlca_rms_norm(x, weight, residual=None, *, eps=1e-6, y=None, total=None, rstd=None, y8=None, total8=None,
+                  want_y=True, want_y8=False, want_total8=False, stream=None):
+    """Root-mean-square norm of the rows of total = ``x`` [N, D] + ``residual``:
+    ``(y, total, rstd, y8, total8)``, None for those not wanted.  ``y8`` is y
+    in 8 bits, ``total8`` total in 8 bits for :func:`rlca_rms_norm_backward`
+    (pairs of e4m3 values and the scales of their groups of 128 columns).
+    Without a residual, total is ``x`` itself; with one, ``total`` may be the
+    residual's own buffer."""
+    lib = _lib.load()
+    fdt = _fdt(x, "x")
+    dev = x.device
+    x_stride = _check_matrix(x, "x", fdt, None, dev)
+    N, D = x.shape
+    _check(weight, "weight", (fdt,), (D,), dev)
+    r_stride = 0
+    if residual is not None:
+        r_stride = _check_matrix(residual, "residual", fdt, (N, D), dev)
+        total = _out(total, "total", fdt, (N, D), dev)
+    elif total is not None:
+        raise ValueError("total without a residual: it is x itself")
+    y = _out(y, "y", fdt, (N, D), dev, want_y)
+    rstd = _out(rstd, "rstd", torch.float32, (N,), dev)
+    q, q_scale = _out_pair(y8, "y8", N, D, dev, want_y8)
+    t8, t8_scale = _out_pair(total8, "total8", N, D, dev, want_total8)
+    _require_cuda(dev)
+    with _on(dev):
+        check("rlca_rms_norm", lib.rlca_rms_norm(
+            x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(total), _ptr(y), _ptr(q), _ptr(q_scale), _ptr(t8),
+            _ptr(t8_scale), rstd.data_ptr(), N, D, x_stride, r_stride, eps, _fflag(fdt), _raw_stream(dev, stream)))
+        _hold(dev, stream, y, total, rstd, q, q_scale, t8, t8_scale)
+    return (y, x if residual is None else total, rstd, None if q is None else (q, q_scale),
+            None if t8 is None else (t8, t8_scale))
+
+
+def rlca_rms_norm_backward(dy, total, weight, rstd, *, d_total=None, dx=None, dweight=None, want_dx=True,
+                           want_dweight=True, workspace=None, stream=None):
+    """Gradient of :func:`rlca_rms_norm`: ``(dx, dweight)`` (None for one not
+    wanted; at least one is).  ``total`` [N, D] is the forward call's, or its
+    ``total8`` pair; ``d_total`` [N, D], the gradient that reaches total from
+    elsewhere, is added to dx, which is the gradient of x and of the residual."""
+    lib = _lib.load()
+    fdt = _fdt(dy, "dy")
+    dev = dy.device
+    dy_stride = _check_matrix(dy, "dy", fdt, None, dev)
+    N, D = dy.shape
+    t_stride = dt_stride = 0
+    q = q_scale = None
+    if isinstance(total, (tuple, list)):
+        q, q_scale = _check_pair(total, "total", N, D, dev)
+        total = None
+    else:
+        t_stride = _check_matrix(total, "total", fdt, (N, D), dev)
+    _check(weight, "weight", (fdt,), (D,), dev)
+    _check(rstd, "rstd", _F, (N,), dev)
+    if d_total is not None:
+        dt_stride = _check_matrix(d_total, "d_total", fdt, (N, D), dev)
+    dx = _out(dx, "dx", fdt, (N, D), dev, want_dx)
+    dweight = _out(dweight, "dweight", fdt, (D,), dev, want_dweight)
+    if dx is None and dweight is None:
+        raise ValueError("no output wanted")
+    _require_cuda(dev)
+    flags = _fflag(fdt)
+    with _on(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_RMS_NORM_BACKWARD, N, D, 0, flags, dev, workspace)
+        check("rlca_rms_norm_backward", lib.rlca_rms_norm_backward(
+            dy.data_ptr(), _ptr(d_total), _ptr(total), _ptr(q), _ptr(q_scale), weight.data_ptr(), rstd.data_ptr(),
+            _ptr(dx), _ptr(dweight), N, D, dy_stride, dt_stride, t_stride, flags, _ptr(ws), wsb,
+            _raw_stream(dev, stream)))
+        _hold(dev, stream, ws, dx, dweight)
+    return dx, dweight
+
+
+def _check_steps(t, name, dtype, shape, device):
+    """Checks a tensor [E, T, D] ([T, E, D]) of rows of D at one row stride,
+    which it returns in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    got = t.shape
+    if len(got) != 3 or (shape is not None and got != shape):
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple(shape) if shape else '3 dimensions'}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    outer, inner, width = got
+    s0, s1, s2 = t.stride()
+    if width > 1 and s2 != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    if t.numel() == 0:
+        return width
+    stride = s1 if inner > 1 else s0 if outer > 1 else width
+    if inner > 1 and outer > 1 and s0 != inner * s1:
+        raise ValueError(f"{name}: its rows do not lie at one stride (strides {t.stride()} for shape {tuple(got)})")
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap (row stride {stride} below width {width})")
+    return stride
+
+
+def _scan_inputs(x, gate, terminated, truncated, state, lengths, time_major):
+    fdt = _fdt(x, "x")
+    dev = x.device
+    xs = _check_steps(x, "x", fdt, None, dev)
+    gs = _check_steps(gate, "gate", fdt, x.shape, dev)
+    E, T = _dims(x, time_major)
+    D = x.shape[2]
+    steps = x.shape[:2]
+    _check(terminated, "terminated", _U8, steps, dev, required=False)
+    _check(truncated, "truncated", _U8, steps, dev, required=False)
+    _check(state, "state", _F, (E, D), dev, required=False)
+    _check(lengths, "lengths", _I32, (E,), dev, required=False)
+    return fdt, dev, E, T, D, xs, gs
+
+
+def rlca_gated_scan(x, gate, terminated=None, truncated=None, state=None, lengths=None, *, time_major=False, h=None,
+                    last=None, want_last=True, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t with a_t =
+    sigmoid(gate_t) over the steps of ``x``, ``gate`` [E, T, D], from ``state``
+    [E, D] float32 (None: 0), starting anew behind flagged steps: ``(h, last)``,
+    ``last`` [E, D] float32 the state to go on with (None when not wanted; the
+    state's own buffer may take it).  Row e takes part up to ``lengths[e]``
+    [E] int32; behind, h is 0 whatever the inputs hold.  Rows of D may lie at
+    any one stride, as the halves of a projection's rows do.  T = 1 is one step
+    of acting."""
+    lib = _lib.load()
+    fdt, dev, E, T, D, xs, gs = _scan_inputs(x, gate, terminated, truncated, state, lengths, time_major)
+    h = _out(h, "h", fdt, x.shape, dev)
+    last = _out(last, "last", torch.float32, (E, D), dev, want_last)
+    _require_cuda(dev)
+    flags = _fflag(fdt) | (_lib.RLCA_TIME_MAJOR if time_major else 0)
+    with _on(dev):
+        check("rlca_gated_scan", lib.rlca_gated_scan(
+            x.data_ptr(), gate.data_ptr(), _ptr(terminated), _ptr(truncated), _ptr(state), _ptr(lengths), h.data_ptr(),
+            _ptr(last), E, T, D, xs, gs, flags, _raw_stream(dev, stream)))
+        _hold(dev, stream, h, last)
+    return h, last
+
+
+def rlca_gated_scan_backward(dh, x, gate, h, terminated=None, truncated=None, state=None, lengths=None, *, d_last=None,
+                             time_major=False, dx=None, dgate=None, d_state=None, want_d_state=True, stream=None):
+    """Gradient of :func:`rlca_gated_scan` from its inputs and its ``h``, for
+    ``dh`` and ``d_last`` (None: 0): ``(dx, dgate, d_state)``, d_state [E, D]
+    float32, None when not wanted.  Buffers given for dx and dgate may have
+    rows at a stride, side by side in one matrix's rows."""
+    lib = _lib.load()
+    fdt, dev, E, T, D, xs, gs = _scan_inputs(x, gate, terminated, truncated, state, lengths, time_major)
+    dhs = _check_steps(dh, "dh", fdt, x.shape, dev)
+    hs = _check_steps(h, "h", fdt, x.shape, dev)
+    _check(d_last, "d_last", _F, (E, D), dev, required=False)
+    dx = torch.empty(x.shape, dtype=fdt, device=dev) if dx is None else dx
+    dgate = torch.empty(x.shape, dtype=fdt, device=dev) if dgate is None else dgate
+    dxs = _check_steps(dx, "dx", fdt, x.shape, dev)
+    dgs = _check_steps(dgate, "dgate", fdt, x.shape, dev)
+    d_state = _out(d_state, "d_state", torch.float32, (E, D), dev, want_d_state)
+    _require_cuda(dev)
+    flags = _fflag(fdt) | (_lib.RLCA_TIME_MAJOR if time_major else 0)
+    with _on(dev):
+        check("rlca_gated_scan_backward", lib.rlca_gated_scan_backward(
+            dh.data_ptr(), x.data_ptr(), gate.data_ptr(), h.data_ptr(), _ptr(terminated), _ptr(truncated), _ptr(state),
+            _ptr(lengths), _ptr(d_last), dx.data_ptr(), dgate.data_ptr(), _ptr(d_state), E, T, D, dhs, xs, gs, hs, dxs,
+            dgs, flags, _raw_stream(dev, stream)))
+        _hold(dev, stream, dx, dgate, d_state)
+    return dx, dgate, d_state

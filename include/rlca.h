@@ -133,6 +133,7 @@ typedef struct CUstream_st *rlca_stream_t;
 #define RLCA_EST_TOKEN_LOGPROB_BACKWARD 11
 #define RLCA_EST_LAYER_NORM_BACKWARD    12
 #define RLCA_EST_CLIP_GRADS             13
+#define RLCA_EST_RMS_NORM_BACKWARD      14
 
 /* ---- prefix-sum element types ------------------------------------------- */
 #define RLCA_F32 0
@@ -158,7 +159,7 @@ int rlca_version(void);
  * No counterpart in the paper: it reports conditions that a kernel records
  * instead of trapping.  The only one in the product build is
  * RLCA_STATUS_WAIT_TIMEOUT: a kernel that waits for its own copies (the
- * time-major bulk driver, the layer norm's gradient) or matrix instructions
+ * time-major bulk driver, the norms' gradients, the gated scans) or matrix instructions
  * (the policy head) gives up after 0.2 s instead of hanging and leaves that
  * call's outputs incomplete.  The copies are synchronous: the
  * call waits for the device's earlier work.  Errors: RLCA_ERR_INVALID_ARG
@@ -549,6 +550,143 @@ int rlca_clip_grads(const void *const *grads, void *const *outs,
                     int64_t count, float max_norm, float eps, float *norm,
                     void *workspace, size_t workspace_bytes,
                     rlca_stream_t stream);
+
+/* ---- a recurrent policy's trunk -------------------------------------------
+ *
+ * The layers in front of a token policy's head, where they are recurrent: the
+ * norm of the residual stream, with the stream's addition and 8-bit results,
+ * and a gated linear recurrence over each rollout's steps, which starts anew
+ * behind an episode's end as the forward scans above do.  No counterpart in
+ * the paper.  Conventions as for the policy update; matrices below have a row
+ * stride where one is named.
+ *
+ * Rows in 8 bits: a row of D values is D e4m3 values q (1 byte each: sign, 4
+ * exponent and 3 mantissa bits, largest 448) and one float32 scale for each
+ * group of RLCA_GROUP consecutive columns (the last group may be narrower):
+ *   scale = max(max |v| / 448, 2^-126),   q = v / scale to the nearest e4m3
+ * A value is read back as q * scale.  NaN stays NaN (and does not count in the
+ * group's maximum); a group that holds an infinity reads back as NaN.  Both
+ * arrays are dense: q [N,D], scale [N, ceil(D / RLCA_GROUP)].
+ */
+#define RLCA_GROUP 128
+
+/*
+ * Root-mean-square norm of N rows of width D, with the residual's addition:
+ *   total = x + residual, rounded to its type   (x itself without a residual)
+ *   rstd  = 1 / sqrt(mean_D(total^2) + eps)
+ *   y     = total * rstd * weight
+ *   x                      [N,D] x, row stride x_stride, required
+ *   residual               [N,D] x, row stride residual_stride, NULL = none
+ *   weight                 [D] x, required
+ *   total                  [N,D] x output, required iff residual is given;
+ *                          may be the residual's own buffer (then dense)
+ *   y                      [N,D] x output, NULL = not written
+ *   y8, y8_scale           y as rows in 8 bits, from its float32 values; both
+ *                          or neither NULL
+ *   total8, total8_scale   total (as stored) as rows in 8 bits, to be kept for
+ *                          rlca_rms_norm_backward; both or neither NULL
+ *   rstd                   [N] f32 output, NULL = not written
+ * At least one output must be given.  N == 0 or D == 0 enqueues nothing.
+ * Errors: RLCA_ERR_INVALID_ARG also for a row stride below D and eps not in
+ * [0, inf).
+ */
+int rlca_rms_norm(const float *x, const float *residual, const float *weight,
+                  float *total, float *y, uint8_t *y8, float *y8_scale,
+                  uint8_t *total8, float *total8_scale, float *rstd,
+                  int64_t N, int64_t D, int64_t x_stride,
+                  int64_t residual_stride, float eps, uint32_t flags,
+                  rlca_stream_t stream);
+
+/*
+ * Gradient of rlca_rms_norm from its saved statistic and its total, as stored
+ * or kept in 8 bits.  With g = dy * weight and s = total * rstd:
+ *   dx = d_total + rstd * (g - s * mean_D(g * s))   (of x and the residual)
+ *   dweight = sum_N dy * s
+ *   dy                     [N,D] x, row stride dy_stride, required
+ *   d_total                [N,D] x, row stride d_total_stride: the gradient
+ *                          that reaches total from elsewhere, NULL = 0
+ *   total                  [N,D] x, row stride total_stride, or NULL and
+ *   total8, total8_scale   total as rows in 8 bits
+ *   weight                 [D] x, required
+ *   rstd                   [N] f32, required
+ *   dx                     [N,D] x output, NULL = not written
+ *   dweight                [D] x output, NULL = not written
+ * Workspace: RLCA_EST_RMS_NORM_BACKWARD.  N == 0 writes zeros to dweight;
+ * D == 0 enqueues nothing.
+ */
+int rlca_rms_norm_backward(const float *dy, const float *d_total,
+                           const float *total, const uint8_t *total8,
+                           const float *total8_scale, const float *weight,
+                           const float *rstd, float *dx, float *dweight,
+                           int64_t N, int64_t D, int64_t dy_stride,
+                           int64_t d_total_stride, int64_t total_stride,
+                           uint32_t flags, void *workspace,
+                           size_t workspace_bytes, rlca_stream_t stream);
+
+/*
+ * Gated linear recurrence over E rows of T steps of D channels, a forward
+ * scan (rl-triton §1 forward-time mirror, with beta_t = 0 behind an episode's
+ * end as in §5):
+ *   a_t = 1 / (1 + exp(-gate_t))
+ *   h_t = a_t h_{t-1} + (1 - a_t) x_t,   h_{-1} = state
+ * where h_{t-1} counts as 0 if step t-1 of the call is flagged (terminated or
+ * truncated).  A row may be shorter than T: steps at and behind lengths[e]
+ * take no part, whatever their inputs and flags hold, and their h is 0.
+ *   last = h at the row's last step (state for a row of length 0), or 0 if
+ *          that step is flagged
+ * so that a rollout cut into several calls gives the results of one, each
+ * call's last being the next one's state.  T = 1 is the form for acting, one
+ * token of E sequences at a time; last may then (and always) be the state's
+ * own buffer.
+ *   x, gate                [E,T,D] x ([T,E,D] with RLCA_TIME_MAJOR), rows of D
+ *                          at row strides x_stride and gate_stride, required
+ *   terminated, truncated  [E,T] ([T,E]) u8, NULL = none
+ *   state                  [E,D] f32, NULL = 0
+ *   lengths                [E] i32, NULL = T; values outside [0, T] count as
+ *                          the nearer end
+ *   h                      [E,T,D] x output, dense, required
+ *   last                   [E,D] f32 output, NULL = not written
+ * Flags: RLCA_TIME_MAJOR, RLCA_BF16 (x, gate and h).  E * T is at most
+ * 2^31 - 1.  E == 0 or D == 0 enqueues nothing; T == 0 writes last only.
+ */
+int rlca_gated_scan(const float *x, const float *gate,
+                    const uint8_t *terminated, const uint8_t *truncated,
+                    const float *state, const int32_t *lengths, float *h,
+                    float *last, int64_t E, int64_t T, int64_t D,
+                    int64_t x_stride, int64_t gate_stride, uint32_t flags,
+                    rlca_stream_t stream);
+
+/*
+ * Gradient of rlca_gated_scan from its inputs and its h, for the gradients dh
+ * and d_last of its outputs, a backward scan.  With k_t = 0 where h_{t-1}
+ * counts as 0 and 1 elsewhere:
+ *   G_t     = dh_t + k_{t+1} a_{t+1} G_{t+1},  behind a row's last step
+ *             d_last (0 if that step is flagged) in place of k a G
+ *   dx_t    = (1 - a_t) G_t
+ *   dgate_t = a_t (1 - a_t) G_t (k_t h_{t-1} - x_t)
+ *   d_state = k_0 a_0 G_0                     (d_last for a row of length 0)
+ * Steps that take no part have gradient 0.
+ *   dh, x, gate, h         [E,T,D] x ([T,E,D]) at their row strides, required
+ *   terminated, truncated, state, lengths  as in the forward call
+ *   d_last                 [E,D] f32, NULL = 0
+ *   dx, dgate              [E,T,D] x outputs at their row strides, required;
+ *                          with one stride they may be parts of one wider
+ *                          matrix's rows
+ *   d_state                [E,D] f32 output, NULL = not written; may be
+ *                          d_last's own buffer
+ * Otherwise as rlca_gated_scan; T == 0 writes d_state only.
+ */
+int rlca_gated_scan_backward(const float *dh, const float *x,
+                             const float *gate, const float *h,
+                             const uint8_t *terminated,
+                             const uint8_t *truncated, const float *state,
+                             const int32_t *lengths, const float *d_last,
+                             float *dx, float *dgate, float *d_state,
+                             int64_t E, int64_t T, int64_t D,
+                             int64_t dh_stride, int64_t x_stride,
+                             int64_t gate_stride, int64_t h_stride,
+                             int64_t dx_stride, int64_t dgate_stride,
+                             uint32_t flags, rlca_stream_t stream);
 
 #ifdef __cplusplus
 }
