@@ -410,6 +410,19 @@ bool encode_matrix_map(CUtensorMap* m, const void* base, int64_t width, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_steps_map(CUtensorMap* m, const void* base, int elem_bytes, int64_t D, int64_t T, int64_t E, int64_t step_stride,
+                      int64_t row_stride, int box_cols, int box_steps) {
+  const EncodeTiledFn fn = encoder();
+  constexpr int64_t kMost = int64_t(1) << 40;  // bytes of a stride: below 2^40
+  if (fn == nullptr || step_stride * elem_bytes >= kMost || row_stride * elem_bytes >= kMost) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)E};
+  const cuuint64_t strides[2] = {(cuuint64_t)(step_stride * elem_bytes), (cuuint64_t)(row_stride * elem_bytes)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_steps, 1}, estr[3] = {1, 1, 1};
+  return fn(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tm_maps(const StagedList& in, int elem_bytes, int64_t E, int64_t T, int ew, int rows, TmaSet* out) {
   for (int i = 0; i < in.nf; ++i)
     if (!encode_2d(&out->f[i], in.fin[i], elem_bytes, E, T, ew, rows)) return false;

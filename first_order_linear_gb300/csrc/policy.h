@@ -114,4 +114,11 @@ int checked_build_status(cudaStream_t s);
 bool encode_matrix_map(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int64_t planes,
                        int64_t row_stride, int64_t plane_stride, int box_rows);
 
+// Map of a tensor [E, T, D] of 2- or 4-byte elements (strides of a step and
+// of a row in elements, base and strides multiples of 16 bytes) for copies of
+// box_cols x box_steps boxes of one row; what lies outside reads as zero.
+// False when the encoder is unavailable or refuses.
+bool encode_steps_map(CUtensorMap* m, const void* base, int elem_bytes, int64_t D, int64_t T, int64_t E, int64_t step_stride,
+                      int64_t row_stride, int box_cols, int box_steps);
+
 }  // namespace rlca
