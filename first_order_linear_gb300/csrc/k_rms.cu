@@ -6,7 +6,6 @@
 //   dw = sum over rows of dy s
 #include <algorithm>
 #include <atomic>
-#include <cstring>
 #include <initializer_list>
 #include <type_traits>
 
@@ -61,12 +60,15 @@ struct Part {
   static constexpr int VE = kAligned ? 16 / Stor<ST>::kBytes : 4;
   static constexpr int kLanes = kGroup / VE;  // of a group
   using E = std::conditional_t<Stor<ST>::kBytes == 4, float, uint16_t>;
-  struct Raw {
+  // as they lie in memory, taken apart when used: at the load that would wait for it
+  struct Apart {
     E e[VE];
   };
-  struct Raw8 {
+  struct Apart8 {
     uint8_t e[VE];
   };
+  using Raw = std::conditional_t<kAligned, uint4, Apart>;
+  using Raw8 = std::conditional_t<kAligned, std::conditional_t<VE == 8, uint2, uint32_t>, Apart8>;
   int lane;  // of the row
   int64_t D;
 
@@ -85,9 +87,8 @@ struct Part {
     Raw r;
     const E* base = reinterpret_cast<const E*>(p) + row;
     if constexpr (kAligned) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (on<TPR>(j, 0) && span_in_range(row + col<TPR>(j, 0), VE, n)) w = *reinterpret_cast<const uint4*>(base + col<TPR>(j, 0));
-      memcpy(&r, &w, 16);
+      r = make_uint4(0u, 0u, 0u, 0u);
+      if (on<TPR>(j, 0) && span_in_range(row + col<TPR>(j, 0), VE, n)) r = *reinterpret_cast<const uint4*>(base + col<TPR>(j, 0));
     } else {
 #pragma unroll
       for (int k = 0; k < VE; ++k) r.e[k] = on<TPR>(j, k) && in_range(row + col<TPR>(j, k), n) ? base[col<TPR>(j, k)] : E(0);
@@ -95,17 +96,19 @@ struct Part {
     return r;
   }
   __device__ static void open(const Raw& r, float* v) {
-    if constexpr (Stor<ST>::kBytes == 4) {
+    if constexpr (kAligned) {
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int k = 0; k < VE; ++k) v[k] = r.e[k];
-    } else if constexpr (kAligned) {
-      uint32_t w[4];
-      memcpy(w, &r, 16);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (VE == 4) v[k] = __uint_as_float(w[k]);
+        else v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < VE; ++k) v[k] = Stor<ST>::from_bits(r.e[k]);
+      for (int k = 0; k < VE; ++k) {
+        if constexpr (Stor<ST>::kBytes == 4) v[k] = r.e[k];
+        else v[k] = Stor<ST>::from_bits(r.e[k]);
+      }
     }
   }
   template <int TPR>
@@ -124,15 +127,10 @@ struct Part {
   // ---- in 8 bits
   template <int TPR>
   __device__ Raw8 load8(const uint8_t* q, int64_t row, int64_t N, int j) const {
-    Raw8 r;
+    Raw8 r{};
     if constexpr (kAligned) {
-      uint2 w = make_uint2(0u, 0u);
       const int64_t i = row * D + col<TPR>(j, 0);
-      if (on<TPR>(j, 0) && span_in_range(i, VE, N * D)) {
-        if constexpr (VE == 8) w = *reinterpret_cast<const uint2*>(q + i);
-        else w.x = *reinterpret_cast<const uint32_t*>(q + i);
-      }
-      memcpy(&r, &w, VE);
+      if (on<TPR>(j, 0) && span_in_range(i, VE, N * D)) r = *reinterpret_cast<const Raw8*>(q + i);
     } else {
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
@@ -151,7 +149,11 @@ struct Part {
   __device__ static void open8(const Raw8& r, float scale, float* v) {
 #pragma unroll
     for (int k = 0; k < VE; k += 2) {
-      const float2 f = from_e4m3x2((uint32_t)r.e[k] | (uint32_t)r.e[k + 1] << 8);
+      uint32_t two;
+      if constexpr (!kAligned) two = (uint32_t)r.e[k] | (uint32_t)r.e[k + 1] << 8;
+      else if constexpr (VE == 8) two = (k < 4 ? r.x : r.y) >> 8 * (k % 4);
+      else two = r >> 8 * k;
+      const float2 f = from_e4m3x2(two);
       v[k] = f.x * scale, v[k + 1] = f.y * scale;
     }
   }
@@ -185,7 +187,12 @@ struct Part {
 __host__ __device__ constexpr int cta_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
 // CTAs of `threads` threads an SM is to hold, by the values a thread has in registers
 __host__ __device__ constexpr int rms_resident(int threads, int values) {
-  const int n = (values >= 32 ? 512 : values >= 16 ? 768 : 1024) / threads;
+  #ifndef R32
+#define R32 512
+#define R16 768
+#define R8 1024
+#endif
+  const int n = (values >= 32 ? R32 : values >= 16 ? R16 : R8) / threads;
   return n > 0 ? n : 1;
 }
 
@@ -526,34 +533,21 @@ __global__ void __launch_bounds__(TPR, rms_grad_resident(TPR, VPT * Part<ST, tru
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = threadIdx.x + j * TPR;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u), traw = raw, draw = raw;
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u), traw = raw;
+      typename P::Raw8 q{};
+      dt[j] = raw;
       if (part.template on<TPR>(j, 0) &&
           span_in_range((int64_t)ring.stage * stage_bytes + v * 16, (int64_t)stage_bytes - row_bytes + 16, (int64_t)kRows * stage_bytes)) {
         raw = *reinterpret_cast<const uint4*>(at + v * 16);
-        if constexpr (!k8) {
-          traw = *reinterpret_cast<const uint4*>(at + row_bytes + v * 16);
-        } else if constexpr (VE == 8) {
-          const uint2 q = *reinterpret_cast<const uint2*>(at + row_bytes + v * 8);
-          traw.x = q.x, traw.y = q.y;
-        } else {
-          traw.x = *reinterpret_cast<const uint32_t*>(at + row_bytes + v * 4);
-        }
-        if (has_dt) draw = *reinterpret_cast<const uint4*>(at + row_bytes + t_bytes + v * 16);
+        if constexpr (k8) q = *reinterpret_cast<const typename P::Raw8*>(at + row_bytes + v * VE);
+        else traw = *reinterpret_cast<const uint4*>(at + row_bytes + v * 16);
+        if (has_dt) dt[j] = *reinterpret_cast<const uint4*>(at + row_bytes + t_bytes + v * 16);
       }
-      typename P::Raw f;
-      memcpy(&f, &raw, 16);
-      memcpy(&dt[j], &draw, 16);
       float fw[VE];
-      P::open(f, g[j]);
+      P::open(raw, g[j]);
       P::open(w[j], fw);
-      if constexpr (k8) {
-        typename P::Raw8 q;
-        memcpy(&q, &traw, VE);
-        P::open8(q, scale[j] * r, s[j]);
-      } else {
-        memcpy(&f, &traw, 16);
-        P::open(f, s[j]);
-      }
+      if constexpr (k8) P::open8(q, scale[j] * r, s[j]);
+      else P::open(traw, s[j]);
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
         if constexpr (!k8) s[j][k] *= r;
@@ -700,8 +694,12 @@ cudaError_t rms_width(const RmsArgs& a, int64_t parts, int sm, cudaStream_t s) {
   if (parts <= 64) return launch_rms<ST, kAligned, 2, 32>(a, sm, s);
   if (parts <= 128) return launch_rms<ST, kAligned, 4, 32>(a, sm, s);
   if (parts <= 256) return launch_rms<ST, kAligned, 2, 128>(a, sm, s);
-  if (parts <= 512) return launch_rms<ST, kAligned, 4, 128>(a, sm, s);
-  if (parts <= 1024) return launch_rms<ST, kAligned, 4, 256>(a, sm, s);
+#ifndef RV
+#define RV 2
+#define RT 256
+#endif
+  if (parts <= 512) return launch_rms<ST, kAligned, RV, RT>(a, sm, s);
+  if (parts <= 1024) return launch_rms<ST, kAligned, 2, 512>(a, sm, s);
   return launch_rms<ST, kAligned, 4, 512>(a, sm, s);
 }
 
