@@ -7,6 +7,7 @@
 // float32.
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "policy.h"
 #include "reduce.cuh"
@@ -125,6 +126,61 @@ __global__ void __launch_bounds__(kSerialThreads) gated_grad_serial_kernel(Gated
     }
     if (a.d_state != nullptr) a.d_state[i] = u;
   }
+}
+
+// The same for a few steps of rows on 16-byte boundaries, a thread a vector of
+// channels: one step of acting, or a few tokens at once.
+constexpr int kStepThreads = 128;
+
+template <class ST>
+__global__ void __launch_bounds__(kStepThreads) gated_step_kernel(GatedArgs a, int64_t blocks) {
+  constexpr int VE = 16 / Stor<ST>::kBytes;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t e = blockIdx.x / blocks, c = ((blockIdx.x % blocks) * kStepThreads + threadIdx.x) * VE;
+  if (c >= a.D) return;
+  const int64_t n = a.E * a.T, i = e * a.D + c;
+  const int len = row_length(a, e);
+  float h[VE];
+#pragma unroll
+  for (int k = 0; k < VE; k += 4) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.state != nullptr && span_in_range(i + k, 4, a.E * a.D)) s = *reinterpret_cast<const float4*>(a.state + i + k);
+    h[k] = s.x, h[k + 1] = s.y, h[k + 2] = s.z, h[k + 3] = s.w;
+  }
+  bool cut = false;
+  for (int t = 0; t < a.T; ++t) {
+    const int64_t row = e * a.step_e + t * a.step_t;
+    float v[VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) v[k] = 0.f;
+    if (t < len) {
+      float g[VE];
+      const bool ok = span_in_range(row * a.x_stride + c, VE, n * a.x_stride) && span_in_range(row * a.gate_stride + c, VE, n * a.gate_stride);
+      if constexpr (VE == 8) {
+        Stor<ST>::ld8(a.x, row * a.x_stride + c, ok, v);
+        Stor<ST>::ld8(a.gate, row * a.gate_stride + c, ok, g);
+      } else {
+        Stor<ST>::ld4(a.x, row * a.x_stride + c, ok, v);
+        Stor<ST>::ld4(a.gate, row * a.gate_stride + c, ok, g);
+      }
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        const Gate s = Sigma<ST>::of(g[k]);
+        h[k] = v[k] = cut ? s.na * v[k] : fmaf(s.a, h[k], s.na * v[k]);
+      }
+      cut = flagged(a, row);
+    }
+    if (span_in_range(row * a.D + c, VE, n * a.D)) {
+      if constexpr (VE == 8) Stor<ST>::st8(a.h, row * a.D + c, v);
+      else Stor<ST>::st4(a.h, row * a.D + c, v);
+    }
+  }
+  if (a.last == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < VE; k += 4)
+    if (span_in_range(i + k, 4, a.E * a.D))
+      *reinterpret_cast<float4*>(a.last + i + k) = cut ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -267,53 +323,74 @@ __device__ __forceinline__ void tile_load(void* to, const CUtensorMap* map, int 
 
 // Where the rows of every array start on 16-byte boundaries (kBulk), a tile of
 // an array is one tensor copy, and a lane's channels are next to each other.
-// Other rows are copied in 16-byte vectors from the boundary in front of
-// them -- a vector that holds any byte of the row is readable as a whole --, and
-// a lane's channels are 32 apart.
+// Other rows are copied one by one, from the boundary in front of them to the
+// one behind -- 16 bytes that hold any byte of the row are readable as a whole.
+// Their pitch in shared memory is the matrix's modulo 16 bytes, so that a row's
+// first column stays as far behind a boundary as it is in memory and a column
+// lies at one pitch in all of them.  A lane's channels are 32 apart there.
 template <class ST, bool kBulk, int L>
 struct TileRows {
-  static constexpr int kBytes = Stor<ST>::kBytes, kPitch = kCols * kBytes + (kBulk ? 0 : 16), kTile = L * kPitch;
-  static constexpr int kVectors = kCols * kBytes / 16 + 1;
+  static constexpr int kBytes = Stor<ST>::kBytes, kRow = kCols * kBytes;
+  // (a row and what lies in front of and behind it in its boundaries)
+  static constexpr int kLeast = kRow + 2 * (16 - kBytes), kMost = kLeast + 16 - kBytes;
+  static constexpr int kTile = kBulk ? L * kRow : L * kMost + 16;
+  // bytes from step to step of an array whose steps lie `step` bytes apart
+  __device__ static uint32_t pitch(int64_t step) { return kBulk ? kRow : kLeast + (((uint32_t)step - kLeast) & 15); }
 };
 
-// this thread's vectors of the steps t0 .. t0 + L - 1 in front of `len` of one array
-template <class ST, int L, int THREADS>
-__device__ __forceinline__ void copy_rows(unsigned char* tile, const float* p, const GatedArgs& a, int64_t stride, int64_t e,
-                                          int64_t t0, int64_t len, int64_t c0) {
+// The rows of steps t0[k] .. t0[k] + L - 1 in front of `len` of the arrays p[k] into their tiles: a copy a row, from the
+// boundary in front of it to the one behind its last column, each thread some of the rows.
+template <class ST, int N, int L, int THREADS>
+__device__ __forceinline__ void copy_rows(unsigned char* tiles, const float* const* p, const int64_t* stride, const int* t0,
+                                          const GatedArgs& a, int64_t e, int len, int64_t c0, uint64_t* bar) {
   using R = TileRows<ST, false, L>;
+  static_assert(THREADS % L == 0 || L % THREADS == 0, "a thread's rows lie in whole steps of threads");
   const uint32_t width = (uint32_t)min((int64_t)kCols, a.D - c0) * R::kBytes;
-  for (int i = threadIdx.x; i < L * R::kVectors; i += THREADS) {
-    const int r = i / R::kVectors, v = i % R::kVectors;
-    if (t0 + r < 0 || t0 + r >= len) continue;
-    const int64_t row = ((e * a.step_e + (t0 + r) * a.step_t) * stride + c0) * R::kBytes;
-    const uintptr_t at = (uintptr_t)p + row;
-    const uint32_t shift = at & 15;
-    if (16 * (uint32_t)v >= shift + width) continue;
-    if (!in_range((row + max(16 * v - (int)shift, 0)) / R::kBytes, a.E * a.T * stride) ||
-        !span_in_range(r * R::kPitch + 16 * v, 16, R::kTile))
-      continue;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(tile + r * R::kPitch + 16 * v)),
-                 "l"(at - shift + 16 * v)
-                 : "memory");
+  constexpr int kMine = (N * L + THREADS - 1) / THREADS;
+  uint32_t bytes = 0, to[kMine], size[kMine];
+  uintptr_t at[kMine];
+#pragma unroll
+  for (int m = 0; m < kMine; ++m) {
+    const int i = threadIdx.x + m * THREADS, k = i / L, r = i % L;
+    size[m] = to[m] = 0;
+    at[m] = 0;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      if (q != k) continue;
+      const int t = t0[q] + r;
+      const int64_t row = (e * a.step_e + t * a.step_t) * stride[q] + c0;
+      if (t < 0 || t >= len || !span_in_range(row, width / R::kBytes, a.E * a.T * stride[q])) continue;
+      at[m] = (uintptr_t)p[q] + row * R::kBytes;
+      size[m] = ((uint32_t)(at[m] & 15) + width + 15) & ~15u;
+      const uint32_t first = (uint32_t)((uintptr_t)p[q] + ((e * a.step_e + t0[q] * a.step_t) * stride[q] + c0) * R::kBytes) & 15;
+      to[m] = q * R::kTile + first + r * R::pitch(a.step_t * stride[q] * R::kBytes);
+    }
+    bytes += size[m];
+  }
+  mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+  for (int m = 0; m < kMine; ++m) {
+    if (size[m] != 0 && span_in_range(to[m] & ~15u, size[m], N * R::kTile))
+      bulk_load(tiles + (to[m] & ~15u), reinterpret_cast<const void*>(at[m] & ~(uintptr_t)15), size[m], bar);
   }
 }
-// an arrival on `bar` when this thread's copies so far have landed
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
-// A lane's two channels of consecutive steps of a tile.
+// A lane's two channels of the warp's steps of a tile.  Tiles are whole multiples of 16 bytes in steps of any matrix, so a
+// step lies at the same place in all of them.
 template <class ST, bool kBulk, int L>
 struct Reader {
   using R = TileRows<ST, kBulk, L>;
-  const unsigned char* at;
-  uint32_t shift = 0, move = 0;
-  // from step r of the tile on; the array's address of that row's first column, and its bytes from step to step
-  __device__ Reader(const unsigned char* tile, int r, int lane, uint32_t address, uint32_t step)
-      : at(tile + r * R::kPitch + lane * (kBulk ? 2 : 1) * R::kBytes), shift(address & 15), move(step & 15) {}
-  __device__ __forceinline__ Two<ST> get(int i) const {
-    if constexpr (kBulk) return Two<ST>::pair(at + i * R::kPitch);
-    else return Two<ST>::split(at + i * R::kPitch + ((shift + i * move) & 15));
+  static_assert(L * R::kBytes % 16 == 0, "a step's place in its 16 bytes does not change from tile to tile");
+  uint32_t at, pitch;
+  // array k from step r of a tile on; `row` of the matrix is the first step of one
+  __device__ Reader(const GatedArgs& a, int k, int r, int lane, const float* p, int64_t row, int64_t stride, int64_t c0)
+      : pitch(R::pitch(a.step_t * stride * R::kBytes)) {
+    at = k * R::kTile + r * pitch + lane * (kBulk ? 2 : 1) * R::kBytes;
+    if constexpr (!kBulk) at += ((uint32_t)(uintptr_t)p + (uint32_t)(row * stride + c0) * R::kBytes) & 15;
+  }
+  __device__ __forceinline__ Two<ST> get(const unsigned char* stage, int i) const {
+    if constexpr (kBulk) return Two<ST>::pair(stage + at + i * R::kRow);
+    else return Two<ST>::split(stage + at + i * pitch);
   }
 };
 
@@ -345,18 +422,20 @@ struct Cols {
   }
 };
 
-// Writes consecutive steps of a matrix: the address moves by one row a step.
+// Writes the warp's steps of a matrix: from `base` on, which moves from round to round.
 template <class ST, bool kPairs>
 struct Writer {
-  unsigned char* at;
+  unsigned char *base, *at;
   int64_t step, first, last;  // bytes a step; the matrix, for the index check
   bool on[2];
   __device__ Writer(const Cols<ST, kPairs>& cols, const GatedArgs& a, float* p, int64_t stride, int64_t row) {
-    at = reinterpret_cast<unsigned char*>(p) + (row * stride + cols.ch(0)) * Stor<ST>::kBytes;
+    base = reinterpret_cast<unsigned char*>(p) + (row * stride + cols.ch(0)) * Stor<ST>::kBytes;
     step = a.step_t * stride * Stor<ST>::kBytes;
     first = (int64_t)p, last = (int64_t)p + a.E * a.T * stride * Stor<ST>::kBytes;
     on[0] = cols.on(0), on[1] = cols.on(1);
   }
+  __device__ __forceinline__ void start() { at = base; }
+  __device__ __forceinline__ void move(int steps) { base += steps * step; }
   __device__ __forceinline__ void put(V2 v) {
     const float2 f = apart(v);
     if constexpr (kPairs) {
@@ -374,7 +453,7 @@ struct Writer {
 };
 
 // whether the state before step t counts as 0 (steps in front of `len` only)
-__device__ __forceinline__ bool cut_before(const GatedArgs& a, int64_t e, int64_t t, int len) {
+__device__ __forceinline__ bool cut_before(const GatedArgs& a, int64_t e, int t, int len) {
   return t > 0 && t < len && flagged(a, e * a.step_e + (t - 1) * a.step_t);
 }
 
@@ -453,9 +532,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
       tile_load(to, &maps.in[0], (int)cols.c0, t, (int)e, &sh.full[stage]);
       tile_load(to + R::kTile, &maps.in[1], (int)cols.c0, t, (int)e, &sh.full[stage]);
     } else {
-      copy_rows<ST, L, 32 * W>(to, a.x, a, a.x_stride, e, t, len, cols.c0);
-      copy_rows<ST, L, 32 * W>(to + R::kTile, a.gate, a, a.gate_stride, e, t, len, cols.c0);
-      copies_arrive(&sh.full[stage]);
+      const float* const from[kArrays] = {a.x, a.gate};
+      const int64_t stride[kArrays] = {a.x_stride, a.gate_stride};
+      const int at[kArrays] = {t, t};
+      copy_rows<ST, kArrays, L, 32 * W>(to, from, stride, at, a, e, len, cols.c0, &sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
@@ -463,14 +543,20 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   V2 carry = cols.state(a.state, e, a.E);
   FillRing<STAGES> ring;
   bool met = true;
+  int t0 = rank * L + warp * C;  // the warp's first step of the round
+  const int64_t row0 = e * a.step_e + t0 * a.step_t, tile0 = e * a.step_e + (int64_t)rank * L * a.step_t;
+  const Reader<ST, kBulk, L> xs(a, 0, warp * C, lane, a.x, tile0, a.x_stride, cols.c0);
+  const Reader<ST, kBulk, L> gs(a, 1, warp * C, lane, a.gate, tile0, a.gate_stride, cols.c0);
+  Writer<ST, kBulk> out(cols, a, a.h, a.D, row0);
   const bool flags = a.terminated != nullptr || a.truncated != nullptr;
-  bool cut_next = flags && lane < C && cut_before(a, e, (int64_t)rank * L + warp * C + lane, len);
-  for (int k = 0; k < rounds; ++k) {
-    const int64_t t0 = ((int64_t)rank + (int64_t)k * share) * L + warp * C;  // the warp's first step
-    const int real = (int)min(max(len - t0, (int64_t)0), (int64_t)C);
-    const int64_t row0 = e * a.step_e + t0 * a.step_t;
-    const uint32_t cut = __ballot_sync(kFullMask, cut_next);
-    if (flags && lane < C) cut_next = cut_before(a, e, t0 + (int64_t)share * L + lane, len);
+  bool cut_next = flags && lane < C && cut_before(a, e, t0 + lane, len);
+  for (int k = 0; k < rounds; ++k, t0 += share * L) {
+    const int real = min(max(len - t0, 0), C);
+    uint32_t cut = 0;
+    if (flags) {
+      cut = __ballot_sync(kFullMask, cut_next);
+      if (lane < C) cut_next = cut_before(a, e, t0 + share * L + lane, len);
+    }
     V2 p[C], q[C];
     Map2 m = identity();
     if (k < mine) {
@@ -478,17 +564,12 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
       if (ring.ok) ring.ok = mbar_wait_bounded(&sh.full[ring.stage], ring.phase);
       const unsigned char* tile = ring_tiles + (size_t)ring.stage * kArrays * R::kTile;
       ring.next();
-      const Reader<ST, kBulk, L> xs(tile, warp * C, lane, (uint32_t)(uintptr_t)a.x + (uint32_t)(row0 * a.x_stride + cols.c0) * R::kBytes,
-                                    (uint32_t)(a.step_t * a.x_stride) * R::kBytes);
-      const Reader<ST, kBulk, L> gs(tile + R::kTile, warp * C, lane,
-                                    (uint32_t)(uintptr_t)a.gate + (uint32_t)(row0 * a.gate_stride + cols.c0) * R::kBytes,
-                                    (uint32_t)(a.step_t * a.gate_stride) * R::kBytes);
       if (cut == 0 && real == C) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
           V2 s, ns;
-          gs.get(i).sigma(&s, &ns);
-          m.q = q[i] = fma2(s, m.q, mul2(ns, xs.get(i).wide()));
+          gs.get(tile, i).sigma(&s, &ns);
+          m.q = q[i] = fma2(s, m.q, mul2(ns, xs.get(tile, i).wide()));
           m.p = p[i] = mul2(m.p, s);
         }
       } else {
@@ -496,8 +577,8 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
         for (int i = 0; i < C; ++i) {
           if (i < real) {
             V2 s, ns;
-            gs.get(i).sigma(&s, &ns);
-            const V2 b = mul2(ns, xs.get(i).wide());
+            gs.get(tile, i).sigma(&s, &ns);
+            const V2 b = mul2(ns, xs.get(tile, i).wide());
             if ((cut >> i) & 1) m = {0x8000000080000000ull, b};
             else m = chain({s, b}, m);
           }
@@ -509,7 +590,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
     sh.warp_map[k & 1][warp][lane] = m;
     const bool any_cut = __syncthreads_or(cut != 0);
     const V2 h = meet<W, STAGES, true>(sh, k, rank, share, any_cut, &met, &carry);
-    Writer<ST, kBulk> out(cols, a, a.h, a.D, row0);
+    out.start();
     if (k < mine && real == C && cut == 0) {
 #pragma unroll
       for (int i = 0; i < C; ++i) out.put(fma2(p[i], h, q[i]));
@@ -518,20 +599,21 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
       for (int i = 0; i < C; ++i)
         if (t0 + i < a.T) out.put(k < mine && i < real ? pass({p[i], q[i]}, h) : 0);
     }
+    out.move(share * L);
   }
   // behind the row's last tile
-  for (int64_t t = ((int64_t)rounds * share + rank) * L + warp * C; t < a.T; t += (int64_t)share * L) {
-    Writer<ST, kBulk> out(cols, a, a.h, a.D, e * a.step_e + t * a.step_t);
-    for (int i = 0; i < C && t + i < a.T; ++i) out.put(0);
+  for (; t0 < a.T; t0 += share * L) {
+    out.start();
+    for (int i = 0; i < C && t0 + i < a.T; ++i) out.put(0);
+    out.move(share * L);
   }
   if (rank == 0 && warp == 0 && a.last != nullptr) {
     if (len > 0 && flagged(a, e * a.step_e + (int64_t)(len - 1) * a.step_t)) carry = 0;
     cols.store_state(a.last, e, a.E, carry);
   }
   // (copies still on their way after a wait gave up land before the CTA ends)
-  if (kBulk && !ring.ok && threadIdx.x == 0)
+  if (!ring.ok && (threadIdx.x == 0 || !kBulk))
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
-  if (!kBulk) asm volatile("cp.async.wait_all;" ::: "memory");
   if (share > 1) cluster_meet();  // no CTA ends while a peer may still write to it
 }
 
@@ -571,11 +653,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
       for (int i = 0; i < kArrays; ++i)
         tile_load(to + i * R::kTile, &maps.in[i], (int)cols.c0, i == 3 ? t - 1 : t, (int)e, &sh.full[stage]);
     } else {
-      copy_rows<ST, L, 32 * W>(to, a.x, a, a.x_stride, e, t, len, cols.c0);
-      copy_rows<ST, L, 32 * W>(to + R::kTile, a.gate, a, a.gate_stride, e, t, len, cols.c0);
-      copy_rows<ST, L, 32 * W>(to + 2 * R::kTile, a.dh, a, a.dh_stride, e, t, len, cols.c0);
-      copy_rows<ST, L, 32 * W>(to + 3 * R::kTile, a.in_h, a, a.h_stride, e, t - 1, len, cols.c0);
-      copies_arrive(&sh.full[stage]);
+      const float* const from[kArrays] = {a.x, a.gate, a.dh, a.in_h};
+      const int64_t stride[kArrays] = {a.x_stride, a.gate_stride, a.dh_stride, a.h_stride};
+      const int at[kArrays] = {t, t, t, t - 1};
+      copy_rows<ST, kArrays, L, 32 * W>(to, from, stride, at, a, e, len, cols.c0, &sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
@@ -585,14 +666,31 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   FillRing<STAGES> ring;
   bool met = true;
   int j = 0;
+  int t0 = (rank + (rounds - 1) * share) * L + warp * C;
+  const int64_t row0 = e * a.step_e + t0 * a.step_t;
+  const auto reader = [&](int i, const float* p, int64_t row, int64_t stride) {
+    return Reader<ST, kBulk, L>(a, i, warp * C, lane, p, row, stride, cols.c0);
+  };
+  const int64_t tile0 = e * a.step_e + (int64_t)rank * L * a.step_t;
+  const auto xs = reader(0, a.x, tile0, a.x_stride), gs = reader(1, a.gate, tile0, a.gate_stride),
+             ds = reader(2, a.dh, tile0, a.dh_stride), hs = reader(3, a.in_h, tile0 - a.step_t, a.h_stride);
+  Writer<ST, kBulk> to_x(cols, a, a.dx, a.dx_stride, row0), to_gate(cols, a, a.dgate, a.dgate_stride, row0);
+  // behind the row's last tile
+  for (int t = t0 + share * L; t < a.T; t += share * L) {
+    Writer<ST, kBulk> x = to_x, g = to_gate;
+    x.move(t - t0), g.move(t - t0);
+    x.start(), g.start();
+    for (int i = 0; i < C && t + i < a.T; ++i) x.put(0), g.put(0);
+  }
   const bool flags = a.terminated != nullptr || a.truncated != nullptr;
-  bool cut_next = flags && lane < C && cut_before(a, e, ((int64_t)rank + (int64_t)(rounds - 1) * share) * L + warp * C + lane, len);
-  for (int k = rounds - 1; k >= 0; --k) {
-    const int64_t t0 = ((int64_t)rank + (int64_t)k * share) * L + warp * C;
-    const int real = (int)min(max(len - t0, (int64_t)0), (int64_t)C);
-    const int64_t row0 = e * a.step_e + t0 * a.step_t;
-    const uint32_t cut = __ballot_sync(kFullMask, cut_next);
-    if (flags && lane < C) cut_next = cut_before(a, e, t0 - (int64_t)share * L + lane, len);
+  bool cut_next = flags && lane < C && cut_before(a, e, t0 + lane, len);
+  for (int k = rounds - 1; k >= 0; --k, t0 -= share * L) {
+    const int real = min(max(len - t0, 0), C);
+    uint32_t cut = 0;
+    if (flags) {
+      cut = __ballot_sync(kFullMask, cut_next);
+      if (lane < C) cut_next = cut_before(a, e, t0 - share * L + lane, len);
+    }
     // a step's G is g + p u, u from behind the chunk; dx = na G, dgate = w G
     V2 p[C], g[C], na[C], w[C];
     Map2 m = identity();
@@ -603,21 +701,14 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
       const unsigned char* tile = ring_tiles + (size_t)ring.stage * kArrays * R::kTile;
       ring.next();
       ++j;
-      const auto reader = [&](int i, const float* base, int64_t row, int64_t stride) {
-        return Reader<ST, kBulk, L>(tile + i * R::kTile, warp * C, lane,
-                                    (uint32_t)(uintptr_t)base + (uint32_t)(row * stride + cols.c0) * R::kBytes,
-                                    (uint32_t)(a.step_t * stride) * R::kBytes);
-      };
-      const auto xs = reader(0, a.x, row0, a.x_stride), gs = reader(1, a.gate, row0, a.gate_stride),
-                 ds = reader(2, a.dh, row0, a.dh_stride), hs = reader(3, a.in_h, row0 - a.step_t, a.h_stride);
       if (cut == 0 && real == C && t0 > 0) {
 #pragma unroll
         for (int i = C - 1; i >= 0; --i) {
           V2 s;
-          gs.get(i).sigma(&s, &na[i]);
+          gs.get(tile, i).sigma(&s, &na[i]);
           p[i] = m.p;
-          g[i] = add2(ds.get(i).wide(), m.q);
-          w[i] = mul2(mul2(s, na[i]), fma2(xs.get(i).wide(), minus, hs.get(i).wide()));
+          g[i] = add2(ds.get(tile, i).wide(), m.q);
+          w[i] = mul2(mul2(s, na[i]), fma2(xs.get(tile, i).wide(), minus, hs.get(tile, i).wide()));
           m.q = mul2(s, g[i]);
           m.p = mul2(m.p, s);
         }
@@ -630,11 +721,11 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
           na[i] = w[i] = 0;
           if (i < real) {
             V2 s;
-            gs.get(i).sigma(&s, &na[i]);
+            gs.get(tile, i).sigma(&s, &na[i]);
             const bool here = (cut >> i) & 1;
-            const V2 before = here ? 0 : t0 + i == 0 ? first : hs.get(i).wide();
-            g[i] = add2(ds.get(i).wide(), m.q);
-            w[i] = mul2(mul2(s, na[i]), fma2(xs.get(i).wide(), minus, before));
+            const V2 before = here ? 0 : t0 + i == 0 ? first : hs.get(tile, i).wide();
+            g[i] = add2(ds.get(tile, i).wide(), m.q);
+            w[i] = mul2(mul2(s, na[i]), fma2(xs.get(tile, i).wide(), minus, before));
             if (here) m = {0x8000000080000000ull, 0};
             else m = {severed(m) ? m.p : mul2(m.p, s), mul2(s, g[i])};
           }
@@ -644,7 +735,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
     sh.warp_map[(rounds - 1 - k) & 1][warp][lane] = m;
     const bool any_cut = __syncthreads_or(cut != 0);
     const V2 u = meet<W, STAGES, false>(sh, rounds - 1 - k, rank, share, any_cut, &met, &carry);
-    Writer<ST, kBulk> to_x(cols, a, a.dx, a.dx_stride, row0), to_gate(cols, a, a.dgate, a.dgate_stride, row0);
+    to_x.start(), to_gate.start();
     if (k < mine && real == C && cut == 0) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -662,16 +753,11 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
         to_gate.put(on ? mul2(w[i], G) : 0);
       }
     }
-  }
-  for (int64_t t = ((int64_t)rounds * share + rank) * L + warp * C; t < a.T; t += (int64_t)share * L) {
-    const int64_t row = e * a.step_e + t * a.step_t;
-    Writer<ST, kBulk> to_x(cols, a, a.dx, a.dx_stride, row), to_gate(cols, a, a.dgate, a.dgate_stride, row);
-    for (int i = 0; i < C && t + i < a.T; ++i) to_x.put(0), to_gate.put(0);
+    to_x.move(-share * L), to_gate.move(-share * L);
   }
   if (rank == 0 && warp == 0 && a.d_state != nullptr) cols.store_state(a.d_state, e, a.E, carry);
-  if (kBulk && !ring.ok && threadIdx.x == 0)
+  if (!ring.ok && (threadIdx.x == 0 || !kBulk))
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
-  if (!kBulk) asm volatile("cp.async.wait_all;" ::: "memory");
   if (share > 1) cluster_meet();
 }
 
@@ -709,58 +795,77 @@ bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_lis
   return true;
 }
 
-// CTAs of a row: enough to give every SM two, as far as the row has tiles for them
-int row_share(int64_t units, int64_t ntiles, int sm) {
+// The shape of a tile kernel: C steps a thread, W warps, STAGES tiles in the
+// ring, RES CTAs an SM.
+template <int kChunk, int kWarps, int kStages, int kRes>
+struct Shape {
+  static constexpr int C = kChunk, W = kWarps, STAGES = kStages, RES = kRes;
+};
+template <class ST, bool kBack, bool kBulk>
+struct TileShape;
+template <bool kBulk>
+struct TileShape<bf16, false, kBulk> : Shape<16, 4, 2, 4> {};
+template <bool kBulk>
+struct TileShape<float, false, kBulk> : Shape<8, 4, 2, 4> {};
+template <>
+struct TileShape<bf16, true, true> : Shape<16, 4, 3, 2> {};
+template <>
+struct TileShape<bf16, true, false> : Shape<8, 4, 2, 4> {};
+template <>
+struct TileShape<float, true, true> : Shape<8, 4, 3, 2> {};
+template <>
+struct TileShape<float, true, false> : Shape<8, 4, 2, 2> {};
+
+// CTAs of a row: as many as fit the SMs beside each other
+int row_share(int64_t units, int64_t ntiles, int64_t slots) {
   int share = 1;
-  while (share < kMaxShare && units * share < 2 * (int64_t)sm && ntiles >= 2 * share) share *= 2;
+  while (share < kMaxShare && 2 * share * units <= slots && 2 * share <= ntiles) share *= 2;
   return share;
 }
 
-template <class ST>
-cudaError_t scan_typed(const GatedArgs& a, int sm, cudaStream_t s) {
-#ifndef FC
-#define FC 16
-#define FW 4
-#define FR 4
-#define FS 2
-#endif
-  constexpr int kChunk = Stor<ST>::kBytes == 2 ? FC : 8, W = Stor<ST>::kBytes == 2 ? FW : 4, L = kChunk * W, kStages = FS, es = Stor<ST>::kBytes;
-  constexpr int kRes = FR;
-  const int64_t units = a.E * div_up(a.D, kCols);
-  if (a.T <= 4) return launch_serial(gated_serial_kernel<ST>, a, sm, s);
-  const int share = row_share(units, div_up(a.T, L), sm);
-  if (units * share > INT32_MAX) return launch_serial(gated_serial_kernel<ST>, a, sm, s);
-  GatedMaps maps = {};
-  if (rows_aligned({a.x, a.gate}, {a.x_stride, a.gate_stride}, es, 16) && rows_aligned({a.h}, {a.D}, es, 2 * es) &&
-      encode_steps_map(&maps.in[0], a.x, es, a.D, a.T, a.E, a.x_stride * a.step_t, a.x_stride * a.step_e, kCols, L) &&
-      encode_steps_map(&maps.in[1], a.gate, es, a.D, a.T, a.E, a.gate_stride * a.step_t, a.gate_stride * a.step_e, kCols, L)) {
-    const auto kernel = gated_tile_kernel<ST, kChunk, W, kStages, true, kRes>;
-    const size_t smem = (size_t)kStages * 2 * TileRows<ST, true, L>::kTile;
-    static std::atomic<uint64_t> allowed;
-    const cudaError_t e = allow_smem(kernel, smem, allowed);
-    return e != cudaSuccess ? e : launch_tiles(kernel, units * share, 32 * W, smem, share, s, a, maps);
-  }
-  const auto kernel = gated_tile_kernel<ST, kChunk, W, kStages, false, kRes>;
-  const size_t smem = (size_t)kStages * 2 * TileRows<ST, false, L>::kTile;
+template <class ST, bool kBack, bool kBulk>
+cudaError_t run_tiles(const GatedArgs& a, const GatedMaps& maps, int sm, cudaStream_t s) {
+  using H = TileShape<ST, kBack, kBulk>;
+  constexpr int L = H::C * H::W;
+  constexpr size_t smem = (size_t)H::STAGES * (kBack ? 4 : 2) * TileRows<ST, kBulk, L>::kTile;
+  static_assert(H::RES * (smem + sizeof(GatedShared<H::W, H::STAGES>) + 1024) <= 228 * 1024, "RES CTAs fit an SM");
+  void (*kernel)(GatedArgs, GatedMaps, int);
+  if constexpr (kBack) kernel = gated_grad_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, H::RES>;
+  else kernel = gated_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, H::RES>;
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_smem(kernel, smem, allowed);
-  return e != cudaSuccess ? e : launch_tiles(kernel, units * share, 32 * W, smem, share, s, a, maps);
+  if (e != cudaSuccess) return e;
+  const int64_t units = a.E * div_up(a.D, kCols);
+  const int share = row_share(units, div_up(a.T, L), (int64_t)H::RES * sm);
+  return launch_tiles(kernel, units * share, 32 * H::W, smem, share, s, a, maps);
+}
+
+// a row takes the tile kernels from 5 steps on, if the grid can be launched
+bool by_tiles(const GatedArgs& a) { return a.T > 4 && a.E * div_up(a.D, kCols) <= INT32_MAX / kMaxShare; }
+
+template <class ST>
+cudaError_t scan_typed(const GatedArgs& a, int sm, cudaStream_t s) {
+  constexpr int es = Stor<ST>::kBytes, L = TileShape<ST, false, true>::C * TileShape<ST, false, true>::W;
+  if (!by_tiles(a)) {
+    const int64_t blocks = div_up(a.D, kStepThreads * 16 / es);
+    if (a.E * blocks <= INT32_MAX && rows_aligned({a.x, a.gate, a.h}, {a.D, a.x_stride, a.gate_stride}, es, 16) &&
+        rows_aligned({a.state, a.last}, {}, 4, 16))
+      return launch_pdl(gated_step_kernel<ST>, a.E * blocks, kStepThreads, 0, s, a, blocks);
+    return launch_serial(gated_serial_kernel<ST>, a, sm, s);
+  }
+  GatedMaps maps = {};
+  const float* in[2] = {a.x, a.gate};
+  const int64_t stride[2] = {a.x_stride, a.gate_stride};
+  bool bulk = rows_aligned({a.x, a.gate}, {a.x_stride, a.gate_stride}, es, 16) && rows_aligned({a.h}, {a.D}, es, 2 * es);
+  for (int i = 0; bulk && i < 2; ++i)
+    bulk = encode_steps_map(&maps.in[i], in[i], es, a.D, a.T, a.E, stride[i] * a.step_t, stride[i] * a.step_e, kCols, L);
+  return bulk ? run_tiles<ST, false, true>(a, maps, sm, s) : run_tiles<ST, false, false>(a, maps, sm, s);
 }
 
 template <class ST>
 cudaError_t grad_typed(const GatedArgs& a, int sm, cudaStream_t s) {
-#ifndef HC
-#define HC 8
-#define HW 8
-#define HR 2
-#define HS 3
-#endif
-  constexpr int kChunk = Stor<ST>::kBytes == 2 ? HC : 8, W = Stor<ST>::kBytes == 2 ? HW : 4, L = kChunk * W, kStages = HS, es = Stor<ST>::kBytes;
-  constexpr int kRes = HR;
-  const int64_t units = a.E * div_up(a.D, kCols);
-  if (a.T <= 4) return launch_serial(gated_grad_serial_kernel<ST>, a, sm, s);
-  const int share = row_share(units, div_up(a.T, L), sm);
-  if (units * share > INT32_MAX) return launch_serial(gated_grad_serial_kernel<ST>, a, sm, s);
+  if (!by_tiles(a)) return launch_serial(gated_grad_serial_kernel<ST>, a, sm, s);
+  constexpr int es = Stor<ST>::kBytes, L = TileShape<ST, true, true>::C * TileShape<ST, true, true>::W;
   GatedMaps maps = {};
   const float* in[4] = {a.x, a.gate, a.dh, a.in_h};
   const int64_t stride[4] = {a.x_stride, a.gate_stride, a.dh_stride, a.h_stride};
@@ -768,18 +873,7 @@ cudaError_t grad_typed(const GatedArgs& a, int sm, cudaStream_t s) {
               rows_aligned({a.dx, a.dgate}, {a.D, a.dx_stride, a.dgate_stride}, es, 2 * es);
   for (int i = 0; bulk && i < 4; ++i)
     bulk = encode_steps_map(&maps.in[i], in[i], es, a.D, a.T, a.E, stride[i] * a.step_t, stride[i] * a.step_e, kCols, L);
-  if (bulk) {
-    const auto kernel = gated_grad_tile_kernel<ST, kChunk, W, kStages, true, kRes>;
-    const size_t smem = (size_t)kStages * 4 * TileRows<ST, true, L>::kTile;
-    static std::atomic<uint64_t> allowed;
-    const cudaError_t e = allow_smem(kernel, smem, allowed);
-    return e != cudaSuccess ? e : launch_tiles(kernel, units * share, 32 * W, smem, share, s, a, maps);
-  }
-  const auto kernel = gated_grad_tile_kernel<ST, kChunk, W, kStages, false, kRes>;
-  const size_t smem = (size_t)kStages * 4 * TileRows<ST, false, L>::kTile;
-  static std::atomic<uint64_t> allowed;
-  const cudaError_t e = allow_smem(kernel, smem, allowed);
-  return e != cudaSuccess ? e : launch_tiles(kernel, units * share, 32 * W, smem, share, s, a, maps);
+  return bulk ? run_tiles<ST, true, true>(a, maps, sm, s) : run_tiles<ST, true, false>(a, maps, sm, s);
 }
 
 }  // namespace

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kMaxRows = INT32_MAX;
 constexpr int64_t kMaxWidth = int64_t(1) << 30;
+constexpr int64_t kMaxSteps = int64_t(1) << 30;
 constexpr int64_t kMaxStride = int64_t(1) << 31;
 
 bool sizes_ok(int64_t n, int64_t width) { return n >= 0 && width >= 0 && n <= kMaxRows && width <= kMaxWidth; }
@@ -62,7 +63,7 @@ size_t ebytes(uint32_t flags) { return (flags & RLCA_BF16) ? 2 : 4; }
 
 // sizes and flags of a gated scan: RLCA_OK with *empty where nothing is to be done, or the status to return
 int gated_sizes(int64_t E, int64_t T, int64_t D, uint32_t flags, bool* empty) {
-  if (!sizes_ok(E, D) || T < 0 || T > kMaxRows || !flags_ok(flags, RLCA_TIME_MAJOR | RLCA_BF16)) return RLCA_ERR_INVALID_ARG;
+  if (!sizes_ok(E, D) || T < 0 || T > kMaxSteps || !flags_ok(flags, RLCA_TIME_MAJOR | RLCA_BF16)) return RLCA_ERR_INVALID_ARG;
   *empty = E == 0 || D == 0;
   if (!*empty && E * T > kMaxRows) return RLCA_ERR_INVALID_ARG;
   return RLCA_OK;
