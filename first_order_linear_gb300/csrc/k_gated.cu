@@ -132,6 +132,16 @@ __global__ void __launch_bounds__(kSerialThreads) gated_grad_serial_kernel(Gated
 // channels: one step of acting, or a few tokens at once.
 constexpr int kStepThreads = 128;
 
+// 16 bytes of elements
+__device__ __forceinline__ void widen(const uint4& r, float (&v)[4]) {
+  v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void widen(const uint4& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+}
+
 template <class ST>
 __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(GatedArgs a, int64_t blocks) {
   constexpr int VE = 16 / Stor<ST>::kBytes;
@@ -149,31 +159,46 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(GatedArgs a, i
     h[k] = s.x, h[k + 1] = s.y, h[k + 2] = s.z, h[k + 3] = s.w;
   }
   bool cut = false;
-  for (int t = 0; t < a.T; ++t) {
-    const int64_t row = e * a.step_e + t * a.step_t;
-    float v[VE];
+  constexpr int kAhead = 4;  // steps whose loads are on their way together
+  for (int t0 = 0; t0 < a.T; t0 += kAhead) {
+    uint4 xs[kAhead], gs[kAhead];
+    bool ends[kAhead];
 #pragma unroll
-    for (int k = 0; k < VE; ++k) v[k] = 0.f;
-    if (t < len) {
-      float g[VE];
-      const bool ok = span_in_range(row * a.x_stride + c, VE, n * a.x_stride) && span_in_range(row * a.gate_stride + c, VE, n * a.gate_stride);
-      if constexpr (VE == 8) {
-        Stor<ST>::ld8(a.x, row * a.x_stride + c, ok, v);
-        Stor<ST>::ld8(a.gate, row * a.gate_stride + c, ok, g);
-      } else {
-        Stor<ST>::ld4(a.x, row * a.x_stride + c, ok, v);
-        Stor<ST>::ld4(a.gate, row * a.gate_stride + c, ok, g);
-      }
-#pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        const Gate s = Sigma<ST>::of(g[k]);
-        h[k] = v[k] = cut ? s.na * v[k] : fmaf(s.a, h[k], s.na * v[k]);
-      }
-      cut = flagged(a, row);
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t row = e * a.step_e + (t0 + u) * a.step_t;
+      xs[u] = gs[u] = make_uint4(0u, 0u, 0u, 0u);
+      ends[u] = false;
+      if (t0 + u >= len) continue;
+      const auto at = [&](const float* p, int64_t stride) {
+        return reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p) + (row * stride + c) * Stor<ST>::kBytes);
+      };
+      if (span_in_range(row * a.x_stride + c, VE, n * a.x_stride)) xs[u] = __ldg(at(a.x, a.x_stride));
+      if (span_in_range(row * a.gate_stride + c, VE, n * a.gate_stride)) gs[u] = __ldg(at(a.gate, a.gate_stride));
+      ends[u] = flagged(a, row);
     }
-    if (span_in_range(row * a.D + c, VE, n * a.D)) {
-      if constexpr (VE == 8) Stor<ST>::st8(a.h, row * a.D + c, v);
-      else Stor<ST>::st4(a.h, row * a.D + c, v);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = t0 + u;
+      if (t >= a.T) break;
+      const int64_t row = e * a.step_e + t * a.step_t;
+      float v[VE], g[VE];
+      widen(xs[u], v);
+      widen(gs[u], g);
+      if (t < len) {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          const Gate s = Sigma<ST>::of(g[k]);
+          h[k] = v[k] = cut ? s.na * v[k] : fmaf(s.a, h[k], s.na * v[k]);
+        }
+        cut = ends[u];
+      } else {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) v[k] = 0.f;
+      }
+      if (span_in_range(row * a.D + c, VE, n * a.D)) {
+        if constexpr (VE == 8) Stor<ST>::st8(a.h, row * a.D + c, v);
+        else Stor<ST>::st4(a.h, row * a.D + c, v);
+      }
     }
   }
   if (a.last == nullptr) return;
@@ -181,6 +206,91 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(GatedArgs a, i
   for (int k = 0; k < VE; k += 4)
     if (span_in_range(i + k, 4, a.E * a.D))
       *reinterpret_cast<float4*>(a.last + i + k) = cut ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+}
+
+template <class ST>
+__global__ void __launch_bounds__(kStepThreads) gated_grad_step_kernel(GatedArgs a, int64_t blocks) {
+  constexpr int VE = 16 / Stor<ST>::kBytes;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t e = blockIdx.x / blocks, c = ((blockIdx.x % blocks) * kStepThreads + threadIdx.x) * VE;
+  if (c >= a.D) return;
+  const int64_t n = a.E * a.T, i = e * a.D + c;
+  const int len = row_length(a, e);
+  const auto load = [&](const float* p, int64_t row, int64_t stride) {
+    if (!span_in_range(row * stride + c, VE, n * stride)) return make_uint4(0u, 0u, 0u, 0u);
+    return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p) + (row * stride + c) * Stor<ST>::kBytes));
+  };
+  const auto store = [&](float* p, int64_t row, int64_t stride, const float* v) {
+    if (!span_in_range(row * stride + c, VE, n * stride)) return;
+    if constexpr (VE == 8) Stor<ST>::st8(p, row * stride + c, v);
+    else Stor<ST>::st4(p, row * stride + c, v);
+  };
+  const auto states = [&](const float* p, float* v) {
+#pragma unroll
+    for (int k = 0; k < VE; k += 4) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p != nullptr && span_in_range(i + k, 4, a.E * a.D)) s = *reinterpret_cast<const float4*>(p + i + k);
+      v[k] = s.x, v[k + 1] = s.y, v[k + 2] = s.z, v[k + 3] = s.w;
+    }
+  };
+  float zero[VE], u[VE];
+#pragma unroll
+  for (int k = 0; k < VE; ++k) zero[k] = 0.f;
+  for (int64_t t = len; t < a.T; ++t) {
+    store(a.dx, e * a.step_e + t * a.step_t, a.dx_stride, zero);
+    store(a.dgate, e * a.step_e + t * a.step_t, a.dgate_stride, zero);
+  }
+  states(a.d_last, u);
+  if (len > 0 && flagged(a, e * a.step_e + (int64_t)(len - 1) * a.step_t)) {
+#pragma unroll
+    for (int k = 0; k < VE; ++k) u[k] = 0.f;
+  }
+  constexpr int kAhead = 2;  // steps whose loads are on their way together
+  for (int t1 = len - 1; t1 >= 0; t1 -= kAhead) {
+    uint4 xs[kAhead], gs[kAhead], ds[kAhead], hs[kAhead];
+    bool cut[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int t = t1 - q;
+      const int64_t row = e * a.step_e + t * a.step_t;
+      xs[q] = gs[q] = ds[q] = hs[q] = make_uint4(0u, 0u, 0u, 0u);
+      cut[q] = false;
+      if (t < 0) continue;
+      xs[q] = load(a.x, row, a.x_stride);
+      gs[q] = load(a.gate, row, a.gate_stride);
+      ds[q] = load(a.dh, row, a.dh_stride);
+      if (t > 0) {
+        hs[q] = load(a.in_h, row - a.step_t, a.h_stride);
+        cut[q] = flagged(a, row - a.step_t);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int t = t1 - q;
+      if (t < 0) break;
+      float x[VE], g[VE], d[VE], before[VE];
+      widen(xs[q], x);
+      widen(gs[q], g);
+      widen(ds[q], d);
+      widen(hs[q], before);
+      if (t == 0) states(a.state, before);
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        const Gate s = Sigma<ST>::of(g[k]);
+        const float G = d[k] + u[k], dx = s.na * G;
+        g[k] = s.a * dx * ((cut[q] ? 0.f : before[k]) - x[k]);
+        x[k] = dx;
+        u[k] = cut[q] ? 0.f : s.a * G;
+      }
+      store(a.dx, e * a.step_e + t * a.step_t, a.dx_stride, x);
+      store(a.dgate, e * a.step_e + t * a.step_t, a.dgate_stride, g);
+    }
+  }
+  if (a.d_state == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < VE; k += 4)
+    if (span_in_range(i + k, 4, a.E * a.D)) *reinterpret_cast<float4*>(a.d_state + i + k) = make_float4(u[k], u[k + 1], u[k + 2], u[k + 3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -840,19 +950,33 @@ cudaError_t run_tiles(const GatedArgs& a, const GatedMaps& maps, int sm, cudaStr
   return launch_tiles(kernel, units * share, 32 * H::W, smem, share, s, a, maps);
 }
 
-// a row takes the tile kernels from 5 steps on, if the grid can be launched
-bool by_tiles(const GatedArgs& a) { return a.T > 4 && a.E * div_up(a.D, kCols) <= INT32_MAX / kMaxShare; }
+// Whether rows of T steps are walked by threads of their own, step by step,
+// instead of by tiles: up to 8 steps, and up to 64 where the rows are many
+// times what fits the SMs as tile CTAs, each of which takes some 3 us to begin.
+// (us, steps / tiles, 2048 channels bfloat16: forward 16 rows of 8 steps 3.0 /
+// 3.8, of 16 4.7 / 3.1; 256 rows of 16 15 / 40, of 64 53 / 43.  Gradient: 64
+// rows of 16 19 / 31, of 32 36 / 33; 256 rows of 64 80 / 114.)
+bool by_steps(const GatedArgs& a, int64_t slots) {
+  const int64_t units = a.E * div_up(a.D, kCols);
+  return a.T <= 8 || (a.T <= 64 && a.T * slots <= 4 * units) || units > INT32_MAX / kMaxShare;
+}
+
+// In vectors where every row starts on a 16-byte boundary (`even`)
+cudaError_t launch_steps(void (*vectors)(GatedArgs, int64_t), void (*single)(GatedArgs), bool even, int es, const GatedArgs& a,
+                         int sm, cudaStream_t s) {
+  const int64_t blocks = div_up(a.D, kStepThreads * 16 / es);
+  if (even && a.E * blocks <= INT32_MAX) return launch_pdl(vectors, a.E * blocks, kStepThreads, 0, s, a, blocks);
+  return launch_serial(single, a, sm, s);
+}
 
 template <class ST>
 cudaError_t scan_typed(const GatedArgs& a, int sm, cudaStream_t s) {
   constexpr int es = Stor<ST>::kBytes, L = TileShape<ST, false, true>::C * TileShape<ST, false, true>::W;
-  if (!by_tiles(a)) {
-    const int64_t blocks = div_up(a.D, kStepThreads * 16 / es);
-    if (a.E * blocks <= INT32_MAX && rows_aligned({a.x, a.gate, a.h}, {a.D, a.x_stride, a.gate_stride}, es, 16) &&
-        rows_aligned({a.state, a.last}, {}, 4, 16))
-      return launch_pdl(gated_step_kernel<ST>, a.E * blocks, kStepThreads, 0, s, a, blocks);
-    return launch_serial(gated_serial_kernel<ST>, a, sm, s);
-  }
+  if (by_steps(a, (int64_t)TileShape<ST, false, true>::RES * sm))
+    return launch_steps(gated_step_kernel<ST>, gated_serial_kernel<ST>,
+                        rows_aligned({a.x, a.gate, a.h}, {a.D, a.x_stride, a.gate_stride}, es, 16) &&
+                            rows_aligned({a.state, a.last}, {}, 4, 16),
+                        es, a, sm, s);
   GatedMaps maps = {};
   const float* in[2] = {a.x, a.gate};
   const int64_t stride[2] = {a.x_stride, a.gate_stride};
@@ -864,8 +988,13 @@ cudaError_t scan_typed(const GatedArgs& a, int sm, cudaStream_t s) {
 
 template <class ST>
 cudaError_t grad_typed(const GatedArgs& a, int sm, cudaStream_t s) {
-  if (!by_tiles(a)) return launch_serial(gated_grad_serial_kernel<ST>, a, sm, s);
   constexpr int es = Stor<ST>::kBytes, L = TileShape<ST, true, true>::C * TileShape<ST, true, true>::W;
+  if (by_steps(a, (int64_t)TileShape<ST, true, true>::RES * sm))
+    return launch_steps(gated_grad_step_kernel<ST>, gated_grad_serial_kernel<ST>,
+                        rows_aligned({a.x, a.gate, a.dh, a.in_h, a.dx, a.dgate},
+                                     {a.D, a.x_stride, a.gate_stride, a.dh_stride, a.h_stride, a.dx_stride, a.dgate_stride}, es, 16) &&
+                            rows_aligned({a.state, a.d_last, a.d_state}, {}, 4, 16),
+                        es, a, sm, s);
   GatedMaps maps = {};
   const float* in[4] = {a.x, a.gate, a.dh, a.in_h};
   const int64_t stride[4] = {a.x_stride, a.gate_stride, a.dh_stride, a.h_stride};

@@ -70,13 +70,13 @@ struct Part {
   using Raw = std::conditional_t<kAligned, uint4, Apart>;
   using Raw8 = std::conditional_t<kAligned, std::conditional_t<VE == 8, uint2, uint32_t>, Apart8>;
   int lane;  // of the row
-  int64_t D;
+  int D;     // (rows that fit registers)
 
   // column of element k of part j, of a row shared by TPR threads
   template <int TPR>
-  __device__ int64_t col(int j, int k) const {
-    if constexpr (kAligned) return (int64_t)(lane + j * TPR) * VE + k;
-    return (int64_t)((lane >> 5) + j * (TPR / 32)) * kGroup + (lane & 31) + 32 * k;
+  __device__ int col(int j, int k) const {
+    if constexpr (kAligned) return lane * VE + j * TPR * VE + k;
+    return (lane >> 5) * kGroup + (lane & 31) + j * (TPR / 32) * kGroup + 32 * k;
   }
   template <int TPR>
   __device__ bool on(int j, int k) const {
@@ -143,7 +143,8 @@ struct Part {
   // the scale of part j's group
   template <int TPR>
   __device__ float scale8(const float* scale, int64_t row, int64_t N, int j) const {
-    const int64_t c = col<TPR>(j, 0), i = row * groups_of(D) + c / kGroup;
+    const int c = col<TPR>(j, 0);
+    const int64_t i = row * groups_of(D) + c / kGroup;
     return c / kGroup * kGroup < D && in_range(i, N * groups_of(D)) ? scale[i] : 0.f;
   }
   __device__ static void open8(const Raw8& r, float scale, float* v) {
@@ -166,7 +167,8 @@ struct Part {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
     const float sc = group_scale(m), inv = __frcp_rn(sc);
-    const int64_t c = col<TPR>(j, 0), groups = groups_of(D), n = N * D;
+    const int c = col<TPR>(j, 0);
+    const int64_t groups = groups_of(D), n = N * D;
     if (c % kGroup == 0 && c < D && in_range(row * groups + c / kGroup, N * groups)) scale[row * groups + c / kGroup] = sc;
     uint32_t w[VE / 2];
 #pragma unroll
@@ -187,12 +189,7 @@ struct Part {
 __host__ __device__ constexpr int cta_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
 // CTAs of `threads` threads an SM is to hold, by the values a thread has in registers
 __host__ __device__ constexpr int rms_resident(int threads, int values) {
-  #ifndef R32
-#define R32 512
-#define R16 768
-#define R8 1024
-#endif
-  const int n = (values >= 32 ? R32 : values >= 16 ? R16 : R8) / threads;
+    const int n = (values >= 32 ? 512 : values >= 16 ? 768 : 1024) / threads;
   return n > 0 ? n : 1;
 }
 
@@ -206,7 +203,7 @@ __device__ __forceinline__ float row_sum(float v, float (*scratch)[32], int slot
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) scratch[slot][warp] = v;
     __syncthreads();
-    v = warp_sum(lane < W ? scratch[slot][lane] : 0.f);
+    v = warp_sum(lane < W ? scratch[slot][warp / W * W + lane] : 0.f);
   }
   return v;
 }
@@ -217,7 +214,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), rms_resident(cta_threads(TPR
   using P = Part<ST, kAligned>;
   constexpr int ROWS = cta_threads(TPR) / TPR, VE = P::VE;
   __shared__ float scratch[2][32];
-  const P part{(int)(threadIdx.x % TPR), a.D};
+  const P part{(int)(threadIdx.x % TPR), (int)a.D};
   const float inv_d = 1.f / (float)a.D;
   const int64_t step = (int64_t)gridDim.x * ROWS, nd = a.N * a.D;
   const int64_t x_size = extent(a.N, a.D, a.x_stride), r_size = extent(a.N, a.D, a.residual_stride);
@@ -350,17 +347,21 @@ __global__ void __launch_bounds__(kLongThreads) rms_long_kernel(RmsArgs a) {
 // joins in order.
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int rms_grad_resident(int threads, int values) {
-  const int n = (values >= 32 ? 384 : values >= 16 ? 512 : 640) / threads;
+  const int n = (values >= 32 ? 384 : 512) / threads;
   return n > 0 ? n : 1;
 }
+// (rows of a CTA beside each other leave one set of sums: 5001 x 1001 float32
+// with 128 threads 19.4 us, 256 15.9 us, 512 15.1 us, but 20000 x 2001 bfloat16
+// 73, 73 and 78 us)
+__host__ __device__ constexpr int grad_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 
 template <class ST, bool kAligned, bool k8, int VPT, int TPR>
-__global__ void __launch_bounds__(cta_threads(TPR), rms_grad_resident(cta_threads(TPR), VPT * Part<ST, kAligned>::VE))
+__global__ void __launch_bounds__(grad_threads(TPR), rms_grad_resident(grad_threads(TPR), VPT * Part<ST, kAligned>::VE))
     rms_grad_kernel(RmsGradArgs a) {
   using P = Part<ST, kAligned>;
-  constexpr int T = cta_threads(TPR), ROWS = T / TPR, VE = P::VE;
+  constexpr int T = grad_threads(TPR), ROWS = T / TPR, VE = P::VE;
   __shared__ float scratch[2][32];
-  const P part{(int)(threadIdx.x % TPR), a.D};
+  const P part{(int)(threadIdx.x % TPR), (int)a.D};
   const float inv_d = 1.f / (float)a.D;
   const int64_t step = (int64_t)gridDim.x * ROWS, nd = a.N * a.D;
   const int64_t dy_size = extent(a.N, a.D, a.dy_stride), dt_size = extent(a.N, a.D, a.d_total_stride),
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), rms_grad_resident(cta_thread
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
           for (int k = 0; k < VE; ++k) {
-            const int c = (int)part.template col<TPR>(j, k);
+            const int c = part.template col<TPR>(j, k);
             if (in_range(c, VPT * TPR * VE)) acc[c] = dw[j][k] + (q > 0 ? acc[c] : 0.f);
           }
       }
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(TPR, rms_grad_resident(TPR, VPT * Part<ST, tru
   extern __shared__ __align__(128) unsigned char ring_rows[];  // [kRows][dy, total, d_total]
   __shared__ __align__(8) uint64_t full[kRows];
   __shared__ float scratch[2][32];
-  const P part{(int)threadIdx.x, a.D};
+  const P part{(int)threadIdx.x, (int)a.D};
   const uint32_t row_bytes = (uint32_t)(a.D * Stor<ST>::kBytes), t_bytes = k8 ? (uint32_t)a.D : row_bytes;
   const bool has_dt = a.d_total != nullptr && a.dx != nullptr;
   const uint32_t stage_bytes = row_bytes + t_bytes + (has_dt ? row_bytes : 0);
@@ -694,11 +695,7 @@ cudaError_t rms_width(const RmsArgs& a, int64_t parts, int sm, cudaStream_t s) {
   if (parts <= 64) return launch_rms<ST, kAligned, 2, 32>(a, sm, s);
   if (parts <= 128) return launch_rms<ST, kAligned, 4, 32>(a, sm, s);
   if (parts <= 256) return launch_rms<ST, kAligned, 2, 128>(a, sm, s);
-#ifndef RV
-#define RV 2
-#define RT 256
-#endif
-  if (parts <= 512) return launch_rms<ST, kAligned, RV, RT>(a, sm, s);
+  if (parts <= 512) return launch_rms<ST, kAligned, 2, 256>(a, sm, s);
   if (parts <= 1024) return launch_rms<ST, kAligned, 2, 512>(a, sm, s);
   return launch_rms<ST, kAligned, 4, 512>(a, sm, s);
 }
@@ -723,7 +720,7 @@ int64_t grad_grid(int64_t N, int T, int R, int values, int sm) {
 
 template <class ST, bool kAligned, bool k8, int VPT, int TPR>
 cudaError_t launch_grad(const RmsGradArgs& a, int sm, cudaStream_t s) {
-  constexpr int T = cta_threads(TPR);
+  constexpr int T = grad_threads(TPR);
   const int64_t grid = grad_grid(a.N, T, T / TPR, VPT * Part<ST, kAligned>::VE, sm);
   const cudaError_t e = launch_pdl(rms_grad_kernel<ST, kAligned, k8, VPT, TPR>, grid, T, 0, s, a);
   return e == cudaSuccess ? join(a, grid, s) : e;
