@@ -448,42 +448,35 @@ struct TileRows {
   __device__ static uint32_t pitch(int64_t step) { return kBulk ? kRow : kLeast + (((uint32_t)step - kLeast) & 15); }
 };
 
-// The rows of steps t0[k] .. t0[k] + L - 1 in front of `len` of the arrays p[k] into their tiles: a copy a row, from the
-// boundary in front of it to the one behind its last column, each thread some of the rows.
-template <class ST, int N, int L, int THREADS>
-__device__ __forceinline__ void copy_rows(unsigned char* tiles, const float* const* p, const int64_t* stride, const int* t0,
-                                          const GatedArgs& a, int64_t e, int len, int64_t c0, uint64_t* bar) {
+// A thread's share of copying tiles row by row: one row of one array, at the
+// same place behind its boundary in every tile.
+template <class ST, int L>
+struct RowCopy {
   using R = TileRows<ST, false, L>;
-  static_assert(THREADS % L == 0 || L % THREADS == 0, "a thread's rows lie in whole steps of threads");
-  const uint32_t width = (uint32_t)min((int64_t)kCols, a.D - c0) * R::kBytes;
-  constexpr int kMine = (N * L + THREADS - 1) / THREADS;
-  uint32_t bytes = 0, to[kMine], size[kMine];
-  uintptr_t at[kMine];
-#pragma unroll
-  for (int m = 0; m < kMine; ++m) {
-    const int i = threadIdx.x + m * THREADS, k = i / L, r = i % L;
-    size[m] = to[m] = 0;
-    at[m] = 0;
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      if (q != k) continue;
-      const int t = t0[q] + r;
-      const int64_t row = (e * a.step_e + t * a.step_t) * stride[q] + c0;
-      if (t < 0 || t >= len || !span_in_range(row, width / R::kBytes, a.E * a.T * stride[q])) continue;
-      at[m] = (uintptr_t)p[q] + row * R::kBytes;
-      size[m] = ((uint32_t)(at[m] & 15) + width + 15) & ~15u;
-      const uint32_t first = (uint32_t)((uintptr_t)p[q] + ((e * a.step_e + t0[q] * a.step_t) * stride[q] + c0) * R::kBytes) & 15;
-      to[m] = q * R::kTile + first + r * R::pitch(a.step_t * stride[q] * R::kBytes);
-    }
-    bytes += size[m];
+  uintptr_t at = 0;   // the row in the next tile, from the boundary in front of it
+  int64_t move = 0;   // bytes and steps from tile to tile
+  int step = 0, t = -1;
+  uint32_t to = 0, size = 0;
+  // row r of array k, step t of the matrix in the first tile copied; `tile` is that tile's first
+  __device__ void start(const GatedArgs& a, int k, int r, const float* p, int64_t stride, int64_t e, int64_t c0, int tile, int tiles) {
+    const uint32_t width = (uint32_t)min((int64_t)kCols, a.D - c0) * R::kBytes;
+    const uintptr_t first = (uintptr_t)p + ((e * a.step_e + tile * a.step_t) * stride + c0) * R::kBytes;
+    const int64_t bytes = a.step_t * stride * R::kBytes;
+    at = first + r * bytes;
+    size = ((uint32_t)(at & 15) + width + 15) & ~15u;
+    to = (k * R::kTile + (uint32_t)(first & 15) + r * R::pitch(bytes)) & ~15u;
+    at &= ~(uintptr_t)15;
+    t = tile + r, step = tiles * L, move = step * bytes;
+    if (!span_in_range(to, size, (k + 1) * R::kTile)) size = 0;
   }
-  mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-  for (int m = 0; m < kMine; ++m) {
-    if (size[m] != 0 && span_in_range(to[m] & ~15u, size[m], N * R::kTile))
-      bulk_load(tiles + (to[m] & ~15u), reinterpret_cast<const void*>(at[m] & ~(uintptr_t)15), size[m], bar);
+  __device__ __forceinline__ void next(unsigned char* stage, int len, uint64_t* bar) {
+    const uint32_t bytes = t >= 0 && t < len ? size : 0;
+    mbar_arrive_expect_tx(bar, bytes);
+    if (bytes != 0) bulk_load(stage + to, reinterpret_cast<const void*>(at), bytes, bar);
+    t += step;
+    at += move;
   }
-}
+};
 
 // A lane's two channels of the warp's steps of a tile.  Tiles are whole multiples of 16 bytes in steps of any matrix, so a
 // step lies at the same place in all of them.
@@ -569,21 +562,21 @@ __device__ __forceinline__ bool cut_before(const GatedArgs& a, int64_t e, int t,
 
 // What the CTAs of a row have in shared memory beside the ring, and how their
 // maps meet.
-template <int W, int STAGES>
+template <int W, int STAGES, bool kShared>
 struct GatedShared {
   Map2 warp_map[2][W][32];
-  Map2 cta_map[2][kMaxShare][32];
+  Map2 cta_map[2][kShared ? kMaxShare : 1][32];
   uint64_t full[STAGES], maps[2];
 };
 
 // The carry in front of this warp's steps (returned) and behind the round's
 // (*carry).  Buffers alternate: a peer sends its map of round k + 2 only when it
 // has this CTA's of round k + 1, which leaves behind the reads of round k.
-template <int W, int STAGES, bool kForward>
-__device__ __forceinline__ V2 meet(GatedShared<W, STAGES>& sh, int round, int rank, int share, bool any_cut, bool* ok, V2* carry) {
+template <int W, int STAGES, bool kShared, bool kForward>
+__device__ __forceinline__ V2 meet(GatedShared<W, STAGES, kShared>& sh, int round, int rank, int share, bool any_cut, bool* ok, V2* carry) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, buf = round & 1;
   V2 at = *carry;
-  if (share == 1) {
+  if constexpr (!kShared) {
     fold<W, kForward>(sh.warp_map[buf], lane, warp, any_cut, carry, &at);
     return at;
   }
@@ -608,14 +601,14 @@ __device__ __forceinline__ V2 meet(GatedShared<W, STAGES>& sh, int round, int ra
   return at;
 }
 
-template <class ST, int C, int W, int STAGES, bool kBulk, int kResident>
+template <class ST, int C, int W, int STAGES, bool kBulk, bool kShared, int kResident>
 __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs a, const __grid_constant__ GatedMaps maps, int share) {
   using R = TileRows<ST, kBulk, C * W>;
   constexpr int L = C * W, kArrays = 2;
   extern __shared__ __align__(128) unsigned char ring_tiles[];  // [STAGES][x, gate]
-  __shared__ __align__(16) GatedShared<W, STAGES> sh;
+  __shared__ __align__(16) GatedShared<W, STAGES, kShared> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = share > 1 ? blockIdx.x % share : 0;
+  const int rank = kShared ? blockIdx.x % share : 0;
   const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / share, e = unit / blocks;
   const Cols<ST, kBulk> cols{(unit % blocks) * kCols, lane, a.D};
   pdl_trigger();
@@ -625,27 +618,31 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
     mbar_init(&sh.maps[1], 1);
     mbar_fence_init();
   }
-  if (share > 1) cluster_meet();  // (a peer's memory is written only once it runs)
+  if constexpr (kShared) cluster_meet();  // (a peer's memory is written only once it runs)
   else __syncthreads();
   pdl_wait();
 
   const int len = row_length(a, e);
   const int ntiles = (len + L - 1) / L, rounds = (ntiles + share - 1) / share;
   const int mine = ntiles > rank ? (ntiles - rank + share - 1) / share : 0;
+  RowCopy<ST, L> copy;
+  if constexpr (!kBulk) {
+    static_assert(kArrays * L <= 32 * W, "a row a thread");
+    const int k = threadIdx.x / L;
+    if (k < kArrays)
+      copy.start(a, k, threadIdx.x % L, k == 0 ? a.x : a.gate, k == 0 ? a.x_stride : a.gate_stride, e, cols.c0, rank * L, share);
+  }
   const auto fill = [&](int stage, int j) {
     if (!in_range(stage, STAGES)) return;
     unsigned char* to = ring_tiles + (size_t)stage * kArrays * R::kTile;
-    const int t = (rank + j * share) * L;
     if constexpr (kBulk) {
       if (threadIdx.x != 0) return;
+      const int t = (rank + j * share) * L;
       mbar_arrive_expect_tx(&sh.full[stage], kArrays * R::kTile);
       tile_load(to, &maps.in[0], (int)cols.c0, t, (int)e, &sh.full[stage]);
       tile_load(to + R::kTile, &maps.in[1], (int)cols.c0, t, (int)e, &sh.full[stage]);
     } else {
-      const float* const from[kArrays] = {a.x, a.gate};
-      const int64_t stride[kArrays] = {a.x_stride, a.gate_stride};
-      const int at[kArrays] = {t, t};
-      copy_rows<ST, kArrays, L, 32 * W>(to, from, stride, at, a, e, len, cols.c0, &sh.full[stage]);
+      copy.next(to, len, &sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
@@ -699,7 +696,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
     }
     sh.warp_map[k & 1][warp][lane] = m;
     const bool any_cut = __syncthreads_or(cut != 0);
-    const V2 h = meet<W, STAGES, true>(sh, k, rank, share, any_cut, &met, &carry);
+    const V2 h = meet<W, STAGES, kShared, true>(sh, k, rank, share, any_cut, &met, &carry);
     out.start();
     if (k < mine && real == C && cut == 0) {
 #pragma unroll
@@ -724,17 +721,17 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   // (copies still on their way after a wait gave up land before the CTA ends)
   if (!ring.ok && (threadIdx.x == 0 || !kBulk))
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
-  if (share > 1) cluster_meet();  // no CTA ends while a peer may still write to it
+  if constexpr (kShared) cluster_meet();  // no CTA ends while a peer may still write to it
 }
 
-template <class ST, int C, int W, int STAGES, bool kBulk, int kResident>
+template <class ST, int C, int W, int STAGES, bool kBulk, bool kShared, int kResident>
 __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(GatedArgs a, const __grid_constant__ GatedMaps maps, int share) {
   using R = TileRows<ST, kBulk, C * W>;
   constexpr int L = C * W, kArrays = 4;
   extern __shared__ __align__(128) unsigned char ring_tiles[];  // [STAGES][x, gate, dh, h one step earlier]
-  __shared__ __align__(16) GatedShared<W, STAGES> sh;
+  __shared__ __align__(16) GatedShared<W, STAGES, kShared> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = share > 1 ? blockIdx.x % share : 0;
+  const int rank = kShared ? blockIdx.x % share : 0;
   const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / share, e = unit / blocks;
   const Cols<ST, kBulk> cols{(unit % blocks) * kCols, lane, a.D};
   pdl_trigger();
@@ -744,7 +741,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
     mbar_init(&sh.maps[1], 1);
     mbar_fence_init();
   }
-  if (share > 1) cluster_meet();
+  if constexpr (kShared) cluster_meet();
   else __syncthreads();
   pdl_wait();
 
@@ -752,21 +749,28 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   const int ntiles = (len + L - 1) / L, rounds = (ntiles + share - 1) / share;
   const int mine = ntiles > rank ? (ntiles - rank + share - 1) / share : 0;
   // the row's last tile first
+  const int last_tile = (rank + (mine - 1) * share) * L;
+  RowCopy<ST, L> copy;
+  if constexpr (!kBulk) {
+    static_assert(kArrays * L <= 32 * W, "a row a thread");
+    const int k = threadIdx.x / L;
+    const float* const p = k == 0 ? a.x : k == 1 ? a.gate : k == 2 ? a.dh : a.in_h;
+    const int64_t stride = k == 0 ? a.x_stride : k == 1 ? a.gate_stride : k == 2 ? a.dh_stride : a.h_stride;
+    if (mine > 0 && k < kArrays)
+      copy.start(a, k, threadIdx.x % L, p, stride, e, cols.c0, k == 3 ? last_tile - 1 : last_tile, -share);
+  }
   const auto fill = [&](int stage, int j) {
     if (!in_range(stage, STAGES)) return;
     unsigned char* to = ring_tiles + (size_t)stage * kArrays * R::kTile;
-    const int t = (rank + (mine - 1 - j) * share) * L;
     if constexpr (kBulk) {
       if (threadIdx.x != 0) return;
+      const int t = last_tile - j * share * L;
       mbar_arrive_expect_tx(&sh.full[stage], kArrays * R::kTile);
 #pragma unroll
       for (int i = 0; i < kArrays; ++i)
         tile_load(to + i * R::kTile, &maps.in[i], (int)cols.c0, i == 3 ? t - 1 : t, (int)e, &sh.full[stage]);
     } else {
-      const float* const from[kArrays] = {a.x, a.gate, a.dh, a.in_h};
-      const int64_t stride[kArrays] = {a.x_stride, a.gate_stride, a.dh_stride, a.h_stride};
-      const int at[kArrays] = {t, t, t, t - 1};
-      copy_rows<ST, kArrays, L, 32 * W>(to, from, stride, at, a, e, len, cols.c0, &sh.full[stage]);
+      copy.next(to, len, &sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
@@ -844,7 +848,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
     }
     sh.warp_map[(rounds - 1 - k) & 1][warp][lane] = m;
     const bool any_cut = __syncthreads_or(cut != 0);
-    const V2 u = meet<W, STAGES, false>(sh, rounds - 1 - k, rank, share, any_cut, &met, &carry);
+    const V2 u = meet<W, STAGES, kShared, false>(sh, rounds - 1 - k, rank, share, any_cut, &met, &carry);
     to_x.start(), to_gate.start();
     if (k < mine && real == C && cut == 0) {
 #pragma unroll
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   if (rank == 0 && warp == 0 && a.d_state != nullptr) cols.store_state(a.d_state, e, a.E, carry);
   if (!ring.ok && (threadIdx.x == 0 || !kBulk))
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
-  if (share > 1) cluster_meet();
+  if constexpr (kShared) cluster_meet();
 }
 
 template <class K>
@@ -933,21 +937,26 @@ int row_share(int64_t units, int64_t ntiles, int64_t slots) {
   return share;
 }
 
-template <class ST, bool kBack, bool kBulk>
-cudaError_t run_tiles(const GatedArgs& a, const GatedMaps& maps, int sm, cudaStream_t s) {
+template <class ST, bool kBack, bool kBulk, bool kShared>
+cudaError_t launch_shape(const GatedArgs& a, const GatedMaps& maps, int share, cudaStream_t s) {
   using H = TileShape<ST, kBack, kBulk>;
   constexpr int L = H::C * H::W;
   constexpr size_t smem = (size_t)H::STAGES * (kBack ? 4 : 2) * TileRows<ST, kBulk, L>::kTile;
-  static_assert(H::RES * (smem + sizeof(GatedShared<H::W, H::STAGES>) + 1024) <= 228 * 1024, "RES CTAs fit an SM");
+  static_assert(H::RES * (smem + sizeof(GatedShared<H::W, H::STAGES, kShared>) + 1024) <= 228 * 1024, "RES CTAs fit an SM");
   void (*kernel)(GatedArgs, GatedMaps, int);
-  if constexpr (kBack) kernel = gated_grad_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, H::RES>;
-  else kernel = gated_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, H::RES>;
+  if constexpr (kBack) kernel = gated_grad_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, kShared, H::RES>;
+  else kernel = gated_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, kShared, H::RES>;
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return e;
-  const int64_t units = a.E * div_up(a.D, kCols);
-  const int share = row_share(units, div_up(a.T, L), (int64_t)H::RES * sm);
-  return launch_tiles(kernel, units * share, 32 * H::W, smem, share, s, a, maps);
+  return launch_tiles(kernel, a.E * div_up(a.D, kCols) * share, 32 * H::W, smem, share, s, a, maps);
+}
+
+template <class ST, bool kBack, bool kBulk>
+cudaError_t run_tiles(const GatedArgs& a, const GatedMaps& maps, int sm, cudaStream_t s) {
+  using H = TileShape<ST, kBack, kBulk>;
+  const int share = row_share(a.E * div_up(a.D, kCols), div_up(a.T, H::C * H::W), (int64_t)H::RES * sm);
+  return share > 1 ? launch_shape<ST, kBack, kBulk, true>(a, maps, share, s) : launch_shape<ST, kBack, kBulk, false>(a, maps, 1, s);
 }
 
 // Whether rows of T steps are walked by threads of their own, step by step,
