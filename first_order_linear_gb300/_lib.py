@@ -44,6 +44,8 @@ RLCA_EST_TOKEN_LOGPROB_BACKWARD = 11
 RLCA_EST_LAYER_NORM_BACKWARD = 12
 RLCA_EST_CLIP_GRADS = 13
 RLCA_EST_RMS_NORM_BACKWARD = 14
+RLCA_EST_GATED_SCAN = 15
+RLCA_EST_GATED_SCAN_BACKWARD = 16
 
 RLCA_F32 = 0
 RLCA_I32 = 1
@@ -89,8 +91,8 @@ SIGNATURES = {
     "rlca_clip_grads": (_i, [_p, _p, _p, _p, _i64, _f, _f, _p, _p, _sz, _p]),
     "rlca_rms_norm": (_i, [_p] * 10 + [_i64, _i64, _i64, _i64, _f, _u32, _p]),
     "rlca_rms_norm_backward": (_i, [_p] * 9 + [_i64] * 5 + [_u32, _p, _sz, _p]),
-    "rlca_gated_scan": (_i, [_p] * 8 + [_i64] * 5 + [_u32, _p]),
-    "rlca_gated_scan_backward": (_i, [_p] * 12 + [_i64] * 9 + [_u32, _p]),
+    "rlca_gated_scan": (_i, [_p] * 8 + [_i64] * 5 + [_u32, _p, _sz, _p]),
+    "rlca_gated_scan_backward": (_i, [_p] * 12 + [_i64] * 9 + [_u32, _p, _sz, _p]),
 }
 
 

@@ -379,13 +379,15 @@ struct Two<bf16> {
   }
 };
 
-// two channels' maps of a run of steps: h -> q + p h, a severed one marked by
-// p = -0 in both (products of gates are not negative)
+// two channels' maps of a run of steps: h -> q + p h.  A severed one, of a run
+// with a flagged step, is marked by a NaN in both p that no arithmetic gives (its
+// results are 0x7fffffff).
 struct Map2 {
   V2 p, q;
 };
+constexpr V2 kSevered = ~V2(0);
 __device__ __forceinline__ Map2 identity() { return {v2(1.f, 1.f), 0}; }
-__device__ __forceinline__ bool severed(const Map2& m) { return (uint32_t)m.p == 0x80000000u; }
+__device__ __forceinline__ bool severed(const Map2& m) { return (uint32_t)m.p == (uint32_t)kSevered; }
 __device__ __forceinline__ V2 pass(const Map2& m, V2 h) { return severed(m) ? m.q : fma2(m.p, h, m.q); }
 // `then` behind `first`
 __device__ __forceinline__ Map2 chain(const Map2& then, const Map2& first) {
@@ -601,6 +603,124 @@ __device__ __forceinline__ V2 meet(GatedShared<W, STAGES, kShared>& sh, int roun
   return at;
 }
 
+// Rows too few even for clusters are cut into segments: a first launch leaves
+// every segment's map, and a segment's CTA starts from the value that the maps in
+// front of its steps (behind them, backward) give.
+__device__ __forceinline__ int64_t segment_at(const GatedArgs& a, int64_t unit, int segment) {
+  return (unit * a.nseg + segment) * 32 + (threadIdx.x & 31);
+}
+__device__ __forceinline__ int64_t segment_maps(const GatedArgs& a) { return a.E * ((a.D + kCols - 1) / kCols) * a.nseg * 32; }
+__device__ __forceinline__ Map2 segment_map(const GatedArgs& a, int64_t unit, int segment) {
+  const int64_t i = segment_at(a, unit, segment);
+  return in_range(i, segment_maps(a)) ? static_cast<const Map2*>(a.ws)[i] : identity();
+}
+
+// ... through `count` maps from `first` on, one after or in front of the other (eight loads in flight)
+template <bool kForward>
+__device__ __forceinline__ V2 through_segments(const GatedArgs& a, int64_t unit, int first, int count, V2 carry) {
+  constexpr int B = 8;
+  for (int q = 0; q < count; q += B) {
+    Map2 m[B];
+#pragma unroll
+    for (int u = 0; u < B; ++u) m[u] = q + u < count ? segment_map(a, unit, kForward ? first + q + u : first - q - u) : identity();
+#pragma unroll
+    for (int u = 0; u < B; ++u) carry = pass(m[u], carry);
+  }
+  return carry;
+}
+
+template <class ST, int C, int W, int STAGES, bool kBulk, bool kBack, int kResident>
+__global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs a, const __grid_constant__ GatedMaps maps, int) {
+  using R = TileRows<ST, kBulk, C * W>;
+  constexpr int L = C * W, kArrays = 2;
+  extern __shared__ __align__(128) unsigned char ring_tiles[];  // [STAGES][x (dh), gate]
+  __shared__ __align__(16) GatedShared<W, STAGES, false> sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / a.nseg, e = unit / blocks;
+  const int part = blockIdx.x % a.nseg;
+  const Cols<ST, kBulk> cols{(unit % blocks) * kCols, lane, a.D};
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], kBulk ? 1 : 32 * W);
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  const int begin = part * a.seg_len, len = row_length(a, e), lim = (int)min((int64_t)len, (int64_t)begin + a.seg_len);
+  const int ntiles = (max(lim - begin, 0) + L - 1) / L;
+  const float* const p = kBack ? a.dh : a.x;
+  const int64_t stride = kBack ? a.dh_stride : a.x_stride;
+  // in the order of the steps, or the last tile first
+  const int first = kBack ? begin + (ntiles - 1) * L : begin, turn = kBack ? -L : L;
+  RowCopy<ST, L> copy;
+  if constexpr (!kBulk) {
+    static_assert(kArrays * L <= 32 * W, "a row a thread");
+    const int k = threadIdx.x / L;
+    if (ntiles > 0 && k < kArrays)
+      copy.start(a, k, threadIdx.x % L, k == 0 ? p : a.gate, k == 0 ? stride : a.gate_stride, e, cols.c0, first, kBack ? -1 : 1);
+  }
+  const auto fill = [&](int stage, int j) {
+    if (!in_range(stage, STAGES)) return;
+    unsigned char* to = ring_tiles + (size_t)stage * kArrays * R::kTile;
+    if constexpr (kBulk) {
+      if (threadIdx.x != 0) return;
+      mbar_arrive_expect_tx(&sh.full[stage], kArrays * R::kTile);
+      tile_load(to, &maps.in[kBack ? 2 : 0], (int)cols.c0, first + j * turn, (int)e, &sh.full[stage]);
+      tile_load(to + R::kTile, &maps.in[1], (int)cols.c0, first + j * turn, (int)e, &sh.full[stage]);
+    } else {
+      copy.next(to, len, &sh.full[stage]);
+    }
+  };
+  for (int j = 0; j < STAGES - 1 && j < ntiles; ++j) fill(j, j);
+  FillRing<STAGES> ring;
+  const int64_t tile0 = e * a.step_e + (int64_t)begin * a.step_t;
+  const Reader<ST, kBulk, L> xs(a, 0, warp * C, lane, p, tile0, stride, cols.c0);
+  const Reader<ST, kBulk, L> gs(a, 1, warp * C, lane, a.gate, tile0, a.gate_stride, cols.c0);
+  const bool flags = a.terminated != nullptr || a.truncated != nullptr;
+  int t0 = first + warp * C;
+  bool cut_next = flags && lane < C && cut_before(a, e, t0 + lane, len);
+  Map2 all = identity();
+  for (int j = 0; j < ntiles; ++j, t0 += turn) {
+    const int real = min(max(lim - t0, 0), C);
+    uint32_t cut = 0;
+    if (flags) {
+      cut = __ballot_sync(kFullMask, cut_next);
+      if (lane < C) cut_next = cut_before(a, e, t0 + turn + lane, len);
+    }
+    if (ring.ok && j + STAGES - 1 < ntiles) fill(ring.fill_stage(), j + STAGES - 1);
+    if (ring.ok) ring.ok = mbar_wait_bounded(&sh.full[ring.stage], ring.phase);
+    const unsigned char* tile = ring_tiles + (size_t)ring.stage * kArrays * R::kTile;
+    ring.next();
+    Map2 m = identity();
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const int i = kBack ? C - 1 - q : q;
+      if (i >= real) continue;
+      V2 s, ns;
+      gs.get(tile, i).sigma(&s, &ns);
+      const V2 v = xs.get(tile, i).wide();
+      const bool here = (cut >> i) & 1;
+      if constexpr (kBack) {
+        if (here) m = {kSevered, 0};
+        else m = {severed(m) ? m.p : mul2(m.p, s), mul2(s, add2(v, m.q))};
+      } else {
+        if (here) m = {kSevered, mul2(ns, v)};
+        else m = chain({s, mul2(ns, v)}, m);
+      }
+    }
+    sh.warp_map[j & 1][warp][lane] = m;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) all = chain(sh.warp_map[j & 1][kBack ? W - 1 - k : k][lane], all);
+    }
+  }
+  if (warp == 0 && in_range(segment_at(a, unit, part), segment_maps(a))) static_cast<Map2*>(a.ws)[segment_at(a, unit, part)] = all;
+  // (copies still on their way after a wait gave up land before the CTA ends)
+  if (!ring.ok && (threadIdx.x == 0 || !kBulk))
+    for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
+}
+
 template <class ST, int C, int W, int STAGES, bool kBulk, bool kShared, int kResident>
 __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs a, const __grid_constant__ GatedMaps maps, int share) {
   using R = TileRows<ST, kBulk, C * W>;
@@ -608,8 +728,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   extern __shared__ __align__(128) unsigned char ring_tiles[];  // [STAGES][x, gate]
   __shared__ __align__(16) GatedShared<W, STAGES, kShared> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = kShared ? blockIdx.x % share : 0;
-  const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / share, e = unit / blocks;
+  const int parts = kShared ? share : a.nseg, part = blockIdx.x % parts, rank = kShared ? part : 0;
+  const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / parts, e = unit / blocks;
+  // a row's steps, or a segment's
+  const int begin = kShared ? 0 : part * a.seg_len, stop = kShared ? (int)a.T : (int)min(a.T, (int64_t)begin + a.seg_len);
   const Cols<ST, kBulk> cols{(unit % blocks) * kCols, lane, a.D};
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -622,22 +744,23 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   else __syncthreads();
   pdl_wait();
 
-  const int len = row_length(a, e);
-  const int ntiles = (len + L - 1) / L, rounds = (ntiles + share - 1) / share;
+  const int len = row_length(a, e), lim = min(len, stop);
+  const int ntiles = (max(lim - begin, 0) + L - 1) / L, rounds = (ntiles + share - 1) / share;
   const int mine = ntiles > rank ? (ntiles - rank + share - 1) / share : 0;
   RowCopy<ST, L> copy;
   if constexpr (!kBulk) {
     static_assert(kArrays * L <= 32 * W, "a row a thread");
     const int k = threadIdx.x / L;
     if (k < kArrays)
-      copy.start(a, k, threadIdx.x % L, k == 0 ? a.x : a.gate, k == 0 ? a.x_stride : a.gate_stride, e, cols.c0, rank * L, share);
+      copy.start(a, k, threadIdx.x % L, k == 0 ? a.x : a.gate, k == 0 ? a.x_stride : a.gate_stride, e, cols.c0,
+                 begin + rank * L, share);
   }
   const auto fill = [&](int stage, int j) {
     if (!in_range(stage, STAGES)) return;
     unsigned char* to = ring_tiles + (size_t)stage * kArrays * R::kTile;
     if constexpr (kBulk) {
       if (threadIdx.x != 0) return;
-      const int t = (rank + j * share) * L;
+      const int t = begin + (rank + j * share) * L;
       mbar_arrive_expect_tx(&sh.full[stage], kArrays * R::kTile);
       tile_load(to, &maps.in[0], (int)cols.c0, t, (int)e, &sh.full[stage]);
       tile_load(to + R::kTile, &maps.in[1], (int)cols.c0, t, (int)e, &sh.full[stage]);
@@ -648,17 +771,18 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
 
   V2 carry = cols.state(a.state, e, a.E);
+  if constexpr (!kShared) carry = through_segments<true>(a, unit, 0, part, carry);
   FillRing<STAGES> ring;
   bool met = true;
-  int t0 = rank * L + warp * C;  // the warp's first step of the round
-  const int64_t row0 = e * a.step_e + t0 * a.step_t, tile0 = e * a.step_e + (int64_t)rank * L * a.step_t;
+  int t0 = begin + rank * L + warp * C;  // the warp's first step of the round
+  const int64_t row0 = e * a.step_e + t0 * a.step_t, tile0 = e * a.step_e + (int64_t)(begin + rank * L) * a.step_t;
   const Reader<ST, kBulk, L> xs(a, 0, warp * C, lane, a.x, tile0, a.x_stride, cols.c0);
   const Reader<ST, kBulk, L> gs(a, 1, warp * C, lane, a.gate, tile0, a.gate_stride, cols.c0);
   Writer<ST, kBulk> out(cols, a, a.h, a.D, row0);
   const bool flags = a.terminated != nullptr || a.truncated != nullptr;
   bool cut_next = flags && lane < C && cut_before(a, e, t0 + lane, len);
   for (int k = 0; k < rounds; ++k, t0 += share * L) {
-    const int real = min(max(len - t0, 0), C);
+    const int real = min(max(lim - t0, 0), C);
     uint32_t cut = 0;
     if (flags) {
       cut = __ballot_sync(kFullMask, cut_next);
@@ -686,7 +810,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
             V2 s, ns;
             gs.get(tile, i).sigma(&s, &ns);
             const V2 b = mul2(ns, xs.get(tile, i).wide());
-            if ((cut >> i) & 1) m = {0x8000000080000000ull, b};
+            if ((cut >> i) & 1) m = {kSevered, b};
             else m = chain({s, b}, m);
           }
           q[i] = m.q;
@@ -704,17 +828,17 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
     } else {
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (t0 + i < a.T) out.put(k < mine && i < real ? pass({p[i], q[i]}, h) : 0);
+        if (t0 + i < stop) out.put(k < mine && i < real ? pass({p[i], q[i]}, h) : 0);
     }
     out.move(share * L);
   }
   // behind the row's last tile
-  for (; t0 < a.T; t0 += share * L) {
+  for (; t0 < stop; t0 += share * L) {
     out.start();
-    for (int i = 0; i < C && t0 + i < a.T; ++i) out.put(0);
+    for (int i = 0; i < C && t0 + i < stop; ++i) out.put(0);
     out.move(share * L);
   }
-  if (rank == 0 && warp == 0 && a.last != nullptr) {
+  if (warp == 0 && a.last != nullptr && part == (kShared ? 0 : parts - 1)) {
     if (len > 0 && flagged(a, e * a.step_e + (int64_t)(len - 1) * a.step_t)) carry = 0;
     cols.store_state(a.last, e, a.E, carry);
   }
@@ -731,8 +855,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   extern __shared__ __align__(128) unsigned char ring_tiles[];  // [STAGES][x, gate, dh, h one step earlier]
   __shared__ __align__(16) GatedShared<W, STAGES, kShared> sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = kShared ? blockIdx.x % share : 0;
-  const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / share, e = unit / blocks;
+  const int parts = kShared ? share : a.nseg, part = blockIdx.x % parts, rank = kShared ? part : 0;
+  const int64_t blocks = (a.D + kCols - 1) / kCols, unit = blockIdx.x / parts, e = unit / blocks;
+  // a row's steps, or a segment's
+  const int begin = kShared ? 0 : part * a.seg_len, stop = kShared ? (int)a.T : (int)min(a.T, (int64_t)begin + a.seg_len);
   const Cols<ST, kBulk> cols{(unit % blocks) * kCols, lane, a.D};
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -745,11 +871,11 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   else __syncthreads();
   pdl_wait();
 
-  const int len = row_length(a, e);
-  const int ntiles = (len + L - 1) / L, rounds = (ntiles + share - 1) / share;
+  const int len = row_length(a, e), lim = min(len, stop);
+  const int ntiles = (max(lim - begin, 0) + L - 1) / L, rounds = (ntiles + share - 1) / share;
   const int mine = ntiles > rank ? (ntiles - rank + share - 1) / share : 0;
   // the row's last tile first
-  const int last_tile = (rank + (mine - 1) * share) * L;
+  const int last_tile = begin + (rank + (mine - 1) * share) * L;
   RowCopy<ST, L> copy;
   if constexpr (!kBulk) {
     static_assert(kArrays * L <= 32 * W, "a row a thread");
@@ -777,29 +903,30 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
 
   V2 carry = cols.state(a.d_last, e, a.E);
   if (len > 0 && flagged(a, e * a.step_e + (int64_t)(len - 1) * a.step_t)) carry = 0;
+  if constexpr (!kShared) carry = through_segments<false>(a, unit, parts - 1, parts - 1 - part, carry);
   FillRing<STAGES> ring;
   bool met = true;
   int j = 0;
-  int t0 = (rank + (rounds - 1) * share) * L + warp * C;
+  int t0 = begin + (rank + (rounds - 1) * share) * L + warp * C;
   const int64_t row0 = e * a.step_e + t0 * a.step_t;
   const auto reader = [&](int i, const float* p, int64_t row, int64_t stride) {
     return Reader<ST, kBulk, L>(a, i, warp * C, lane, p, row, stride, cols.c0);
   };
-  const int64_t tile0 = e * a.step_e + (int64_t)rank * L * a.step_t;
+  const int64_t tile0 = e * a.step_e + (int64_t)(begin + rank * L) * a.step_t;
   const auto xs = reader(0, a.x, tile0, a.x_stride), gs = reader(1, a.gate, tile0, a.gate_stride),
              ds = reader(2, a.dh, tile0, a.dh_stride), hs = reader(3, a.in_h, tile0 - a.step_t, a.h_stride);
   Writer<ST, kBulk> to_x(cols, a, a.dx, a.dx_stride, row0), to_gate(cols, a, a.dgate, a.dgate_stride, row0);
   // behind the row's last tile
-  for (int t = t0 + share * L; t < a.T; t += share * L) {
+  for (int t = t0 + share * L; t < stop; t += share * L) {
     Writer<ST, kBulk> x = to_x, g = to_gate;
     x.move(t - t0), g.move(t - t0);
     x.start(), g.start();
-    for (int i = 0; i < C && t + i < a.T; ++i) x.put(0), g.put(0);
+    for (int i = 0; i < C && t + i < stop; ++i) x.put(0), g.put(0);
   }
   const bool flags = a.terminated != nullptr || a.truncated != nullptr;
   bool cut_next = flags && lane < C && cut_before(a, e, t0 + lane, len);
   for (int k = rounds - 1; k >= 0; --k, t0 -= share * L) {
-    const int real = min(max(len - t0, 0), C);
+    const int real = min(max(lim - t0, 0), C);
     uint32_t cut = 0;
     if (flags) {
       cut = __ballot_sync(kFullMask, cut_next);
@@ -840,7 +967,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
             const V2 before = here ? 0 : t0 + i == 0 ? first : hs.get(tile, i).wide();
             g[i] = add2(ds.get(tile, i).wide(), m.q);
             w[i] = mul2(mul2(s, na[i]), fma2(xs.get(tile, i).wide(), minus, before));
-            if (here) m = {0x8000000080000000ull, 0};
+            if (here) m = {kSevered, 0};
             else m = {severed(m) ? m.p : mul2(m.p, s), mul2(s, g[i])};
           }
         }
@@ -860,7 +987,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
     } else {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        if (t0 + i >= a.T) continue;
+        if (t0 + i >= stop) continue;
         const bool on = k < mine && i < real;
         const V2 G = on ? pass({p[i], g[i]}, u) : 0;
         to_x.put(on ? mul2(na[i], G) : 0);
@@ -869,7 +996,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
     }
     to_x.move(-share * L), to_gate.move(-share * L);
   }
-  if (rank == 0 && warp == 0 && a.d_state != nullptr) cols.store_state(a.d_state, e, a.E, carry);
+  if (warp == 0 && part == 0 && a.d_state != nullptr) cols.store_state(a.d_state, e, a.E, carry);
   if (!ring.ok && (threadIdx.x == 0 || !kBulk))
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
   if constexpr (kShared) cluster_meet();
@@ -930,33 +1057,61 @@ struct TileShape<float, true, true> : Shape<8, 4, 3, 2> {};
 template <>
 struct TileShape<float, true, false> : Shape<8, 4, 2, 2> {};
 
-// CTAs of a row: as many as fit the SMs beside each other
-int row_share(int64_t units, int64_t ntiles, int64_t slots) {
-  int share = 1;
-  while (share < kMaxShare && 2 * share * units <= slots && 2 * share <= ntiles) share *= 2;
-  return share;
+// CTAs of a row: as many as fit the SMs beside each other in clusters of up to
+// 8; where those would leave two thirds of them idle, segments of at least two
+// tiles, which read the inputs twice.  (bfloat16, one row of 65536 steps, us
+// clusters / segments: 256 channels 183 / 43, 1024 238 / 136, the gradient 208 /
+// 67 and 261 / 259; 4096 channels 285 / 572.  4096 steps of 1024 channels 18.9 /
+// 15.1, the gradient 20.1 / 23.5; 2048 steps of 256 channels 7.1 / 10.6.)
+constexpr int kSegStep = 64;  // whole tiles of every shape
+struct Split {
+  int share = 1, nseg = 1, seg_len = 0;
+};
+Split split_rows(int64_t E, int64_t T, int64_t D, int64_t slots) {
+  const int64_t units = E * div_up(D, kCols), tiles = div_up(T, kSegStep);
+  Split r;
+  r.seg_len = (int)T;
+  if (3 * units * kMaxShare <= slots && tiles > 4 * kMaxShare) {
+    const int64_t segs = std::min(slots / units, tiles / 2);
+    r.seg_len = (int)(div_up(tiles, segs) * kSegStep);
+    r.nseg = (int)div_up(T, r.seg_len);
+    return r;
+  }
+  while (r.share < kMaxShare && 2 * r.share * units <= slots && 2 * r.share <= tiles) r.share *= 2;
+  return r;
+}
+template <class ST, bool kBack>
+Split split_rows(int64_t E, int64_t T, int64_t D, int sm) {
+  return split_rows(E, T, D, (int64_t)TileShape<ST, kBack, true>::RES * sm);
 }
 
-template <class ST, bool kBack, bool kBulk, bool kShared>
+template <class ST, bool kBack, bool kBulk, bool kShared, bool kMaps>
 cudaError_t launch_shape(const GatedArgs& a, const GatedMaps& maps, int share, cudaStream_t s) {
-  using H = TileShape<ST, kBack, kBulk>;
+  using H = TileShape<ST, kBack && !kMaps, kBulk>;
+  static_assert(kSegStep % (H::C * H::W) == 0, "segments of whole tiles");
   constexpr int L = H::C * H::W;
-  constexpr size_t smem = (size_t)H::STAGES * (kBack ? 4 : 2) * TileRows<ST, kBulk, L>::kTile;
+  constexpr size_t smem = (size_t)H::STAGES * (kBack && !kMaps ? 4 : 2) * TileRows<ST, kBulk, L>::kTile;
   static_assert(H::RES * (smem + sizeof(GatedShared<H::W, H::STAGES, kShared>) + 1024) <= 228 * 1024, "RES CTAs fit an SM");
   void (*kernel)(GatedArgs, GatedMaps, int);
-  if constexpr (kBack) kernel = gated_grad_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, kShared, H::RES>;
+  if constexpr (kMaps) kernel = gated_map_kernel<ST, H::C, H::W, H::STAGES, kBulk, kBack, H::RES>;
+  else if constexpr (kBack) kernel = gated_grad_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, kShared, H::RES>;
   else kernel = gated_tile_kernel<ST, H::C, H::W, H::STAGES, kBulk, kShared, H::RES>;
   static std::atomic<uint64_t> allowed;
   const cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return e;
-  return launch_tiles(kernel, a.E * div_up(a.D, kCols) * share, 32 * H::W, smem, share, s, a, maps);
+  return launch_tiles(kernel, a.E * div_up(a.D, kCols) * share * a.nseg, 32 * H::W, smem, share, s, a, maps);
 }
 
 template <class ST, bool kBack, bool kBulk>
-cudaError_t run_tiles(const GatedArgs& a, const GatedMaps& maps, int sm, cudaStream_t s) {
-  using H = TileShape<ST, kBack, kBulk>;
-  const int share = row_share(a.E * div_up(a.D, kCols), div_up(a.T, H::C * H::W), (int64_t)H::RES * sm);
-  return share > 1 ? launch_shape<ST, kBack, kBulk, true>(a, maps, share, s) : launch_shape<ST, kBack, kBulk, false>(a, maps, 1, s);
+cudaError_t run_tiles(GatedArgs a, const GatedMaps& maps, int sm, cudaStream_t s) {
+  const Split r = split_rows<ST, kBack>(a.E, a.T, a.D, sm);
+  a.nseg = r.nseg, a.seg_len = r.seg_len;
+  if (r.share > 1) return launch_shape<ST, kBack, kBulk, true, false>(a, maps, r.share, s);
+  if (r.nseg > 1) {
+    const cudaError_t e = launch_shape<ST, kBack, kBulk, false, true>(a, maps, 1, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_shape<ST, kBack, kBulk, false, false>(a, maps, 1, s);
 }
 
 // Whether rows of T steps are walked by threads of their own, step by step,
@@ -965,9 +1120,19 @@ cudaError_t run_tiles(const GatedArgs& a, const GatedMaps& maps, int sm, cudaStr
 // (us, steps / tiles, 2048 channels bfloat16: forward 16 rows of 8 steps 3.0 /
 // 3.8, of 16 4.7 / 3.1; 256 rows of 16 15 / 40, of 64 53 / 43.  Gradient: 64
 // rows of 16 19 / 31, of 32 36 / 33; 256 rows of 64 80 / 114.)
-bool by_steps(const GatedArgs& a, int64_t slots) {
-  const int64_t units = a.E * div_up(a.D, kCols);
-  return a.T <= 8 || (a.T <= 64 && a.T * slots <= 4 * units) || units > INT32_MAX / kMaxShare;
+bool by_steps(int64_t E, int64_t T, int64_t D, int64_t slots) {
+  const int64_t units = E * div_up(D, kCols);
+  return T <= 8 || (T <= 64 && T * slots <= 4 * units) || units > INT32_MAX / kMaxShare;
+}
+template <class ST, bool kBack>
+bool by_steps(int64_t E, int64_t T, int64_t D, int sm) {
+  return by_steps(E, T, D, (int64_t)TileShape<ST, kBack, true>::RES * sm);
+}
+template <class ST, bool kBack>
+size_t workspace_of(int64_t E, int64_t T, int64_t D, int sm) {
+  if (by_steps<ST, kBack>(E, T, D, sm)) return 0;
+  const Split r = split_rows<ST, kBack>(E, T, D, sm);
+  return r.nseg > 1 ? (size_t)(E * div_up(D, kCols)) * r.nseg * 32 * sizeof(Map2) : 0;
 }
 
 // In vectors where every row starts on a 16-byte boundary (`even`)
@@ -981,7 +1146,7 @@ cudaError_t launch_steps(void (*vectors)(GatedArgs, int64_t), void (*single)(Gat
 template <class ST>
 cudaError_t scan_typed(const GatedArgs& a, int sm, cudaStream_t s) {
   constexpr int es = Stor<ST>::kBytes, L = TileShape<ST, false, true>::C * TileShape<ST, false, true>::W;
-  if (by_steps(a, (int64_t)TileShape<ST, false, true>::RES * sm))
+  if (by_steps<ST, false>(a.E, a.T, a.D, sm))
     return launch_steps(gated_step_kernel<ST>, gated_serial_kernel<ST>,
                         rows_aligned({a.x, a.gate, a.h}, {a.D, a.x_stride, a.gate_stride}, es, 16) &&
                             rows_aligned({a.state, a.last}, {}, 4, 16),
@@ -997,8 +1162,10 @@ cudaError_t scan_typed(const GatedArgs& a, int sm, cudaStream_t s) {
 
 template <class ST>
 cudaError_t grad_typed(const GatedArgs& a, int sm, cudaStream_t s) {
-  constexpr int es = Stor<ST>::kBytes, L = TileShape<ST, true, true>::C * TileShape<ST, true, true>::W;
-  if (by_steps(a, (int64_t)TileShape<ST, true, true>::RES * sm))
+  using H = TileShape<ST, true, true>;
+  constexpr int es = Stor<ST>::kBytes, L = H::C * H::W;
+  static_assert(L == TileShape<ST, false, true>::C * TileShape<ST, false, true>::W, "one box of steps for both launches");
+  if (by_steps<ST, true>(a.E, a.T, a.D, sm))
     return launch_steps(gated_grad_step_kernel<ST>, gated_grad_serial_kernel<ST>,
                         rows_aligned({a.x, a.gate, a.dh, a.in_h, a.dx, a.dgate},
                                      {a.D, a.x_stride, a.gate_stride, a.dh_stride, a.h_stride, a.dx_stride, a.dgate_stride}, es, 16) &&
@@ -1022,6 +1189,12 @@ cudaError_t run_gated_scan(const GatedArgs& a, int sm, cudaStream_t s) {
 
 cudaError_t run_gated_scan_backward(const GatedArgs& a, int sm, cudaStream_t s) {
   return a.bf16_io ? grad_typed<bf16>(a, sm, s) : grad_typed<float>(a, sm, s);
+}
+
+size_t gated_scan_workspace(int64_t E, int64_t T, int64_t D, bool bf16_io, bool backward, int sm) {
+  if (E == 0 || T == 0 || D == 0) return 0;
+  if (backward) return bf16_io ? workspace_of<bf16, true>(E, T, D, sm) : workspace_of<float, true>(E, T, D, sm);
+  return bf16_io ? workspace_of<bf16, false>(E, T, D, sm) : workspace_of<float, false>(E, T, D, sm);
 }
 
 cudaError_t status_gated(unsigned int* word, bool clear) { return unit_status(word, clear); }

@@ -95,8 +95,10 @@ struct ClipArgs {
 size_t clip_workspace(int64_t count, int sm_count);
 cudaError_t run_clip_grads(const ClipArgs& a, int sm_count, cudaStream_t s);
 
-// workspace of the RMS norm's gradient (k_rms.cu; its calls are in trunk.h)
+// workspaces of the RMS norm's gradient and of the gated scans (their calls
+// are in trunk.h)
 size_t rms_norm_backward_workspace(int64_t N, int64_t D, int sm_count);
+size_t gated_scan_workspace(int64_t E, int64_t T, int64_t D, bool bf16_io, bool backward, int sm_count);
 
 // the device status words of these translation units, ORed into *word
 cudaError_t status_norm(unsigned int* word, bool clear);

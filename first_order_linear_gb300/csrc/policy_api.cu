@@ -46,16 +46,19 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
 }  // namespace
 
 bool policy_estimator(int estimator) {
-  return estimator >= RLCA_EST_TOKEN_LOGPROB && estimator <= RLCA_EST_RMS_NORM_BACKWARD;
+  return estimator >= RLCA_EST_TOKEN_LOGPROB && estimator <= RLCA_EST_GATED_SCAN_BACKWARD;
 }
 
 int policy_workspace_size(int estimator, int64_t E, int64_t T, int32_t num_actions, uint32_t flags, size_t* bytes) {
-  if (!flags_ok(flags, RLCA_BF16)) return RLCA_ERR_INVALID_ARG;
+  const bool scan = estimator == RLCA_EST_GATED_SCAN || estimator == RLCA_EST_GATED_SCAN_BACKWARD;
+  if (!flags_ok(flags, scan ? RLCA_BF16 | RLCA_TIME_MAJOR : RLCA_BF16)) return RLCA_ERR_INVALID_ARG;
   const bool head = estimator == RLCA_EST_TOKEN_LOGPROB || estimator == RLCA_EST_TOKEN_LOGPROB_BACKWARD;
   if (head) {
     const int st = head_sizes(E, T, num_actions);
     if (st != RLCA_OK) return st;
   } else if (E < 0 || T < 0 || E > kMaxRows || T > kMaxWidth) {
+    return RLCA_ERR_INVALID_ARG;
+  } else if (scan && (num_actions < 0 || num_actions > kMaxWidth || (num_actions > 0 && E * T > kMaxRows))) {
     return RLCA_ERR_INVALID_ARG;
   }
   if (E == 0 || T == 0) return RLCA_OK;
@@ -65,6 +68,8 @@ int policy_workspace_size(int estimator, int64_t E, int64_t T, int32_t num_actio
     *bytes = head_workspace(E, T, num_actions, (flags & RLCA_BF16) != 0, estimator == RLCA_EST_TOKEN_LOGPROB_BACKWARD, sm);
   else if (estimator == RLCA_EST_LAYER_NORM_BACKWARD)
     *bytes = layer_norm_backward_workspace(E, T, sm);
+  else if (scan)
+    *bytes = gated_scan_workspace(E, T, num_actions, (flags & RLCA_BF16) != 0, estimator == RLCA_EST_GATED_SCAN_BACKWARD, sm);
   else if (estimator == RLCA_EST_RMS_NORM_BACKWARD)
     *bytes = rms_norm_backward_workspace(E, T, sm);
   else

@@ -46,6 +46,8 @@ struct GatedArgs {
   int64_t E, T, D, step_e, step_t;
   int64_t x_stride, gate_stride, h_stride, dh_stride, dx_stride, dgate_stride;
   bool bf16_io;
+  void* ws;
+  int nseg, seg_len;  // segments of a row, and their steps (set by the calls)
 };
 cudaError_t run_gated_scan(const GatedArgs& a, int sm_count, cudaStream_t s);
 cudaError_t run_gated_scan_backward(const GatedArgs& a, int sm_count, cudaStream_t s);

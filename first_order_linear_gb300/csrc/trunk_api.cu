@@ -59,6 +59,10 @@ Rows flat(const void* p, int64_t n, size_t elem) { return {p, 1, n, n > 0 ? n : 
 
 int launched(cudaError_t e, cudaStream_t s) { return e == cudaSuccess ? checked_build_status(s) : RLCA_ERR_CUDA; }
 
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws != nullptr && have >= need && aligned(ws, 16));
+}
+
 size_t ebytes(uint32_t flags) { return (flags & RLCA_BF16) ? 2 : 4; }
 
 // sizes and flags of a gated scan: RLCA_OK with *empty where nothing is to be done, or the status to return
@@ -125,8 +129,7 @@ int rlca_rms_norm_backward(const float* dy, const float* d_total, const float* t
   if (rows_clash({rdy, rdt, rt, q, sc, rw, rs, ws}, {rdx, rdw})) return RLCA_ERR_INVALID_ARG;
   int sm = 0;
   if (sm_count_of_current_device(&sm) != cudaSuccess) return RLCA_ERR_CUDA;
-  const size_t need = N == 0 ? 0 : rms_norm_backward_workspace(N, D, sm);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return RLCA_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, N == 0 ? 0 : rms_norm_backward_workspace(N, D, sm))) return RLCA_ERR_INVALID_ARG;
   RmsGradArgs a = {};
   a.dy = dy; a.d_total = d_total; a.total = total; a.total8 = total8; a.total8_scale = total8_scale;
   a.weight = weight; a.rstd = rstd; a.dx = dx; a.dweight = dweight;
@@ -137,7 +140,8 @@ int rlca_rms_norm_backward(const float* dy, const float* d_total, const float* t
 
 int rlca_gated_scan(const float* x, const float* gate, const uint8_t* terminated, const uint8_t* truncated,
                     const float* state, const int32_t* lengths, float* h, float* last, int64_t E, int64_t T, int64_t D,
-                    int64_t x_stride, int64_t gate_stride, uint32_t flags, rlca_stream_t stream) {
+                    int64_t x_stride, int64_t gate_stride, uint32_t flags, void* workspace, size_t workspace_bytes,
+                    rlca_stream_t stream) {
   bool empty = false;
   const int st = gated_sizes(E, T, D, flags, &empty);
   if (st != RLCA_OK || empty) return st;
@@ -149,11 +153,15 @@ int rlca_gated_scan(const float* x, const float* gate, const uint8_t* terminated
   const Rows t1 = flat(terminated, n, 1), t2 = flat(truncated, n, 1), len = flat(lengths, E, 4);
   const Rows s0 = flat(state, E * D, 4), s1 = flat(last, E * D, 4);
   if ((n > 0 && !rows_ok({rx, rg, rh})) || !rows_ok({len, s0, s1})) return RLCA_ERR_INVALID_ARG;
-  if (rows_clash({rx, rg, t1, t2, len}, {rh, s1}) || rows_overlap(rh, s0) || (last != state && rows_overlap(s1, s0)))
+  const Rows ws = flat(workspace, (int64_t)workspace_bytes, 1);
+  if (rows_clash({rx, rg, t1, t2, len, ws}, {rh, s1}) || rows_overlap(rh, s0) || (last != state && rows_overlap(s1, s0)))
     return RLCA_ERR_INVALID_ARG;
   int sm = 0;
   if (sm_count_of_current_device(&sm) != cudaSuccess) return RLCA_ERR_CUDA;
+  if (!workspace_ok(workspace, workspace_bytes, gated_scan_workspace(E, T, D, (flags & RLCA_BF16) != 0, false, sm)))
+    return RLCA_ERR_INVALID_ARG;
   GatedArgs a = {};
+  a.ws = workspace;
   a.x = x; a.gate = gate; a.terminated = terminated; a.truncated = truncated; a.state = state; a.lengths = lengths;
   a.h = h; a.last = last;
   a.E = E; a.T = T; a.D = D; a.step_e = (flags & RLCA_TIME_MAJOR) ? 1 : T; a.step_t = (flags & RLCA_TIME_MAJOR) ? E : 1;
@@ -166,7 +174,7 @@ int rlca_gated_scan_backward(const float* dh, const float* x, const float* gate,
                              const int32_t* lengths, const float* d_last, float* dx, float* dgate, float* d_state,
                              int64_t E, int64_t T, int64_t D, int64_t dh_stride, int64_t x_stride, int64_t gate_stride,
                              int64_t h_stride, int64_t dx_stride, int64_t dgate_stride, uint32_t flags,
-                             rlca_stream_t stream) {
+                             void* workspace, size_t workspace_bytes, rlca_stream_t stream) {
   bool empty = false;
   const int st = gated_sizes(E, T, D, flags, &empty);
   if (st != RLCA_OK || empty) return st;
@@ -179,12 +187,16 @@ int rlca_gated_scan_backward(const float* dh, const float* x, const float* gate,
   const Rows t1 = flat(terminated, n, 1), t2 = flat(truncated, n, 1), len = flat(lengths, E, 4);
   const Rows s0 = flat(state, E * D, 4), dl = flat(d_last, E * D, 4), ds = flat(d_state, E * D, 4);
   if ((n > 0 && !rows_ok({rdh, rx, rg, rh, rdx, rdg})) || !rows_ok({len, s0, dl, ds})) return RLCA_ERR_INVALID_ARG;
-  if (rows_clash({rdh, rx, rg, rh, t1, t2, len, s0}, {rdx, rdg, ds}) || rows_overlap(rdx, dl) || rows_overlap(rdg, dl) ||
+  const Rows ws = flat(workspace, (int64_t)workspace_bytes, 1);
+  if (rows_clash({rdh, rx, rg, rh, t1, t2, len, s0, ws}, {rdx, rdg, ds}) || rows_overlap(rdx, dl) || rows_overlap(rdg, dl) ||
       (d_state != d_last && rows_overlap(ds, dl)))
     return RLCA_ERR_INVALID_ARG;
   int sm = 0;
   if (sm_count_of_current_device(&sm) != cudaSuccess) return RLCA_ERR_CUDA;
+  if (!workspace_ok(workspace, workspace_bytes, gated_scan_workspace(E, T, D, (flags & RLCA_BF16) != 0, true, sm)))
+    return RLCA_ERR_INVALID_ARG;
   GatedArgs a = {};
+  a.ws = workspace;
   a.dh = dh; a.x = x; a.gate = gate; a.in_h = h; a.terminated = terminated; a.truncated = truncated; a.state = state;
   a.lengths = lengths; a.d_last = d_last; a.dx = dx; a.dgate = dgate; a.d_state = d_state;
   a.E = E; a.T = T; a.D = D; a.step_e = (flags & RLCA_TIME_MAJOR) ? 1 : T; a.step_t = (flags & RLCA_TIME_MAJOR) ? E : 1;

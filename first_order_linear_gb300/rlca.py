@@ -819,7 +819,7 @@ def _scan_inputs(x, gate, terminated, truncated, state, lengths, time_major):
 
 
 def rlca_gated_scan(x, gate, terminated=None, truncated=None, state=None, lengths=None, *, time_major=False, h=None,
-                    last=None, want_last=True, stream=None):
+                    last=None, want_last=True, workspace=None, stream=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t with a_t =
     sigmoid(gate_t) over the steps of ``x``, ``gate`` [E, T, D], from ``state``
     [E, D] float32 (None: 0), starting anew behind flagged steps: ``(h, last)``,
@@ -835,15 +835,17 @@ def rlca_gated_scan(x, gate, terminated=None, truncated=None, state=None, length
     _require_cuda(dev)
     flags = _fflag(fdt) | (_lib.RLCA_TIME_MAJOR if time_major else 0)
     with _on(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_GATED_SCAN, E, T, D, flags, dev, workspace)
         check("rlca_gated_scan", lib.rlca_gated_scan(
             x.data_ptr(), gate.data_ptr(), _ptr(terminated), _ptr(truncated), _ptr(state), _ptr(lengths), h.data_ptr(),
-            _ptr(last), E, T, D, xs, gs, flags, _raw_stream(dev, stream)))
-        _hold(dev, stream, h, last)
+            _ptr(last), E, T, D, xs, gs, flags, _ptr(ws), wsb, _raw_stream(dev, stream)))
+        _hold(dev, stream, ws, h, last)
     return h, last
 
 
 def rlca_gated_scan_backward(dh, x, gate, h, terminated=None, truncated=None, state=None, lengths=None, *, d_last=None,
-                             time_major=False, dx=None, dgate=None, d_state=None, want_d_state=True, stream=None):
+                             time_major=False, dx=None, dgate=None, d_state=None, want_d_state=True,
+                             workspace=None, stream=None):
     """Gradient of :func:`rlca_gated_scan` from its inputs and its ``h``, for
     ``dh`` and ``d_last`` (None: 0): ``(dx, dgate, d_state)``, d_state [E, D]
     float32, None when not wanted.  Buffers given for dx and dgate may have
@@ -861,9 +863,10 @@ def rlca_gated_scan_backward(dh, x, gate, h, terminated=None, truncated=None, st
     _require_cuda(dev)
     flags = _fflag(fdt) | (_lib.RLCA_TIME_MAJOR if time_major else 0)
     with _on(dev):
+        ws, wsb = _workspace(_lib.RLCA_EST_GATED_SCAN_BACKWARD, E, T, D, flags, dev, workspace)
         check("rlca_gated_scan_backward", lib.rlca_gated_scan_backward(
             dh.data_ptr(), x.data_ptr(), gate.data_ptr(), h.data_ptr(), _ptr(terminated), _ptr(truncated), _ptr(state),
             _ptr(lengths), _ptr(d_last), dx.data_ptr(), dgate.data_ptr(), _ptr(d_state), E, T, D, dhs, xs, gs, hs, dxs,
-            dgs, flags, _raw_stream(dev, stream)))
-        _hold(dev, stream, dx, dgate, d_state)
+            dgs, flags, _ptr(ws), wsb, _raw_stream(dev, stream)))
+        _hold(dev, stream, ws, dx, dgate, d_state)
     return dx, dgate, d_state

@@ -134,6 +134,9 @@ typedef struct CUstream_st *rlca_stream_t;
 #define RLCA_EST_LAYER_NORM_BACKWARD    12
 #define RLCA_EST_CLIP_GRADS             13
 #define RLCA_EST_RMS_NORM_BACKWARD      14
+/* the gated scans: E, T, num_actions = channels */
+#define RLCA_EST_GATED_SCAN             15
+#define RLCA_EST_GATED_SCAN_BACKWARD    16
 
 /* ---- prefix-sum element types ------------------------------------------- */
 #define RLCA_F32 0
@@ -179,7 +182,8 @@ int rlca_index_checks(void);
  * Bytes of device workspace that the call of `estimator` (RLCA_EST_*) with
  * these sizes and flags needs on the CURRENT device (0 for the one-pass
  * path).  num_actions is read for RLCA_EST_RETRACE (actions) and the
- * RLCA_EST_TOKEN_LOGPROB ids (vocabulary) only.  Writes the size to *bytes.  Errors: RLCA_ERR_INVALID_ARG for a NULL `bytes`, an unknown
+ * RLCA_EST_TOKEN_LOGPROB (vocabulary) and RLCA_EST_GATED_SCAN (channels) ids
+ * only.  Writes the size to *bytes.  Errors: RLCA_ERR_INVALID_ARG for a NULL `bytes`, an unknown
  * estimator, bad sizes or flags; RLCA_ERR_CUDA if the device cannot be
  * queried.
  */
@@ -648,12 +652,14 @@ int rlca_rms_norm_backward(const float *dy, const float *d_total,
  *   last                   [E,D] f32 output, NULL = not written
  * Flags: RLCA_TIME_MAJOR, RLCA_BF16 (x, gate and h).  E * T is at most
  * 2^31 - 1.  E == 0 or D == 0 enqueues nothing; T == 0 writes last only.
+ * Workspace: RLCA_EST_GATED_SCAN (nothing unless a few rows are long).
  */
 int rlca_gated_scan(const float *x, const float *gate,
                     const uint8_t *terminated, const uint8_t *truncated,
                     const float *state, const int32_t *lengths, float *h,
                     float *last, int64_t E, int64_t T, int64_t D,
                     int64_t x_stride, int64_t gate_stride, uint32_t flags,
+                    void *workspace, size_t workspace_bytes,
                     rlca_stream_t stream);
 
 /*
@@ -674,7 +680,8 @@ int rlca_gated_scan(const float *x, const float *gate,
  *                          matrix's rows
  *   d_state                [E,D] f32 output, NULL = not written; may be
  *                          d_last's own buffer
- * Otherwise as rlca_gated_scan; T == 0 writes d_state only.
+ * Otherwise as rlca_gated_scan; T == 0 writes d_state only.  Workspace:
+ * RLCA_EST_GATED_SCAN_BACKWARD.
  */
 int rlca_gated_scan_backward(const float *dh, const float *x,
                              const float *gate, const float *h,
@@ -686,7 +693,8 @@ int rlca_gated_scan_backward(const float *dh, const float *x,
                              int64_t dh_stride, int64_t x_stride,
                              int64_t gate_stride, int64_t h_stride,
                              int64_t dx_stride, int64_t dgate_stride,
-                             uint32_t flags, rlca_stream_t stream);
+                             uint32_t flags, void *workspace,
+                             size_t workspace_bytes, rlca_stream_t stream);
 
 #ifdef __cplusplus
 }

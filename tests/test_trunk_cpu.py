@@ -143,7 +143,7 @@ def test_rms_norm_backward_refusals(lib):
 
 def _scan(lib, **k):
     a = dict(x=P[0], gate=P[1], term=P[2], trunc=None, state=P[4], len=P[5], h=P[6], last=P[7], E=3, T=5, D=8, xs=8, gs=8,
-             flags=0)
+             flags=0, ws=None, wsb=0)
     a.update(k)
     return lib.rlca_gated_scan(*a.values(), None)
 
@@ -153,14 +153,15 @@ def test_gated_scan_refusals(lib):
     assert _scan(lib, T=0, x=None, gate=None, h=None, last=None) == OK
     for bad in (dict(E=-1), dict(T=-1), dict(D=-1), dict(E=1 << 16, T=1 << 15), dict(x=None), dict(gate=None),
                 dict(h=None), dict(xs=7), dict(gs=0), dict(flags=0x2), dict(flags=0x10), dict(h=P[0]), dict(h=P[4]),
-                dict(last=P[1]), dict(last=P[6]), dict(last=_at(4, 4)), dict(last=P[5]), dict(h=P[2]),
+                dict(last=P[1]), dict(last=P[6]), dict(ws=P[6], wsb=64), dict(last=_at(4, 4)), dict(last=P[5]), dict(h=P[2]),
                 dict(x=_at(0, 1)), dict(state=_at(4, 2)), dict(len=_at(5, 1))):
         assert _scan(lib, **bad) == INV, bad
 
 
 def _scan_grad(lib, **k):
     a = dict(dh=P[0], x=P[1], gate=P[2], h=P[3], term=P[4], trunc=None, state=P[5], len=P[6], dl=P[7], dx=P[8], dg=P[9],
-             ds=P[10], E=3, T=5, D=8, dhs=8, xs=8, gs=8, hs=8, dxs=8, dgs=8, flags=0)
+             ds=P[10], E=3, T=5, D=8, dhs=8, xs=8, gs=8, hs=8, dxs=8, dgs=8, flags=0, ws=None,
+             wsb=0)
     a.update(k)
     return lib.rlca_gated_scan_backward(*a.values(), None)
 
@@ -170,7 +171,7 @@ def test_gated_scan_backward_refusals(lib):
     for bad in (dict(E=-1), dict(T=-1), dict(dh=None), dict(x=None), dict(gate=None), dict(h=None), dict(dx=None),
                 dict(dg=None), dict(dhs=7), dict(xs=7), dict(gs=7), dict(hs=7), dict(dxs=7), dict(dgs=7),
                 dict(flags=0x4), dict(dx=P[0]), dict(dg=P[1]), dict(dx=P[3]), dict(dg=P[8]), dict(ds=P[5]),
-                dict(ds=_at(7, 4)), dict(dx=P[7]), dict(dx=_at(8, 2)),
+                dict(ds=_at(7, 4)), dict(ws=P[9], wsb=64), dict(dx=P[7]), dict(dx=_at(8, 2)),
                 # parts of one matrix's rows that share a column, or lie at different strides
                 dict(dxs=15, dgs=15, dg=_at(8, 32)), dict(dxs=16, dgs=17, dg=_at(8, 32)),
                 dict(dxs=16, dgs=16, dg=_at(8, 36)), dict(dxs=16, dgs=16, dg=_at(8, 28))):
@@ -182,6 +183,15 @@ def test_rms_workspace_size_refusals(lib):
     q = lambda *a: lib.rlca_workspace_size(_lib.RLCA_EST_RMS_NORM_BACKWARD, *a, C.byref(out))  # noqa: E731
     assert q(-1, 8, 0, 0) == INV and q(4, 8, 0, _lib.RLCA_TIME_MAJOR) == INV
     assert q(0, 8, 0, 0) == OK and out.value == 0
+
+
+@pytest.mark.parametrize("estimator", [_lib.RLCA_EST_GATED_SCAN, _lib.RLCA_EST_GATED_SCAN_BACKWARD])
+def test_gated_scan_workspace_size_refusals(lib, estimator):
+    out = C.c_size_t(1)
+    q = lambda *a: lib.rlca_workspace_size(estimator, *a, C.byref(out))  # noqa: E731
+    assert q(4, 8, -1, 0) == INV and q(1 << 16, 1 << 15, 8, 0) == INV and q(4, 8, 8, _lib.RLCA_MULTIPASS) == INV
+    assert q(4, 0, 8, _lib.RLCA_TIME_MAJOR | BF) == OK and out.value == 0
+    assert lib.rlca_workspace_size(estimator + 2, 4, 8, 8, 0, C.byref(out)) == INV
 
 
 # ---- refusals of the Python binding ------------------------------------------

@@ -139,7 +139,7 @@ def check_scan(E, T, D, dtype, backward=True, tol=1e-6, **kw):
 # that do not; rows that share the SMs and one row alone
 SCAN_SIZES = [(1, 1, 1), (3, 1, 130), (1, 2, 64), (2, 7, 33), (5, 16, 128), (2, 63, 100), (1, 64, 256), (3, 65, 65),
               (2, 127, 72), (1, 129, 8), (4, 255, 40), (1, 300, 514), (2, 513, 96), (70, 33, 192), (1, 2049, 64),
-              (1, 5000, 130), (9, 1000, 24)]
+              (1, 5000, 130), (9, 1000, 24), (1, 4200, 40), (2, 9001, 64)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -239,6 +239,30 @@ def test_gated_scan_extreme_gates():
                     (-200.0, x)):
         h, _ = rlca.rlca_gated_scan(x, torch.full_like(x, g), state=state)
         assert torch.equal(h, want), g
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,T,D", [(2, 700, 64), (1, 900, 96), (2, 9001, 64), (4, 7, 64)])
+def test_gated_scan_closed_gates_beside_open_ones(E, T, D, dtype):
+    """Channels whose gates are shut so far that products of them vanish, next to channels that remember, with ends of
+    episodes between: what marks an end in one channel's product says nothing in another's."""
+    d = steps_problem(E, T, D, dtype, seed=T, ends=0.02)
+    dh, d_last = d.pop("dh"), d.pop("d_last")
+    shut = torch.tensor([-20.0, -100.0, -17.0, -60.0], device="cuda").repeat(T)[:T].to(dtype)
+    d["gate"][..., 0::2] = shut[:, None]
+    want_h, want_last, bh, bl = ref.gated_scan(**d)
+    h, last = rlca.rlca_gated_scan(**d)
+    k = SCAN[dtype] * U
+    # (a gate below 2^-24 counts as one of up to 2 u: that much of the state may pass)
+    leak = 2 * U * want_h.abs().amax()
+    _close(h, want_h, k * bh + leak + half_step(dtype) * (want_h.abs() + k * bh), "h")
+    _close(last, want_last, k * bl + leak + U * want_last.abs(), "last")
+    want = ref.gated_scan_backward(dh, d["x"], d["gate"], h, d["terminated"], d["truncated"], d["state"], None, d_last)
+    dx, dgate, d_state = rlca.rlca_gated_scan_backward(dh, d["x"], d["gate"], h, d["terminated"], d["truncated"], d["state"],
+                                                       d_last=d_last)
+    big = want[3].amax() + want[4].amax() + want[5].amax()
+    for name, got, w, b in (("dx", dx, want[0], want[3]), ("dgate", dgate, want[1], want[4]), ("d_state", d_state, want[2], want[5])):
+        _close(got, w, k * b + 4 * U * big + half_step(got.dtype) * (w.abs() + k * b), name)
 
 
 def test_gated_scan_empty():
