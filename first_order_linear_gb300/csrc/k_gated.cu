@@ -562,6 +562,14 @@ __device__ __forceinline__ bool cut_before(const GatedArgs& a, int64_t e, int t,
   return t > 0 && t < len && flagged(a, e * a.step_e + (t - 1) * a.step_t);
 }
 
+// the value in front of a row's steps (behind them, backward)
+template <bool kBack, class C>
+__device__ __forceinline__ V2 outer_value(const C& cols, const GatedArgs& a, int64_t e, int len) {
+  if constexpr (!kBack) return cols.state(a.state, e, a.E);
+  if (len > 0 && flagged(a, e * a.step_e + (int64_t)(len - 1) * a.step_t)) return 0;
+  return cols.state(a.d_last, e, a.E);
+}
+
 // What the CTAs of a row have in shared memory beside the ring, and how their
 // maps meet.
 template <int W, int STAGES, bool kShared>
@@ -605,11 +613,20 @@ __device__ __forceinline__ V2 meet(GatedShared<W, STAGES, kShared>& sh, int roun
 
 // Rows too few even for clusters are cut into segments: a first launch leaves
 // every segment's map, and a segment's CTA starts from the value that the maps in
-// front of its steps (behind them, backward) give.
+// front of its steps (behind them, backward) give.  The value in front of all
+// segments comes through the workspace too: its buffer may be the one that the
+// last segment writes.
+__host__ __device__ constexpr int64_t segment_slots(int nseg) { return nseg + 1; }
 __device__ __forceinline__ int64_t segment_at(const GatedArgs& a, int64_t unit, int segment) {
-  return (unit * a.nseg + segment) * 32 + (threadIdx.x & 31);
+  return (unit * segment_slots(a.nseg) + segment) * 32 + (threadIdx.x & 31);
 }
-__device__ __forceinline__ int64_t segment_maps(const GatedArgs& a) { return a.E * ((a.D + kCols - 1) / kCols) * a.nseg * 32; }
+__device__ __forceinline__ int64_t segment_maps(const GatedArgs& a) {
+  return a.E * ((a.D + kCols - 1) / kCols) * segment_slots(a.nseg) * 32;
+}
+__device__ __forceinline__ void leave_map(const GatedArgs& a, int64_t unit, int segment, const Map2& m) {
+  const int64_t i = segment_at(a, unit, segment);
+  if (in_range(i, segment_maps(a))) static_cast<Map2*>(a.ws)[i] = m;
+}
 __device__ __forceinline__ Map2 segment_map(const GatedArgs& a, int64_t unit, int segment) {
   const int64_t i = segment_at(a, unit, segment);
   return in_range(i, segment_maps(a)) ? static_cast<const Map2*>(a.ws)[i] : identity();
@@ -715,7 +732,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs 
       for (int k = 0; k < W; ++k) all = chain(sh.warp_map[j & 1][kBack ? W - 1 - k : k][lane], all);
     }
   }
-  if (warp == 0 && in_range(segment_at(a, unit, part), segment_maps(a))) static_cast<Map2*>(a.ws)[segment_at(a, unit, part)] = all;
+  if (warp == 0) {
+    leave_map(a, unit, part, all);
+    if (part == 0) leave_map(a, unit, a.nseg, {kSevered, outer_value<kBack>(cols, a, e, len)});
+  }
   // (copies still on their way after a wait gave up land before the CTA ends)
   if (!ring.ok && (threadIdx.x == 0 || !kBulk))
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
@@ -770,7 +790,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
 
-  V2 carry = cols.state(a.state, e, a.E);
+  V2 carry = parts > 1 && !kShared ? segment_map(a, unit, parts).q : outer_value<false>(cols, a, e, len);
   if constexpr (!kShared) carry = through_segments<true>(a, unit, 0, part, carry);
   FillRing<STAGES> ring;
   bool met = true;
@@ -901,8 +921,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
 
-  V2 carry = cols.state(a.d_last, e, a.E);
-  if (len > 0 && flagged(a, e * a.step_e + (int64_t)(len - 1) * a.step_t)) carry = 0;
+  V2 carry = parts > 1 && !kShared ? segment_map(a, unit, parts).q : outer_value<true>(cols, a, e, len);
   if constexpr (!kShared) carry = through_segments<false>(a, unit, parts - 1, parts - 1 - part, carry);
   FillRing<STAGES> ring;
   bool met = true;
@@ -1132,7 +1151,7 @@ template <class ST, bool kBack>
 size_t workspace_of(int64_t E, int64_t T, int64_t D, int sm) {
   if (by_steps<ST, kBack>(E, T, D, sm)) return 0;
   const Split r = split_rows<ST, kBack>(E, T, D, sm);
-  return r.nseg > 1 ? (size_t)(E * div_up(D, kCols)) * r.nseg * 32 * sizeof(Map2) : 0;
+  return r.nseg > 1 ? (size_t)(E * div_up(D, kCols)) * segment_slots(r.nseg) * 32 * sizeof(Map2) : 0;
 }
 
 // In vectors where every row starts on a 16-byte boundary (`even`)

@@ -23,7 +23,7 @@ assert lib.rlca_index_checks() == 1, "not the index-check build"
 from tests import test_trunk_gpu as t
 for dtype in (torch.float32, torch.bfloat16):
     for E, T, D in t.SCAN_SIZES:
-        for kw in (dict(), dict(time_major=True, fused=True), dict(shift=True, lengths=[T, 0, T // 2, 1])):
+        for kw in (dict(time_major=True, fused=True), dict(shift=True, lengths=[T, 0, T // 2, 1])):
             t.check_scan(E, T, D, dtype, seed=T, **kw)
     for N, D in t.RMS_SIZES:
         for kw in (dict(), dict(strided=True), dict(shift=True, residual=False)):

@@ -139,7 +139,7 @@ def check_scan(E, T, D, dtype, backward=True, tol=1e-6, **kw):
 # that do not; rows that share the SMs and one row alone
 SCAN_SIZES = [(1, 1, 1), (3, 1, 130), (1, 2, 64), (2, 7, 33), (5, 16, 128), (2, 63, 100), (1, 64, 256), (3, 65, 65),
               (2, 127, 72), (1, 129, 8), (4, 255, 40), (1, 300, 514), (2, 513, 96), (70, 33, 192), (1, 2049, 64),
-              (1, 5000, 130), (9, 1000, 24), (1, 4200, 40), (2, 9001, 64)]
+              (1, 5000, 130), (9, 1000, 24), (1, 2300, 40), (2, 2999, 64)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -160,7 +160,7 @@ def test_gated_scan_layouts(dtype, time_major, fused, shift):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("time_major", [False, True])
 def test_gated_scan_lengths(dtype, time_major):
-    for E, T, D in ((6, 300, 72), (5, 1, 64), (7, 64, 129), (3, 2000, 64)):
+    for E, T, D in ((6, 300, 72), (5, 1, 64), (7, 64, 129), (3, 2000, 64), (6, 2500, 40), (40, 12, 64)):
         check_scan(E, T, D, dtype, seed=T, time_major=time_major, lengths=[T, 0, 1, T // 2 + 1, max(T - 1, 0), 64])
         check_scan(E, T, D, dtype, seed=T, time_major=time_major, lengths=[0], state=False)
 
@@ -179,6 +179,61 @@ def test_gated_scan_long_memory(dtype):
     to 1.5 u, 0.9 u on average, add up to 0.9 sqrt(T) u, and what does not cancel like that is a bias."""
     check_scan(1, 6000, 128, dtype, seed=1, ends=0.0, bias=10.0, tol=2 * U * 6000 ** 0.5)
     check_scan(3, 3000, 64, dtype, seed=2, ends=0.0005, bias=10.0, time_major=True, tol=2 * U * 3000 ** 0.5)
+
+
+@pytest.mark.parametrize("E,T,D", [(3, 1, 64), (3, 5, 61), (2, 200, 64), (1, 900, 64), (1, 9001, 64), (2, 7000, 61)])
+def test_gated_scan_states_in_place(E, T, D):
+    """last in the state's buffer and d_state in d_last's give what buffers of their own give, however a row is shared out."""
+    d = steps_problem(E, T, D, torch.bfloat16, seed=T, ends=0.0005)
+    dh, d_last = d.pop("dh"), d.pop("d_last")
+    h, last = rlca.rlca_gated_scan(**d)
+    args = (dh, d["x"], d["gate"], h, d["terminated"], d["truncated"], d["state"])
+    grads = rlca.rlca_gated_scan_backward(*args, d_last=d_last)
+    for _ in range(5):
+        own = d["state"].clone()
+        h1, last1 = rlca.rlca_gated_scan(**dict(d, state=own), last=own)
+        assert last1 is own and torch.equal(last1, last) and torch.equal(h1, h)
+        own = d_last.clone()
+        g1 = rlca.rlca_gated_scan_backward(*args, d_last=own, d_state=own)
+        assert g1[2] is own and all(torch.equal(a, b) for a, b in zip(g1, grads))
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^31 elements: their ends against the same rows by themselves."""
+    D, T = 2048, (1 << 20) + 333
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    both = torch.empty(1, T, 2 * D, dtype=torch.bfloat16, device="cuda")
+    both.normal_(generator=gen)
+    x, gate = both[..., :D], both[..., D:]
+    ends = torch.zeros(1, T, dtype=torch.uint8, device="cuda")
+    cut = T - 500
+    ends[0, cut - 1] = 1
+    h, last = rlca.rlca_gated_scan(x, gate, ends)
+    assert h.numel() > 1 << 31
+    h_end, last_end = rlca.rlca_gated_scan(x[:, cut:], gate[:, cut:])
+    assert (h[:, cut:].float() - h_end.float()).norm() <= 1e-3 * h_end.float().norm()
+    assert (last - last_end).norm() <= 1e-5 * last_end.norm()
+    grads = torch.empty_like(both)
+    dl = torch.randn(1, D, device="cuda")
+    rlca.rlca_gated_scan_backward(h, x, gate, h, ends, d_last=dl, dx=grads[..., :D], dgate=grads[..., D:])
+    dx, dgate, _ = rlca.rlca_gated_scan_backward(h[:, cut:], x[:, cut:], gate[:, cut:], h[:, cut:], d_last=dl)
+    assert (grads[:, cut:, :D].float() - dx.float()).norm() <= 1e-3 * dx.float().norm()
+    assert (grads[:, cut:, D:].float() - dgate.float()).norm() <= 1e-3 * dgate.float().norm()
+    del grads, dx, dgate, h, both
+    N = (1 << 20) + 333
+    rows = torch.empty(N, D, dtype=torch.bfloat16, device="cuda")
+    rows.normal_(generator=gen)
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    y, total, rstd, y8, t8 = rlca.rlca_rms_norm(rows, w, rows.clone(), want_y8=True, want_total8=True)
+    y1, total1, rstd1, y81, t81 = rlca.rlca_rms_norm(rows[-300:], w, rows[-300:].clone(), want_y8=True, want_total8=True)
+    for a, b in ((y, y1), (total, total1), (rstd, rstd1), (y8[0].view(torch.uint8), y81[0].view(torch.uint8)), (y8[1], y81[1]),
+                 (t8[0].view(torch.uint8), t81[0].view(torch.uint8)), (t8[1], t81[1])):
+        assert torch.equal(a[-300:], b)
+    for kept, kept1 in ((total, total1), (t8, t81)):
+        dx, _ = rlca.rlca_rms_norm_backward(y, kept, w, rstd, d_total=rows)
+        dx1, _ = rlca.rlca_rms_norm_backward(y1, kept1, w, rstd1, d_total=rows[-300:])
+        assert torch.equal(dx[-300:], dx1)
 
 
 def test_gated_scan_cut_in_calls():
@@ -242,7 +297,7 @@ def test_gated_scan_extreme_gates():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("E,T,D", [(2, 700, 64), (1, 900, 96), (2, 9001, 64), (4, 7, 64)])
+@pytest.mark.parametrize("E,T,D", [(2, 700, 64), (1, 900, 96), (2, 2999, 64), (4, 7, 64)])
 def test_gated_scan_closed_gates_beside_open_ones(E, T, D, dtype):
     """Channels whose gates are shut so far that products of them vanish, next to channels that remember, with ends of
     episodes between: what marks an end in one channel's product says nothing in another's."""
