@@ -435,9 +435,9 @@ __device__ __forceinline__ void tile_load(void* to, const CUtensorMap* map, int 
 
 // Where the rows of every array start on 16-byte boundaries (kBulk), a tile of
 // an array is one tensor copy, and a lane's channels are next to each other.
-// Other rows are copied one by one, from the boundary in front of them to the
-// one behind -- 16 bytes that hold any byte of the row are readable as a whole.
-// Their pitch in shared memory is the matrix's modulo 16 bytes, so that a row's
+// Other rows are copied in 16-byte vectors, from the boundary in front of them
+// on -- 16 bytes that hold any byte of the row are readable as a whole.  (A bulk
+// copy a row has to be issued thread by thread, some 12 instructions each.)  Their pitch in shared memory is the matrix's modulo 16 bytes, so that a row's
 // first column stays as far behind a boundary as it is in memory and a column
 // lies at one pitch in all of them.  A lane's channels are 32 apart there.
 template <class ST, bool kBulk, int L>
@@ -450,35 +450,52 @@ struct TileRows {
   __device__ static uint32_t pitch(int64_t step) { return kBulk ? kRow : kLeast + (((uint32_t)step - kLeast) & 15); }
 };
 
-// A thread's share of copying tiles row by row: one row of one array, at the
-// same place behind its boundary in every tile.
-template <class ST, int L>
+// Copies the tiles of one array by vectors: a thread one vector of some rows,
+// each at the same place behind its boundary in every tile.
+template <class ST, int L, int THREADS>
 struct RowCopy {
   using R = TileRows<ST, false, L>;
-  uintptr_t at = 0;   // the row in the next tile, from the boundary in front of it
-  int64_t move = 0;   // bytes and steps from tile to tile
-  int step = 0, t = -1;
-  uint32_t to = 0, size = 0;
-  // row r of array k, step t of the matrix in the first tile copied; `tile` is that tile's first
-  __device__ void start(const GatedArgs& a, int k, int r, const float* p, int64_t stride, int64_t e, int64_t c0, int tile, int tiles) {
-    const uint32_t width = (uint32_t)min((int64_t)kCols, a.D - c0) * R::kBytes;
-    const uintptr_t first = (uintptr_t)p + ((e * a.step_e + tile * a.step_t) * stride + c0) * R::kBytes;
-    const int64_t bytes = a.step_t * stride * R::kBytes;
-    at = first + r * bytes;
-    size = ((uint32_t)(at & 15) + width + 15) & ~15u;
-    to = (k * R::kTile + (uint32_t)(first & 15) + r * R::pitch(bytes)) & ~15u;
-    at &= ~(uintptr_t)15;
-    t = tile + r, step = tiles * L, move = step * bytes;
-    if (!span_in_range(to, size, (k + 1) * R::kTile)) size = 0;
+  static constexpr int V = R::kRow / 16 + 1;                    // vectors that a row can touch
+  static constexpr int kRows = THREADS / V, kTurns = (L + kRows - 1) / kRows;  // rows at a time
+  uintptr_t at = 0;  // this thread's first vector in the next tile, shift included
+  int64_t bytes = 0;
+  uint32_t to = 0, pitch = 0;
+  int row = L, past = 0;  // its first row; what the shift has to exceed for the vector to hold a column
+  uintptr_t lo = 0, hi = 0;
+  // array k; `first`: the first tile's first step
+  __device__ void start(const GatedArgs& a, int k, const float* p, int64_t stride, int64_t e, int64_t c0, int first) {
+    const int v = threadIdx.x % V;
+    row = threadIdx.x / V < kRows ? threadIdx.x / V : L;
+    bytes = a.step_t * stride * R::kBytes;
+    pitch = R::pitch(bytes);
+    at = (uintptr_t)p + ((e * a.step_e + first * a.step_t) * stride + c0) * R::kBytes;
+    to = k * R::kTile + (uint32_t)(at & 15) + row * pitch + 16 * v;
+    at += row * bytes + 16 * v;
+    past = 16 * v - (int)min((int64_t)kCols, a.D - c0) * R::kBytes;
+    if constexpr (kIndexCheck) lo = (uintptr_t)p, hi = lo + (uintptr_t)(a.E * a.T * stride) * R::kBytes;
   }
-  __device__ __forceinline__ void next(unsigned char* stage, int len, uint64_t* bar) {
-    const uint32_t bytes = t >= 0 && t < len ? size : 0;
-    mbar_arrive_expect_tx(bar, bytes);
-    if (bytes != 0) bulk_load(stage + to, reinterpret_cast<const void*>(at), bytes, bar);
-    t += step;
-    at += move;
+  // the tile of steps t .. t + L - 1, of which those in [0, len) are there; `move`: steps to the next one copied
+  __device__ __forceinline__ void next(uint32_t stage, int t, int len, int move) {
+    uintptr_t from = at;
+    uint32_t dst = stage + to;
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+      const int r = row + q * kRows;
+      if (r < L && t + r >= 0 && t + r < len && (int)(from & 15) > past) {
+        const uintptr_t vec = from & ~(uintptr_t)15;
+        if (!kIndexCheck || in_range((int64_t)(max(vec, lo) - lo), (int64_t)(hi - lo)))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst & ~15u), "l"(vec) : "memory");
+      }
+      from += kRows * bytes;
+      dst += kRows * pitch;
+    }
+    at += move * bytes;
   }
 };
+// an arrival on `bar` when this thread's copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // A lane's two channels of the warp's steps of a tile.  Tiles are whole multiples of 16 bytes in steps of any matrix, so a
 // step lies at the same place in all of them.
@@ -669,12 +686,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs 
   const int64_t stride = kBack ? a.dh_stride : a.x_stride;
   // in the order of the steps, or the last tile first
   const int first = kBack ? begin + (ntiles - 1) * L : begin, turn = kBack ? -L : L;
-  RowCopy<ST, L> copy;
+  RowCopy<ST, L, 32 * W> copy[kArrays];
   if constexpr (!kBulk) {
-    static_assert(kArrays * L <= 32 * W, "a row a thread");
-    const int k = threadIdx.x / L;
-    if (ntiles > 0 && k < kArrays)
-      copy.start(a, k, threadIdx.x % L, k == 0 ? p : a.gate, k == 0 ? stride : a.gate_stride, e, cols.c0, first, kBack ? -1 : 1);
+    copy[0].start(a, 0, p, stride, e, cols.c0, first);
+    copy[1].start(a, 1, a.gate, a.gate_stride, e, cols.c0, first);
   }
   const auto fill = [&](int stage, int j) {
     if (!in_range(stage, STAGES)) return;
@@ -685,7 +700,9 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs 
       tile_load(to, &maps.in[kBack ? 2 : 0], (int)cols.c0, first + j * turn, (int)e, &sh.full[stage]);
       tile_load(to + R::kTile, &maps.in[1], (int)cols.c0, first + j * turn, (int)e, &sh.full[stage]);
     } else {
-      copy.next(to, len, &sh.full[stage]);
+#pragma unroll
+      for (int i = 0; i < kArrays; ++i) copy[i].next(smem_u32(to), first + j * turn, len, turn);
+      copies_arrive(&sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < ntiles; ++j) fill(j, j);
@@ -737,8 +754,9 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs 
     if (part == 0) leave_map(a, unit, a.nseg, {kSevered, outer_value<kBack>(cols, a, e, len)});
   }
   // (copies still on their way after a wait gave up land before the CTA ends)
-  if (!ring.ok && (threadIdx.x == 0 || !kBulk))
+  if (kBulk && !ring.ok && threadIdx.x == 0)
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
+  if constexpr (!kBulk) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <class ST, int C, int W, int STAGES, bool kBulk, bool kShared, int kResident>
@@ -767,13 +785,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
   const int len = row_length(a, e), lim = min(len, stop);
   const int ntiles = (max(lim - begin, 0) + L - 1) / L, rounds = (ntiles + share - 1) / share;
   const int mine = ntiles > rank ? (ntiles - rank + share - 1) / share : 0;
-  RowCopy<ST, L> copy;
+  RowCopy<ST, L, 32 * W> copy[kArrays];
   if constexpr (!kBulk) {
-    static_assert(kArrays * L <= 32 * W, "a row a thread");
-    const int k = threadIdx.x / L;
-    if (k < kArrays)
-      copy.start(a, k, threadIdx.x % L, k == 0 ? a.x : a.gate, k == 0 ? a.x_stride : a.gate_stride, e, cols.c0,
-                 begin + rank * L, share);
+    copy[0].start(a, 0, a.x, a.x_stride, e, cols.c0, begin + rank * L);
+    copy[1].start(a, 1, a.gate, a.gate_stride, e, cols.c0, begin + rank * L);
   }
   const auto fill = [&](int stage, int j) {
     if (!in_range(stage, STAGES)) return;
@@ -785,7 +800,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
       tile_load(to, &maps.in[0], (int)cols.c0, t, (int)e, &sh.full[stage]);
       tile_load(to + R::kTile, &maps.in[1], (int)cols.c0, t, (int)e, &sh.full[stage]);
     } else {
-      copy.next(to, len, &sh.full[stage]);
+      const int t = begin + (rank + j * share) * L;
+#pragma unroll
+      for (int i = 0; i < kArrays; ++i) copy[i].next(smem_u32(to), t, len, share * L);
+      copies_arrive(&sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
@@ -863,8 +881,9 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
     cols.store_state(a.last, e, a.E, carry);
   }
   // (copies still on their way after a wait gave up land before the CTA ends)
-  if (!ring.ok && (threadIdx.x == 0 || !kBulk))
+  if (kBulk && !ring.ok && threadIdx.x == 0)
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
+  if constexpr (!kBulk) asm volatile("cp.async.wait_all;" ::: "memory");
   if constexpr (kShared) cluster_meet();  // no CTA ends while a peer may still write to it
 }
 
@@ -896,14 +915,12 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
   const int mine = ntiles > rank ? (ntiles - rank + share - 1) / share : 0;
   // the row's last tile first
   const int last_tile = begin + (rank + (mine - 1) * share) * L;
-  RowCopy<ST, L> copy;
+  RowCopy<ST, L, 32 * W> copy[kArrays];
   if constexpr (!kBulk) {
-    static_assert(kArrays * L <= 32 * W, "a row a thread");
-    const int k = threadIdx.x / L;
-    const float* const p = k == 0 ? a.x : k == 1 ? a.gate : k == 2 ? a.dh : a.in_h;
-    const int64_t stride = k == 0 ? a.x_stride : k == 1 ? a.gate_stride : k == 2 ? a.dh_stride : a.h_stride;
-    if (mine > 0 && k < kArrays)
-      copy.start(a, k, threadIdx.x % L, p, stride, e, cols.c0, k == 3 ? last_tile - 1 : last_tile, -share);
+    copy[0].start(a, 0, a.x, a.x_stride, e, cols.c0, last_tile);
+    copy[1].start(a, 1, a.gate, a.gate_stride, e, cols.c0, last_tile);
+    copy[2].start(a, 2, a.dh, a.dh_stride, e, cols.c0, last_tile);
+    copy[3].start(a, 3, a.in_h, a.h_stride, e, cols.c0, last_tile - 1);
   }
   const auto fill = [&](int stage, int j) {
     if (!in_range(stage, STAGES)) return;
@@ -916,7 +933,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
       for (int i = 0; i < kArrays; ++i)
         tile_load(to + i * R::kTile, &maps.in[i], (int)cols.c0, i == 3 ? t - 1 : t, (int)e, &sh.full[stage]);
     } else {
-      copy.next(to, len, &sh.full[stage]);
+      const int t = last_tile - j * share * L;
+#pragma unroll
+      for (int i = 0; i < kArrays; ++i) copy[i].next(smem_u32(to), i == 3 ? t - 1 : t, len, -share * L);
+      copies_arrive(&sh.full[stage]);
     }
   };
   for (int j = 0; j < STAGES - 1 && j < mine; ++j) fill(j, j);
@@ -1016,8 +1036,9 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
     to_x.move(-share * L), to_gate.move(-share * L);
   }
   if (warp == 0 && part == 0 && a.d_state != nullptr) cols.store_state(a.d_state, e, a.E, carry);
-  if (!ring.ok && (threadIdx.x == 0 || !kBulk))
+  if (kBulk && !ring.ok && threadIdx.x == 0)
     for (int i = 0; i < STAGES; ++i) mbar_wait_bounded(&sh.full[i], ring.last_fill(i));
+  if constexpr (!kBulk) asm volatile("cp.async.wait_all;" ::: "memory");
   if constexpr (kShared) cluster_meet();
 }
 
