@@ -701,14 +701,16 @@ cudaError_t launch_rms(const RmsArgs& a, int sm, cudaStream_t s) {
   return launch_pdl(rms_kernel<ST, kAligned, VPT, TPR>, std::min<int64_t>(div_up(a.N, T / TPR), (int64_t)R * sm), T, 0, s, a);
 }
 
-// Threads a row, and parts of one a thread (32768 x 4096 bfloat16 with both
-// 8-bit outputs: 256 threads x 2 parts 162 us, 128 x 4 175 us, 512 x 1 174 us);
+// Threads a row, and parts of one a thread (bfloat16 with both 8-bit outputs:
+// 32768 x 4096 with 256 threads x 2 parts 162 us, 128 x 4 175 us, 512 x 1 174 us;
+// 60000 x 1000 with 128 x 1 79 us, 32 x 4 89 us; 131072 x 512 with 64 x 1 84 us,
+// 32 x 2 89 us; unaligned 300000 x 201 with 64 x 1 171 us, 32 x 2 164 us);
 // `parts`: of a row
 template <class ST, bool kAligned>
 cudaError_t rms_width(const RmsArgs& a, int64_t parts, int sm, cudaStream_t s) {
   if (parts <= 32) return launch_rms<ST, kAligned, 1, 32>(a, sm, s);
-  if (parts <= 64) return launch_rms<ST, kAligned, 2, 32>(a, sm, s);
-  if (parts <= 128) return launch_rms<ST, kAligned, 4, 32>(a, sm, s);
+  if (parts <= 64) return kAligned ? launch_rms<ST, kAligned, 1, 64>(a, sm, s) : launch_rms<ST, kAligned, 2, 32>(a, sm, s);
+  if (parts <= 128) return launch_rms<ST, kAligned, 1, 128>(a, sm, s);
   if (parts <= 256) return launch_rms<ST, kAligned, 2, 128>(a, sm, s);
   if (parts <= 512) return launch_rms<ST, kAligned, 2, 256>(a, sm, s);
   if (parts <= 1024) return launch_rms<ST, kAligned, 2, 512>(a, sm, s);
@@ -756,7 +758,9 @@ cudaError_t launch_grad_ring(const RmsGradArgs& a, int sm, cudaStream_t s) {
 }
 
 // Rows that start on 16-byte boundaries (`parts` vectors each) or not (32
-// parts a group); from 65 vectors on the former take the ring.
+// parts a group); from 65 vectors on the former take the ring, if rows in 8 bits
+// are whole multiples of 16 bytes too (20000 x 4088 bfloat16 without: 104 us; as
+// unaligned rows 150 us).
 template <class ST, bool k8>
 cudaError_t grad_width(const RmsGradArgs& a, bool even, bool ring, int64_t parts, int sm, cudaStream_t s, bool* taken) {
   *taken = true;
@@ -767,12 +771,17 @@ cudaError_t grad_width(const RmsGradArgs& a, bool even, bool ring, int64_t parts
     if (ring && parts <= 256) return launch_grad_ring<ST, k8, 2, 128, 4>(a, sm, s);
     if (ring && parts <= 512) return launch_grad_ring<ST, k8, 2, 256, 4>(a, sm, s);
     if (ring && parts <= 1024) return launch_grad_ring<ST, k8, 2, 512, 4>(a, sm, s);
+    if (!ring && parts <= 128) return launch_grad<ST, true, k8, 1, 128>(a, sm, s);
+    if (!ring && parts <= 256) return launch_grad<ST, true, k8, 2, 128>(a, sm, s);
+    if (!ring && parts <= 512) return launch_grad<ST, true, k8, 2, 256>(a, sm, s);
+    if (!ring && parts <= 1024) return launch_grad<ST, true, k8, 2, 512>(a, sm, s);
     if constexpr (Stor<ST>::kBytes == 4)
       if (ring && parts <= 2048) return launch_grad_ring<ST, k8, 4, 512, 2>(a, sm, s);
   }
   parts = groups_of(a.D) * 32;
   if (parts <= 32) return launch_grad<ST, false, k8, 1, 32>(a, sm, s);
   if (parts <= 64) return launch_grad<ST, false, k8, 2, 32>(a, sm, s);
+  if (parts <= 128) return launch_grad<ST, false, k8, 1, 128>(a, sm, s);
   if (parts <= 256) return launch_grad<ST, false, k8, 2, 128>(a, sm, s);
   if (parts <= 512) return launch_grad<ST, false, k8, 2, 256>(a, sm, s);
   if (parts <= 1024) return launch_grad<ST, false, k8, 2, 512>(a, sm, s);
