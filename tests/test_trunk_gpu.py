@@ -294,6 +294,11 @@ def test_gated_scan_extreme_gates():
                     (-200.0, x)):
         h, _ = rlca.rlca_gated_scan(x, torch.full_like(x, g), state=state)
         assert torch.equal(h, want), g
+        # (bfloat16: a shut gate counts as one of up to 2 u)
+        xb = x.bfloat16()
+        h, _ = rlca.rlca_gated_scan(xb, torch.full_like(xb, g), state=state)
+        want = want.double() if g > 0 else xb.double()
+        _close(h, want, half_step(torch.bfloat16) * want.abs() + 4 * U * state.abs().amax(), f"gates of {g}")
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
