@@ -1110,20 +1110,25 @@ struct TileShape<float, true, false> : Shape<8, 4, 2, 2> {};
 
 // CTAs of a row: as many as fit the SMs beside each other in clusters of up to
 // 8; where those would leave two thirds of them idle, segments of at least two
-// tiles, which read the inputs twice.  (bfloat16, one row of 65536 steps, us
-// clusters / segments: 256 channels 183 / 43, 1024 238 / 136, the gradient 208 /
-// 67 and 261 / 259; 4096 channels 285 / 572.  4096 steps of 1024 channels 18.9 /
-// 15.1, the gradient 20.1 / 23.5; 2048 steps of 256 channels 7.1 / 10.6.)
+// tiles, which read the inputs twice.  The gradient, whose first launch needs two
+// of its four inputs, is cut where half would idle if its rows are long, and
+// then finely enough that its first launch fills the SMs too.  (bfloat16, one
+// row of 65536 steps, us clusters / segments: 256 channels 183 / 43, 1024 238 /
+// 136, the gradient 208 / 67 and 261 / 195 -- 259 with as many segments as fit
+// the SMs --; 4096 channels 285 / 572.  4096 steps of 1024 channels 18.9 / 15.5,
+// the gradient 20.1 / 22.6; 2048 steps of 256 channels 7.1 / 10.6.)
 constexpr int kSegStep = 64;  // whole tiles of every shape
 struct Split {
   int share = 1, nseg = 1, seg_len = 0;
 };
-Split split_rows(int64_t E, int64_t T, int64_t D, int64_t slots) {
-  const int64_t units = E * div_up(D, kCols), tiles = div_up(T, kSegStep);
+Split split_rows(int64_t E, int64_t T, int64_t D, int64_t slots, bool back) {
+  const int64_t units = E * div_up(D, kCols), tiles = div_up(T, kSegStep), most = units * kMaxShare;
   Split r;
   r.seg_len = (int)T;
-  if (3 * units * kMaxShare <= slots && tiles > 4 * kMaxShare) {
-    const int64_t segs = std::min(slots / units, tiles / 2);
+  if ((3 * most <= slots && tiles > 4 * kMaxShare) || (back && 2 * most <= slots && tiles >= 16 * kMaxShare)) {
+    int64_t segs = slots / units;
+    if (back && tiles >= 8 * segs) segs *= 2;
+    segs = std::min(segs, tiles / 2);
     r.seg_len = (int)(div_up(tiles, segs) * kSegStep);
     r.nseg = (int)div_up(T, r.seg_len);
     return r;
@@ -1133,7 +1138,7 @@ Split split_rows(int64_t E, int64_t T, int64_t D, int64_t slots) {
 }
 template <class ST, bool kBack>
 Split split_rows(int64_t E, int64_t T, int64_t D, int sm) {
-  return split_rows(E, T, D, (int64_t)TileShape<ST, kBack, true>::RES * sm);
+  return split_rows(E, T, D, (int64_t)TileShape<ST, kBack, true>::RES * sm, kBack);
 }
 
 template <class ST, bool kBack, bool kBulk, bool kShared, bool kMaps>
