@@ -444,7 +444,8 @@ __device__ __forceinline__ void tile_load(void* to, const CUtensorMap* map, int 
 // an array is one tensor copy, and a lane's channels are next to each other.
 // Other rows are copied in 16-byte vectors, from the boundary in front of them
 // on -- 16 bytes that hold any byte of the row are readable as a whole.  (A bulk
-// copy a row has to be issued thread by thread, some 12 instructions each.)  Their pitch in shared memory is the matrix's modulo 16 bytes, so that a row's
+// copy a row has to be issued thread by thread, some 12 instructions each.)
+// Their pitch in shared memory is the matrix's modulo 16 bytes, so that a row's
 // first column stays as far behind a boundary as it is in memory and a column
 // lies at one pitch in all of them.  A lane's channels are 32 apart there.
 template <class ST, bool kBulk, int L>
@@ -621,7 +622,7 @@ __device__ __forceinline__ V2 meet(GatedShared<W, STAGES, kShared>& sh, int roun
     for (int k = 1; k < W; ++k) all = chain(sh.warp_map[buf][kForward ? k : W - 1 - k][lane], all);
     for (int r = 0; r < share; ++r) send(&sh.cta_map[buf][rank][lane], &sh.maps[buf], r, all);
   }
-  if (*ok) *ok = mbar_wait_bounded(&sh.maps[buf], (round >> 1) & 1);
+  if (*ok) *ok = mbar_wait_bounded<true>(&sh.maps[buf], (round >> 1) & 1);
   for (int k = 0; k < share; ++k) {
     const int r = kForward ? k : share - 1 - k;
     if (r == rank) at = *carry;
