@@ -25,6 +25,8 @@ for dtype in (torch.float32, torch.bfloat16):
     for E, T, D in t.SCAN_SIZES:
         for kw in (dict(time_major=True, fused=True), dict(shift=True, lengths=[T, 0, T // 2, 1])):
             t.check_scan(E, T, D, dtype, seed=T, **kw)
+    for E, T, D in ((3000, 12, 64), (2500, 11, 61)):
+        t.check_scan(E, T, D, dtype, seed=T, lengths=[T, 0, 3])
     for N, D in t.RMS_SIZES:
         for kw in (dict(), dict(strided=True), dict(shift=True, residual=False)):
             t.check_rms(N, D, dtype, seed=N, **kw)

@@ -166,6 +166,26 @@ def test_gated_scan_lengths(dtype, time_major):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("time_major", [False, True])
+def test_gated_scan_many_short_rows(dtype, time_major):
+    """Far more rows than the SMs hold, of a few dozen steps at most: walked step by step, in vectors and not."""
+    for E, T, D in ((3000, 12, 64), (9000, 33, 40), (2500, 11, 61)):
+        check_scan(E, T, D, dtype, seed=E, time_major=time_major, lengths=[T, 0, 1, T - 1, 5, 8])
+        check_scan(E, T, D, dtype, seed=E + 1, time_major=time_major, ends=0.0, fused=True)
+
+
+def test_gated_scan_lengths_out_of_range_and_bool_flags():
+    d = steps_problem(4, 90, 64, torch.float32, seed=4)
+    for k in ("dh", "d_last"):
+        d.pop(k)
+    wild = torch.tensor([-5, 1000, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    tame = torch.tensor([0, 90, 90, 0], dtype=torch.int32, device="cuda")
+    a = rlca.rlca_gated_scan(**dict(d, lengths=wild))
+    b = rlca.rlca_gated_scan(**dict(d, lengths=tame, terminated=d["terminated"].bool(), truncated=d["truncated"].bool()))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("ends", [0.0, 0.002, 0.5, 1.0])
 def test_gated_scan_boundaries(dtype, ends):
     check_scan(4, 700, 64, dtype, seed=3, ends=ends)
