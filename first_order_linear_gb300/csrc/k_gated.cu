@@ -1089,7 +1089,8 @@ bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_lis
 // deeper rings: forward bfloat16 (256 x 512 x 1024 time-major) {16, 4, 2, 4} 141
 // us, {16, 4, 3, 3} 155, {16, 8, 3, 2} 155, {8, 8, 3, 3} 164; the gradient, whose
 // 16 steps keep 128 values a thread, {16, 4, 3, 2} (one row of 65536 x 2048) 268 us,
-// {8, 8, 3, 2} 308, {8, 4, 2, 4} 485.
+// {8, 8, 3, 2} 308, {8, 4, 2, 4} 485.  Unaligned rows have room for fewer tiles: the
+// gradient, float32 (37 x 515 x 1001 time-major) {4, 8, 2, 2} 73 us, {8, 4, 2, 2} 76.
 template <int kChunk, int kWarps, int kStages, int kRes>
 struct Shape {
   static constexpr int C = kChunk, W = kWarps, STAGES = kStages, RES = kRes;
@@ -1107,7 +1108,7 @@ struct TileShape<bf16, true, false> : Shape<8, 4, 2, 4> {};
 template <>
 struct TileShape<float, true, true> : Shape<8, 4, 3, 2> {};
 template <>
-struct TileShape<float, true, false> : Shape<8, 4, 2, 2> {};
+struct TileShape<float, true, false> : Shape<4, 8, 2, 2> {};
 
 // CTAs of a row: as many as fit the SMs beside each other in clusters of up to
 // 8; where those would leave two thirds of them idle, segments of at least two
