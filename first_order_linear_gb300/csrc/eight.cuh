@@ -16,7 +16,12 @@ constexpr float kE4m3Max = 448.f;
 
 __host__ __device__ constexpr int64_t groups_of(int64_t D) { return (D + kGroup - 1) / kGroup; }
 
-// (a group of zeros gets the smallest normal scale, whose reciprocal is finite)
+// Products with reciprocals: quotients rounded as divisions round them would
+// only move values that lie on a border of two steps already, and the norm's
+// issue slots are its next bound behind HBM (65536 x 4096 bfloat16 with two
+// 8-bit outputs: 318 us; with divisions 513 us, with a paired remainder step in
+// their place 340 us; unaligned 300000 x 201 163, 276 and 193 us).
+// (A group of zeros gets the smallest normal scale, whose reciprocal is finite.)
 __device__ __forceinline__ float group_scale(float amax) { return fmaxf(amax * (1.f / kE4m3Max), 1.17549435e-38f); }
 
 // two values, the first at the lower address; saturating, NaN kept

@@ -567,8 +567,11 @@ int rlca_clip_grads(const void *const *grads, void *const *outs,
  * Rows in 8 bits: a row of D values is D e4m3 values q (1 byte each: sign, 4
  * exponent and 3 mantissa bits, largest 448) and one float32 scale for each
  * group of RLCA_GROUP consecutive columns (the last group may be narrower):
- *   scale = max(max |v| / 448, 2^-126),   q = v / scale to the nearest e4m3
- * A value is read back as q * scale.  NaN stays NaN (and does not count in the
+ *   scale = max(max |v| * (1 / 448), 2^-126)
+ *   q     = v * (1 / scale), to the nearest e4m3, ties to the even one
+ * with 1 / 448, 1 / scale and the products rounded to float32: a value whose
+ * ratio to the scale lies within 2^-22 of a border between two e4m3 may go to
+ * either side of it.  A value is read back as q * scale.  NaN stays NaN (and does not count in the
  * group's maximum); a group that holds an infinity reads back as NaN.  Both
  * arrays are dense: q [N,D], scale [N, ceil(D / RLCA_GROUP)].
  */
