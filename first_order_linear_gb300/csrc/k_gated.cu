@@ -406,6 +406,31 @@ __device__ __forceinline__ Map2 chain(const Map2& then, const Map2& first) {
   if (severed(then)) return then;
   return {severed(first) ? first.p : mul2(then.p, first.p), fma2(then.p, first.q, then.q)};
 }
+// one step, of gates s and input b, behind `first`
+__device__ __forceinline__ Map2 step(V2 s, V2 b, const Map2& first) {
+  return {severed(first) ? first.p : mul2(s, first.p), fma2(s, first.q, b)};
+}
+
+// Products of gates are above 0 however far below float32's least they lie, and
+// an infinity stays one through any of them; the rounded product, 0, would make
+// it NaN.  So the maps that threads hand each other keep products of 2^-126 at
+// least (which moves no finite value by more than that of it), and a thread's own
+// products are left out (`meeting`) where the value in front is not finite.
+__device__ __forceinline__ Map2 lasting(const Map2& m) {
+  const float2 p = apart(m.p);
+  constexpr float kLeast = 1.17549435e-38f;
+  return {severed(m) ? m.p : v2(fmaxf(p.x, kLeast), fmaxf(p.y, kLeast)), m.q};
+}
+constexpr float kLargest = 3.402823466e38f;
+__device__ __forceinline__ bool finite(V2 v) {
+  const float2 f = apart(v);
+  return fabsf(f.x) <= kLargest && fabsf(f.y) <= kLargest;
+}
+__device__ __forceinline__ V2 meeting(V2 p, V2 h) {
+  if ((uint32_t)p == (uint32_t)kSevered) return p;
+  const float2 f = apart(h), r = apart(p);
+  return v2(fabsf(f.x) <= kLargest ? r.x : 1.f, fabsf(f.y) <= kLargest ? r.y : 1.f);
+}
 
 // carry through the maps of W warps, in order of the steps or against it; at:
 // what it is in front of this warp's
@@ -537,6 +562,12 @@ struct Cols {
   int64_t D;
   __device__ int64_t ch(int k) const { return kPairs ? c0 + 2 * lane + k : c0 + lane + 32 * k; }
   __device__ bool on(int k) const { return ch(k) < D; }
+  // v, without what channels that are none hold (their columns of a tile are not copied, or 0 by tensor copies)
+  __device__ V2 there(V2 v) const {
+    if constexpr (kPairs) return v;
+    const float2 f = apart(v);
+    return v2(on(0) ? f.x : 0.f, on(1) ? f.y : 0.f);
+  }
   // the two channels' states in float32 [E, D]
   __device__ V2 state(const float* p, int64_t e, int64_t E) const {
     float v[2];
@@ -625,6 +656,7 @@ __device__ __forceinline__ V2 meet(GatedShared<W, STAGES, kShared>& sh, int roun
     Map2 all = sh.warp_map[buf][kForward ? 0 : W - 1][lane];
 #pragma unroll
     for (int k = 1; k < W; ++k) all = chain(sh.warp_map[buf][kForward ? k : W - 1 - k][lane], all);
+    all = lasting(all);
     for (int r = 0; r < share; ++r) send(&sh.cta_map[buf][rank][lane], &sh.maps[buf], r, all);
   }
   if (*ok) *ok = mbar_wait_bounded<true>(&sh.maps[buf], (round >> 1) & 1);
@@ -752,10 +784,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs 
         else m = {severed(m) ? m.p : mul2(m.p, s), mul2(s, add2(v, m.q))};
       } else {
         if (here) m = {kSevered, mul2(ns, v)};
-        else m = chain({s, mul2(ns, v)}, m);
+        else m = step(s, mul2(ns, v), m);
       }
     }
-    sh.warp_map[j & 1][warp][lane] = m;
+    sh.warp_map[j & 1][warp][lane] = lasting(m);
     __syncthreads();
     if (warp == 0) {
 #pragma unroll
@@ -763,7 +795,7 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_map_kernel(GatedArgs 
     }
   }
   if (warp == 0) {
-    leave_map(a, unit, part, all);
+    leave_map(a, unit, part, lasting(all));
     if (part == 0) leave_map(a, unit, a.nseg, {kSevered, outer_value<kBack>(cols, a, e, len)});
   }
   // (copies still on their way after a wait gave up land before the CTA ends)
@@ -862,21 +894,25 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_tile_kernel(GatedArgs
             gs.get(tile, i).sigma(&s, &ns);
             const V2 b = mul2(ns, xs.get(tile, i).wide());
             if ((cut >> i) & 1) m = {kSevered, b};
-            else m = chain({s, b}, m);
+            else m = step(s, b, m);
           }
           q[i] = m.q;
           p[i] = m.p;
         }
       }
     }
-    sh.warp_map[k & 1][warp][lane] = m;
+    sh.warp_map[k & 1][warp][lane] = lasting(m);
     const bool any_cut = __syncthreads_or(cut != 0);
-    const V2 h = meet<W, STAGES, kShared, true>(sh, k, rank, share, any_cut, &met, &carry);
+    const V2 h = cols.there(meet<W, STAGES, kShared, true>(sh, k, rank, share, any_cut, &met, &carry));
     out.start();
-    if (k < mine && real == C && cut == 0) {
+    if (k < mine && real == C && cut == 0 && finite(h)) {
 #pragma unroll
       for (int i = 0; i < C; ++i) out.put(fma2(p[i], h, q[i]));
     } else {
+      if (!finite(h)) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) p[i] = meeting(p[i], h);
+      }
 #pragma unroll
       for (int i = 0; i < C; ++i)
         if (t0 + i < stop) out.put(k < mine && i < real ? pass({p[i], q[i]}, h) : 0);
@@ -1025,11 +1061,11 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
         }
       }
     }
-    sh.warp_map[(rounds - 1 - k) & 1][warp][lane] = m;
+    sh.warp_map[(rounds - 1 - k) & 1][warp][lane] = lasting(m);
     const bool any_cut = __syncthreads_or(cut != 0);
-    const V2 u = meet<W, STAGES, kShared, false>(sh, rounds - 1 - k, rank, share, any_cut, &met, &carry);
+    const V2 u = cols.there(meet<W, STAGES, kShared, false>(sh, rounds - 1 - k, rank, share, any_cut, &met, &carry));
     to_x.start(), to_gate.start();
-    if (k < mine && real == C && cut == 0) {
+    if (k < mine && real == C && cut == 0 && finite(u)) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const V2 G = fma2(p[i], u, g[i]);
@@ -1037,6 +1073,10 @@ __global__ void __launch_bounds__(32 * W, kResident) gated_grad_tile_kernel(Gate
         to_gate.put(mul2(w[i], G));
       }
     } else {
+      if (!finite(u)) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) p[i] = meeting(p[i], u);
+      }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         if (t0 + i >= stop) continue;

@@ -646,7 +646,9 @@ int rlca_rms_norm_backward(const float *dy, const float *d_total,
  * token of E sequences at a time; last may then (and always) be the state's
  * own buffer.  a_t and 1 - a_t are formed in float32, each relatively exact to
  * 2^-20 (bfloat16 gates g: to (4 + 1.2 |g|) 2^-23) however small it is, down to
- * 2^-125; bfloat16 gates below -86 count as -86.
+ * 2^-125; bfloat16 gates below -86 count as -86.  A state or an x that is not
+ * finite reaches every later h of its channel up to an episode's end: an
+ * infinity stays one wherever a_t is not 0 in float32.
  *   x, gate                [E,T,D] x ([T,E,D] with RLCA_TIME_MAJOR), rows of D
  *                          at row strides x_stride and gate_stride, required
  *   terminated, truncated  [E,T] ([T,E]) u8, NULL = none
