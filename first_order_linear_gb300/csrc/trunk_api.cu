@@ -126,7 +126,7 @@ int rlca_rms_norm_backward(const float* dy, const float* d_total, const float* t
   const Rows q{total8, N, D, D, 1}, sc{total8_scale, N, groups, groups, 4}, rw = flat(weight, D, es), rs = flat(rstd, N, 4);
   const Rows ws = flat(workspace, (int64_t)workspace_bytes, 1), rdx{dx, N, D, D, es}, rdw = flat(dweight, D, es);
   if ((N > 0 && !rows_ok({rdy, rdt, rt, sc, rw, rs, rdx})) || !rdw.ok()) return RLCA_ERR_INVALID_ARG;
-  if (rows_clash({rdy, rdt, rt, q, sc, rw, rs, ws}, {rdx, rdw})) return RLCA_ERR_INVALID_ARG;
+  if (rows_clash({rdy, rdt, rt, q, sc, rw, rs}, {rdx, rdw, ws})) return RLCA_ERR_INVALID_ARG;
   int sm = 0;
   if (sm_count_of_current_device(&sm) != cudaSuccess) return RLCA_ERR_CUDA;
   if (!workspace_ok(workspace, workspace_bytes, N == 0 ? 0 : rms_norm_backward_workspace(N, D, sm))) return RLCA_ERR_INVALID_ARG;
@@ -154,7 +154,8 @@ int rlca_gated_scan(const float* x, const float* gate, const uint8_t* terminated
   const Rows s0 = flat(state, E * D, 4), s1 = flat(last, E * D, 4);
   if ((n > 0 && !rows_ok({rx, rg, rh})) || !rows_ok({len, s0, s1})) return RLCA_ERR_INVALID_ARG;
   const Rows ws = flat(workspace, (int64_t)workspace_bytes, 1);
-  if (rows_clash({rx, rg, t1, t2, len, ws}, {rh, s1}) || rows_overlap(rh, s0) || (last != state && rows_overlap(s1, s0)))
+  if (rows_clash({rx, rg, t1, t2, len}, {rh, s1, ws}) || rows_overlap(rh, s0) || rows_overlap(ws, s0) ||
+      (last != state && rows_overlap(s1, s0)))
     return RLCA_ERR_INVALID_ARG;
   int sm = 0;
   if (sm_count_of_current_device(&sm) != cudaSuccess) return RLCA_ERR_CUDA;
@@ -188,8 +189,8 @@ int rlca_gated_scan_backward(const float* dh, const float* x, const float* gate,
   const Rows s0 = flat(state, E * D, 4), dl = flat(d_last, E * D, 4), ds = flat(d_state, E * D, 4);
   if ((n > 0 && !rows_ok({rdh, rx, rg, rh, rdx, rdg})) || !rows_ok({len, s0, dl, ds})) return RLCA_ERR_INVALID_ARG;
   const Rows ws = flat(workspace, (int64_t)workspace_bytes, 1);
-  if (rows_clash({rdh, rx, rg, rh, t1, t2, len, s0, ws}, {rdx, rdg, ds}) || rows_overlap(rdx, dl) || rows_overlap(rdg, dl) ||
-      (d_state != d_last && rows_overlap(ds, dl)))
+  if (rows_clash({rdh, rx, rg, rh, t1, t2, len, s0}, {rdx, rdg, ds, ws}) || rows_overlap(rdx, dl) || rows_overlap(rdg, dl) ||
+      rows_overlap(ws, dl) || (d_state != d_last && rows_overlap(ds, dl)))
     return RLCA_ERR_INVALID_ARG;
   int sm = 0;
   if (sm_count_of_current_device(&sm) != cudaSuccess) return RLCA_ERR_CUDA;

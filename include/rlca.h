@@ -50,7 +50,9 @@
  *    bytes (16-byte aligned).  A NULL workspace is valid when the size is 0.
  *    The workspace is scratch: its contents on entry are ignored and on exit
  *    are unspecified; calls that share one workspace must not overlap on the
- *    GPU.
+ *    GPU.  It shares no memory with the arrays of its call: one that overlaps
+ *    an output is refused everywhere, one that overlaps an input by the calls
+ *    of a recurrent policy's trunk.
  *  - E == 0 or T == 0 returns RLCA_OK and enqueues nothing.
  *  - Errors: RLCA_ERR_INVALID_ARG (NULL required pointer, negative or
  *    oversized E/T, overlapping outputs, workspace too small or misaligned,
