@@ -709,7 +709,10 @@ cudaError_t launch_rms(const RmsArgs& a, int sm, cudaStream_t s) {
 template <class ST, bool kAligned>
 cudaError_t rms_width(const RmsArgs& a, int64_t parts, int sm, cudaStream_t s) {
   if (parts <= 32) return launch_rms<ST, kAligned, 1, 32>(a, sm, s);
-  if (parts <= 64) return kAligned ? launch_rms<ST, kAligned, 1, 64>(a, sm, s) : launch_rms<ST, kAligned, 2, 32>(a, sm, s);
+  if (parts <= 64) {
+    if constexpr (kAligned) return launch_rms<ST, kAligned, 1, 64>(a, sm, s);
+    else return launch_rms<ST, kAligned, 2, 32>(a, sm, s);
+  }
   if (parts <= 128) return launch_rms<ST, kAligned, 1, 128>(a, sm, s);
   if (parts <= 256) return launch_rms<ST, kAligned, 2, 128>(a, sm, s);
   if (parts <= 512) return launch_rms<ST, kAligned, 2, 256>(a, sm, s);
@@ -771,10 +774,12 @@ cudaError_t grad_width(const RmsGradArgs& a, bool even, bool ring, int64_t parts
     if (ring && parts <= 256) return launch_grad_ring<ST, k8, 2, 128, 4>(a, sm, s);
     if (ring && parts <= 512) return launch_grad_ring<ST, k8, 2, 256, 4>(a, sm, s);
     if (ring && parts <= 1024) return launch_grad_ring<ST, k8, 2, 512, 4>(a, sm, s);
-    if (!ring && parts <= 128) return launch_grad<ST, true, k8, 1, 128>(a, sm, s);
-    if (!ring && parts <= 256) return launch_grad<ST, true, k8, 2, 128>(a, sm, s);
-    if (!ring && parts <= 512) return launch_grad<ST, true, k8, 2, 256>(a, sm, s);
-    if (!ring && parts <= 1024) return launch_grad<ST, true, k8, 2, 512>(a, sm, s);
+    if constexpr (k8) {  // (without rows in 8 bits every aligned row takes the ring)
+      if (!ring && parts <= 128) return launch_grad<ST, true, k8, 1, 128>(a, sm, s);
+      if (!ring && parts <= 256) return launch_grad<ST, true, k8, 2, 128>(a, sm, s);
+      if (!ring && parts <= 512) return launch_grad<ST, true, k8, 2, 256>(a, sm, s);
+      if (!ring && parts <= 1024) return launch_grad<ST, true, k8, 2, 512>(a, sm, s);
+    }
     if constexpr (Stor<ST>::kBytes == 4)
       if (ring && parts <= 2048) return launch_grad_ring<ST, k8, 4, 512, 2>(a, sm, s);
   }
