@@ -1135,7 +1135,10 @@ bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_lis
 // us, {16, 4, 3, 3} 155, {16, 8, 3, 2} 155, {8, 8, 3, 3} 164; the gradient, whose
 // 16 steps keep 128 values a thread, {16, 4, 3, 2} (one row of 65536 x 2048) 268 us,
 // {8, 8, 3, 2} 308, {8, 4, 2, 4} 485.  Unaligned rows have room for fewer tiles: the
-// gradient, float32 (37 x 515 x 1001 time-major) {4, 8, 2, 2} 73 us, {8, 4, 2, 2} 76.
+// gradient, float32, {4, 8, 2, 2} / {8, 4, 2, 2}: 37 x 515 x 1001 time-major with
+// lengths 73 / 76 us, without 80 / 81, 256 x 512 x 201 156 / 159, 64 x 256 x 333
+// 41.7 / 42.3, 8 x 4000 x 2049 282 / 281; a few rows in clusters rather the other
+// way, 1 x 20000 x 1001 144 / 139, 3 x 900 x 501 14.2 / 13.4.
 template <int kChunk, int kWarps, int kStages, int kRes>
 struct Shape {
   static constexpr int C = kChunk, W = kWarps, STAGES = kStages, RES = kRes;
@@ -1164,6 +1167,11 @@ struct TileShape<float, true, false> : Shape<4, 8, 2, 2> {};
 // 136, the gradient 208 / 67 and 261 / 195 -- 259 with as many segments as fit
 // the SMs --; 4096 channels 285 / 572.  4096 steps of 1024 channels 18.9 / 15.5,
 // the gradient 20.1 / 22.6; 2048 steps of 256 channels 7.1 / 10.6.)
+//
+// The CTAs an SM are those of the aligned shape for every alignment: the size of
+// the workspace follows from this, and is asked for before there are addresses.
+// (Two shapes of unaligned rows hold another number: the bfloat16 gradient's
+// twice as many, the float32 one's as many of twice the warps.)
 constexpr int kSegStep = 64;  // whole tiles of every shape
 struct Split {
   int share = 1, nseg = 1, seg_len = 0;

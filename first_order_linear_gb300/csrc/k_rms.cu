@@ -289,7 +289,10 @@ __global__ void __launch_bounds__(cta_threads(TPR), rms_resident(cta_threads(TPR
 
 // ---------------------------------------------------------------------------
 // A CTA a row, two passes over it: a warp takes a group of columns at a time,
-// a lane four of them, 32 apart.
+// a lane four of them, 32 apart.  Rows wider than registers hold, bound by their
+// single elements: 5000 x 12288 float32 with a residual 262 us, 0.55 of the copy
+// rate; 10000 x 20000 bfloat16 836 us, 0.28.  The gradients further down, three passes with
+// dw's: 10000 x 12288 bfloat16 463 us, 0.31; 5000 x 20000 from 8 bits 467 us, 0.22.
 // ---------------------------------------------------------------------------
 constexpr int kLongThreads = 512;
 constexpr int kPart = kGroup / 32;
@@ -358,7 +361,10 @@ __global__ void __launch_bounds__(kLongThreads) rms_long_kernel(RmsArgs a) {
 // Gradient: rows in registers as above, the next one loaded ahead; each CTA
 // leaves the sums of dw over its rows in ws[CTA][D], which a second kernel
 // joins in order.  (131072 x 512 bfloat16: 87 us, 0.91 of the copy rate;
-// unaligned rows, 20000 x 2001 bfloat16: 73 us, 0.57, bound by instructions.)
+// unaligned rows, 20000 x 2001 bfloat16: 73 us, 0.57, bound by instructions; rows
+// of 4097 to 8192 unaligned columns, whose 16 values, their products and sums a
+// thread do not fit 128 registers (56 to 84 bytes spilled), 10000 x 7001 bfloat16
+// 202 us, 0.36, 5000 x 7001 float32 95 us, 0.71.)
 // ---------------------------------------------------------------------------
 // CTAs an SM is to hold: 512 threads with up to 16 values (5001 x 1001 float32: 768
 // threads 22.3 us, 512 15.9 us)
