@@ -57,4 +57,9 @@ inline bool aligned(const void* p, uintptr_t a) { return p == nullptr || ((uintp
 
 inline bool flags_ok(uint32_t flags, uint32_t allowed) { return (flags & ~allowed) == 0u; }
 
+// a workspace of `have` bytes where `need` are asked for
+inline bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws != nullptr && have >= need && aligned(ws, 16));
+}
+
 }  // namespace rlca

@@ -1120,15 +1120,6 @@ cudaError_t launch_tiles(void (*kernel)(GatedArgs, GatedMaps, int), int64_t grid
   return cudaLaunchKernelEx(&cfg, kernel, a, maps, share);
 }
 
-// rows of every matrix on 16-byte boundaries: tensor copies can take them
-bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides, int es, int to) {
-  for (const void* p : bases)
-    if (((uintptr_t)p % to) != 0) return false;
-  for (int64_t r : strides)
-    if ((r * es) % to != 0) return false;
-  return true;
-}
-
 // The shape of a tile kernel: C steps a thread, W warps, STAGES tiles in the
 // ring, RES CTAs an SM.  More CTAs cover a tile's chain of waits better than
 // deeper rings: forward bfloat16 (256 x 512 x 1024 time-major) {16, 4, 2, 4} 141

@@ -570,14 +570,6 @@ __global__ void __launch_bounds__(1024)
 // 4 vectors (forward; 2 backward, whose sums take the registers) or 8 single
 // elements a thread.
 // ---------------------------------------------------------------------------
-bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides, int es) {
-  for (const void* p : bases)
-    if (((uintptr_t)p & 15) != 0) return false;
-  for (int64_t s : strides)
-    if ((s * es) % 16 != 0) return false;
-  return true;
-}
-
 template <class ST, int VE, int VPT, int TPR>
 cudaError_t launch_norm(const NormArgs& a, int sm, cudaStream_t s) {
   constexpr int T = cta_threads(TPR), R = norm_resident(T, VPT * VE);

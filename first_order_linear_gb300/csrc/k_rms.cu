@@ -691,14 +691,6 @@ int64_t slice_rows(int64_t N, int64_t D, int sm) {
   return std::max<int64_t>(1, div_up(N, want));
 }
 
-// whether all rows start on 16-byte boundaries
-bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides, int es) {
-  for (const void* p : bases)
-    if (((uintptr_t)p & 15) != 0) return false;
-  for (int64_t s : strides)
-    if ((s * es) % 16 != 0) return false;
-  return true;
-}
 bool aligned_to(const void* p, int to) { return ((uintptr_t)p % to) == 0; }
 
 template <class ST, bool kAligned, int VPT, int TPR>

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cuda.h>  // CUtensorMap
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 namespace rlca {
 
@@ -43,6 +44,15 @@ cudaError_t allow_smem(K* kernel, size_t bytes, std::atomic<uint64_t>& done) {
 }
 
 constexpr int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// whether all rows of es-byte elements, of every base and stride, start on `to`-byte boundaries
+inline bool rows_aligned(std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides, int es, int to = 16) {
+  for (const void* p : bases)
+    if (((uintptr_t)p % to) != 0) return false;
+  for (int64_t r : strides)
+    if ((r * es) % to != 0) return false;
+  return true;
+}
 
 // ---- layer norm (k_norm.cu) ------------------------------------------------
 struct NormArgs {

@@ -13,22 +13,12 @@ namespace rlca {
 
 namespace {
 
-// largest row count, width and vocabulary: products of any two, times the
-// element size and a tile's rounding, stay well inside 63 bits
-constexpr int64_t kMaxRows = INT32_MAX;
-constexpr int64_t kMaxWidth = int64_t(1) << 30;
-
-size_t ebytes(uint32_t flags) { return (flags & RLCA_BF16) ? 2 : 4; }
-
 // bytes from the first to the last element of n rows of `width` elements
 size_t matrix_bytes(int64_t n, int64_t width, int64_t stride, size_t elem) {
   return n == 0 ? 0 : ((size_t)(n - 1) * (size_t)stride + (size_t)width) * elem;
 }
 
-bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride <= (int64_t(1) << 31); }
-
-// status of a finished sequence of launches
-int launched(cudaError_t e, cudaStream_t s) { return e == cudaSuccess ? checked_build_status(s) : RLCA_ERR_CUDA; }
+bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride <= kMaxStride; }
 
 // head sizes: RLCA_OK, or the status to return
 int head_sizes(int64_t N, int64_t D, int64_t V) {
@@ -38,10 +28,6 @@ int head_sizes(int64_t N, int64_t D, int64_t V) {
 }
 
 bool temperature_ok(float inv) { return inv > 0.f && std::isfinite(inv); }
-
-bool workspace_ok(const void* ws, size_t have, size_t need) {
-  return need == 0 || (ws != nullptr && have >= need && aligned(ws, 16));
-}
 
 }  // namespace
 

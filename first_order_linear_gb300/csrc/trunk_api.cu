@@ -5,6 +5,7 @@
 
 #include "host_checks.h"
 #include "policy.h"
+#include "policy_checks.h"
 #include "rlca.h"
 #include "trunk.h"
 
@@ -12,10 +13,7 @@ namespace rlca {
 
 namespace {
 
-constexpr int64_t kMaxRows = INT32_MAX;
-constexpr int64_t kMaxWidth = int64_t(1) << 30;
 constexpr int64_t kMaxSteps = int64_t(1) << 30;
-constexpr int64_t kMaxStride = int64_t(1) << 31;
 
 bool sizes_ok(int64_t n, int64_t width) { return n >= 0 && width >= 0 && n <= kMaxRows && width <= kMaxWidth; }
 
@@ -56,14 +54,6 @@ bool rows_ok(std::initializer_list<Rows> all) {
 }
 
 Rows flat(const void* p, int64_t n, size_t elem) { return {p, 1, n, n > 0 ? n : 1, elem}; }
-
-int launched(cudaError_t e, cudaStream_t s) { return e == cudaSuccess ? checked_build_status(s) : RLCA_ERR_CUDA; }
-
-bool workspace_ok(const void* ws, size_t have, size_t need) {
-  return need == 0 || (ws != nullptr && have >= need && aligned(ws, 16));
-}
-
-size_t ebytes(uint32_t flags) { return (flags & RLCA_BF16) ? 2 : 4; }
 
 // sizes and flags of a gated scan: RLCA_OK with *empty where nothing is to be done, or the status to return
 int gated_sizes(int64_t E, int64_t T, int64_t D, uint32_t flags, bool* empty) {
