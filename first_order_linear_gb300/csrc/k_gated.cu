@@ -6,10 +6,10 @@
 // with k_t = 0 where step t-1 is flagged.  The state and all arithmetic are
 // float32.  A step reads two elements a channel and writes one, its gradient
 // reads four and writes two: both are bound by HBM where the rows are many or
-// long and aligned -- bfloat16, 256 x 512 x 1024: 123 us, 0.97 of the measured
-// copy rate; 16 x 4096 x 2048 128 us, 0.93; one row of 65536 x 4096 in clusters
-// 285 us, 0.83; the gradient, 32 x 4096 x 2048: 518 us, 6.2 TB/s, 0.92; float32
-// 16 x 1024 x 2048 0.89 and 0.95.
+// long and aligned -- bfloat16, 256 x 512 x 1024: 125 us, 0.95 of the measured
+// copy rate; 16 x 4096 x 2048 131 us, 0.90; one row of 65536 x 4096 in clusters
+// 299 us, 0.79; the gradient, 32 x 4096 x 2048: 528 us, 6.1 TB/s, 0.90; float32
+// 16 x 1024 x 2048 0.88 and 0.94.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -41,13 +41,12 @@ struct Sigma {
 // bfloat16 gates: 1 - sigma from one exponential and one reciprocal at either
 // sign; sigma is that reciprocal itself below 0, where it keeps its digits
 // however small it is (the gradient of a shut gate is proportional to it), and
-// the difference to 1 above, unbiased.  The selection costs 1 to 3% (one row of
-// 65536 x 4096: 294 us, 286 with the difference alone, which leaves of a gate of
-// -10 three digits and of -17 none; one Newton step of the reciprocal instead
-// 300 us).  The short exponential's error, (2 + 1.2 |g|) 2^-23 of the value, is
-// far below the gate's own rounding.  (The exponent is bounded so that the
-// product stays a number: a gate below -86 counts as one of -86, which lets
-// 2^-125 through.)
+// the difference to 1 above, unbiased.  The difference alone would leave of a
+// gate of -10 three digits, of -17 none; the selection costs 1 to 3% (8 of 299 us
+// on one row of 65536 x 4096; one Newton step of the reciprocal instead 14 us).
+// The short exponential's error, (2 + 1.2 |g|) 2^-23 of the value, is far below
+// the gate's own rounding.  (The exponent is bounded so that the product stays a
+// number: a gate below -86 counts as one of -86, which lets 2^-125 through.)
 template <>
 struct Sigma<bf16> {
   __device__ __forceinline__ static Gate of(float g) {
@@ -307,9 +306,9 @@ __global__ void __launch_bounds__(kStepThreads) gated_grad_step_kernel(GatedArgs
 // a warp, a lane two channels, whose arithmetic is paired.  A thread scans its
 // steps from 0 and keeps, for each, the value and the product of gates that
 // the state before them still meets; the warps' maps (product, value) meet in
-// shared memory, and one multiply-add a step brings the state in.  That is 17
-// instructions an element forward and 26 backward; where HBM does not bound it,
-// a tile's chain of waits does (45% of the issue slots, 4 CTAs an SM: copies in
+// shared memory, and one multiply-add a step brings the state in.  That is 19
+// instructions an element forward and 28 backward; where HBM does not bound it,
+// a tile's chain of waits does (50% of the issue slots, 4 CTAs an SM: copies in
 // flight, the barrier, the fold).  Behind a flagged step nothing of the state before it arrives, whatever it holds: flags
 // are the same for all channels, so that is a matter of branches and not of
 // products with 0.
@@ -415,7 +414,8 @@ __device__ __forceinline__ Map2 step(V2 s, V2 b, const Map2& first) {
 // an infinity stays one through any of them; the rounded product, 0, would make
 // it NaN.  So the maps that threads hand each other keep products of 2^-126 at
 // least (which moves no finite value by more than that of it), and a thread's own
-// products are left out (`meeting`) where the value in front is not finite.
+// products are left out (`meeting`) where the value in front is not finite.  (One
+// row of 65536 x 4096 5 us of 299; passing every map with regard to it 45 us.)
 __device__ __forceinline__ Map2 lasting(const Map2& m) {
   const float2 p = apart(m.p);
   constexpr float kLeast = 1.17549435e-38f;
@@ -1154,10 +1154,14 @@ struct TileShape<float, true, false> : Shape<4, 8, 2, 2> {};
 // tiles, which read the inputs twice.  The gradient, whose first launch needs two
 // of its four inputs, is cut where half would idle if its rows are long, and
 // then finely enough that its first launch fills the SMs too.  (bfloat16, one
-// row of 65536 steps, us clusters / segments: 256 channels 183 / 43, 1024 238 /
-// 136, the gradient 208 / 67 and 261 / 195 -- 259 with as many segments as fit
-// the SMs --; 4096 channels 285 / 572.  4096 steps of 1024 channels 18.9 / 15.5,
-// the gradient 20.1 / 22.6; 2048 steps of 256 channels 7.1 / 10.6.)
+// row of 65536 steps, us clusters / segments: 256 channels 182 / 41, 1024 246 /
+// 125, 1536 234 / 191, 2048 277 / 251 -- on the wrong side of the rule --, 4096
+// 299 / 527; the gradient of 64 205 / 37, of 256 206 / 69, of 1024 261 / 201.
+// 4096 steps of 1024 channels 19.9 / 14.9, the gradient 20.4 / 24.9; 2048 steps of
+// 256 channels 7.2 / 10.5.)  A segment's CTA walks the maps in front of it, eight
+// loads in flight, all its warps the same ones: with hundreds of segments that
+// takes longer than the rest (64 channels, 512 segments: 24 of 38 us; 256: 7 of
+// 41; 1024: 1 of 125; the gradient of 256, 16 of 69).
 //
 // The CTAs an SM are those of the aligned shape for every alignment: the size of
 // the workspace follows from this, and is asked for before there are addresses.
